@@ -20,12 +20,15 @@ P_VOID = ctypes.POINTER(c_void_p)
 
 DFLASH_F32, DFLASH_BF16 = 0, 1
 DERR_BITS = {0x1: "KV_CAPACITY", 0x2: "PAGE_RANGE", 0x4: "TOKEN_RANGE", 0x8: "POSITION",
-             0x10: "OUTPUT_ROW", 0x20: "TIMEOUT", 0x40: "ROW_RANGE"}
+             0x10: "OUTPUT_ROW", 0x20: "TIMEOUT", 0x40: "ROW_RANGE", 0x80: "SAMPLING",
+             0x100: "EMPTY_ROW"}
 EXPORTED = ["dflash_create", "dflash_destroy", "dflash_workspace_size", "dflash_bind_workspace",
             "dflash_inject_context", "dflash_draft_block", "dflash_accept_commit",
             "dflash_accept_commit_sampled",
             "dflash_selector_workspace_size", "dflash_set_selector", "dflash_draft_block_selector",
             "dflash_accept_commit_sampled_q",
+            "dflash_rope_init", "dflash_append_kv", "dflash_paged_attention_workspace_size",
+            "dflash_paged_attention", "dflash_target_probs", "dflash_sample_tokens",
             "dflash_get_error", "dflash_status_string", "dflash_last_error",
             "dflash_profile_enable", "dflash_profile_disable", "dflash_profile_collect"]
 
@@ -57,6 +60,23 @@ class DflashKV(ctypes.Structure):
 class DflashSelector(ctypes.Structure):
     _fields_ = [("K", c_int32), ("rank", c_int32), ("W_h", c_void_p), ("A", c_void_p),
                 ("B", c_void_p)]
+
+
+class DflashLayerKV(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("n_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("k_pages", c_void_p), ("v_pages", c_void_p),
+                ("n_pages", c_int32), ("page_table", c_void_p), ("pages_per_req", c_int32),
+                ("prefix_pages", c_void_p), ("prefix_len", c_int32)]
+
+
+class DflashRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", c_int32), ("interleaved", c_int32), ("amplitude", c_float),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+class DflashSampling(ctypes.Structure):
+    _fields_ = [("temperature", c_void_p), ("top_k", c_void_p), ("top_p", c_void_p),
+                ("min_p", c_void_p), ("rows_per_entry", c_int32)]
 
 
 class DflashProfileEntry(ctypes.Structure):
@@ -103,6 +123,23 @@ def load_library(path=LIB_PATH):
                                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                                    c_int32, c_void_p]
+    c_int64, c_double = ctypes.c_int64, ctypes.c_double
+    lib.dflash_rope_init.argtypes = [c_int32, c_int32, c_double, ctypes.c_int, c_double, c_double,
+                                     c_double, c_double, ctypes.POINTER(DflashRope)]
+    lib.dflash_append_kv.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_int32,
+                                     c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                     c_void_p, c_int64, c_void_p, c_void_p, c_float,
+                                     ctypes.POINTER(DflashRope), c_void_p, c_int64, c_void_p]
+    lib.dflash_paged_attention_workspace_size.argtypes = [ctypes.POINTER(DflashLayerKV), c_int32,
+                                                          c_int32, ctypes.POINTER(c_size_t)]
+    lib.dflash_paged_attention.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_int32,
+                                           c_void_p, c_void_p, c_void_p, c_int64, c_float, c_int32,
+                                           c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.dflash_target_probs.argtypes = [c_void_p, c_int32, c_int32, c_void_p, ctypes.c_int, c_int64,
+                                        ctypes.POINTER(DflashSampling), c_void_p, c_void_p]
+    lib.dflash_sample_tokens.argtypes = [c_void_p, c_int32, c_int32, c_void_p, ctypes.c_int,
+                                         c_int64, ctypes.POINTER(DflashSampling), c_void_p,
+                                         c_void_p, c_void_p, c_void_p]
     lib.dflash_get_error.argtypes = [c_void_p, c_void_p, ctypes.POINTER(ctypes.c_uint32)]
     lib.dflash_profile_enable.argtypes = [c_void_p, c_int32]
     lib.dflash_profile_disable.argtypes = [c_void_p]
@@ -117,7 +154,9 @@ def load_library(path=LIB_PATH):
                  "dflash_accept_commit_sampled", "dflash_selector_workspace_size",
                  "dflash_set_selector", "dflash_draft_block_selector",
                  "dflash_accept_commit_sampled_q", "dflash_get_error", "dflash_profile_enable", "dflash_profile_disable",
-                 "dflash_profile_collect"]:
+                 "dflash_profile_collect", "dflash_rope_init", "dflash_append_kv",
+                 "dflash_paged_attention_workspace_size", "dflash_paged_attention",
+                 "dflash_target_probs", "dflash_sample_tokens"]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -220,6 +259,49 @@ def dflash_accept_commit_sampled_q(h, batch, draft_ids, probs, K, cand_ids, q_ro
         _p(output_ids), out_stride, stream))
 
 
+def dflash_rope_init(rotary_dim, interleaved, theta, scaling, factor, original_positions, low, high):
+    r = DflashRope()
+    _check(load_library().dflash_rope_init(rotary_dim, interleaved, theta, scaling, factor,
+                                           original_positions, low, high, ctypes.byref(r)))
+    return r
+
+
+def dflash_append_kv(h, kv: DflashLayerKV, batch, total_rows, row_start, kv_len, q, q_stride, k,
+                     k_stride, v, v_stride, q_gain, k_gain, eps, rope: DflashRope, q_out,
+                     q_out_stride, stream):
+    _check(load_library().dflash_append_kv(h, kv, batch, total_rows, _p(row_start), _p(kv_len),
+                                           _p(q), q_stride, _p(k), k_stride, _p(v), v_stride,
+                                           _p(q_gain), _p(k_gain), eps, rope, _p(q_out),
+                                           q_out_stride, stream))
+
+
+def dflash_paged_attention_workspace_size(kv: DflashLayerKV, batch, total_rows):
+    n = c_size_t()
+    _check(load_library().dflash_paged_attention_workspace_size(kv, batch, total_rows,
+                                                                ctypes.byref(n)))
+    return n.value
+
+
+def dflash_paged_attention(h, kv: DflashLayerKV, batch, total_rows, row_start, kv_len, q, q_stride,
+                           scale, causal, out, out_stride, workspace, nbytes, stream):
+    _check(load_library().dflash_paged_attention(h, kv, batch, total_rows, _p(row_start),
+                                                 _p(kv_len), _p(q), q_stride, scale, causal,
+                                                 _p(out), out_stride, _p(workspace), nbytes,
+                                                 stream))
+
+
+def dflash_target_probs(h, rows, vocab, logits, dtype, row_stride, params: DflashSampling, probs,
+                        stream):
+    _check(load_library().dflash_target_probs(h, rows, vocab, _p(logits), dtype, row_stride, params,
+                                              _p(probs), stream))
+
+
+def dflash_sample_tokens(h, rows, vocab, logits, dtype, row_stride, params: DflashSampling,
+                         exp_noise, ids, prob, stream):
+    _check(load_library().dflash_sample_tokens(h, rows, vocab, _p(logits), dtype, row_stride,
+                                               params, _p(exp_noise), _p(ids), _p(prob), stream))
+
+
 def dflash_get_error(h, stream):
     """Returns the device error word (0 = clean) after synchronising the stream."""
     w = ctypes.c_uint32()
@@ -250,3 +332,4 @@ def decode_error(word):
 
 
 from .session import DraftSession  # noqa: E402,F401
+from .target import LayerKV, rope_plan  # noqa: E402,F401

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "target_ops.h"
 
 namespace dflash {
 
@@ -153,6 +154,8 @@ cudaError_t prepare_kernels() {
   if (e == cudaSuccess) e = prepare_attention_mma();
   if (e == cudaSuccess) e = prepare_attention_tc();
   if (e == cudaSuccess) e = prepare_selector();
+  if (e == cudaSuccess) e = prepare_sampling();
+  if (e == cudaSuccess) e = prepare_paged_attention_simt();
   return e;
 }
 

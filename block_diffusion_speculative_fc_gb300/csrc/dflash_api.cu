@@ -9,6 +9,7 @@
 #include "../../include/dflash.h"
 #include "../../include/dflash_testing.h"
 #include "kernels.h"
+#include "target_ops.h"
 
 using namespace dflash;
 
@@ -45,6 +46,7 @@ struct dflash_handle {
   Layout L;
   char *ws = nullptr;
   size_t ws_bytes = 0;
+  int device = -1;   // device that was current when the workspace was bound
   int store;      // ST_F32 / ST_BF16
   bool fuse = true;   // dependent bf16 GEMMs as one cooperative launch
   bool attn_tc = true;  // tcgen05 attention where it applies (else the mma.sync kernel)
@@ -303,6 +305,28 @@ int handle_lm_head(const dflash_handle *h, const void **lm_head, int *hidden, in
   return DFLASH_OK;
 }
 void set_last_error(const char *msg) { g_last_error = msg; }
+
+int handle_ready(const dflash_handle *h, unsigned int **err) {
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (!h->ws) return fail(DFLASH_ESTATE, "no workspace bound");
+  int dev = -1;
+  if (int st = check_cuda(cudaGetDevice(&dev), "cudaGetDevice")) return st;
+  if (dev != h->device)
+    return fail(DFLASH_EINVAL, "the handle's workspace was bound on another device");
+  *err = (unsigned int *)(h->ws + h->L.err);
+  return DFLASH_OK;
+}
+int handle_timed_begin(dflash_handle *h, const char *name, cudaStream_t s) {
+  if (!h->prof_on || h->recs.size() >= h->prof_cap) return -1;
+  const int idx = (int)h->recs.size();
+  h->recs.push_back({name, h->ev[2 * idx], h->ev[2 * idx + 1]});
+  cudaEventRecord(h->ev[2 * idx], s);
+  return idx;
+}
+int handle_timed_end(dflash_handle *h, int idx, const char *name, cudaStream_t s, cudaError_t e) {
+  if (idx >= 0) cudaEventRecord(h->ev[2 * idx + 1], s);
+  return check_cuda(e, name);
+}
 }  // namespace dflash
 
 extern "C" {
@@ -457,6 +481,7 @@ int dflash_bind_workspace(dflash_handle *h, void *dev_ptr, size_t bytes, dflash_
   cudaStream_t s = (cudaStream_t)stream;
   h->ws = (char *)dev_ptr;
   h->ws_bytes = bytes;
+  if (cudaGetDevice(&h->device) != cudaSuccess) h->device = -1;
   int st = check_cuda(cudaMemsetAsync(h->ws + h->L.err, 0, 256, s), "clear error word");
   if (st) return st;
   if (h->L.tc_max_tiles > 0 &&

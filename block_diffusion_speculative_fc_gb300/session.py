@@ -14,8 +14,10 @@ from . import (DFLASH_BF16, DFLASH_F32, DflashConfig, DflashKV, DflashWeights, _
                dflash_accept_commit_sampled, dflash_draft_block, dflash_get_error,
                dflash_inject_context, dflash_workspace_size, DflashSelector,
                dflash_selector_workspace_size, dflash_set_selector, dflash_draft_block_selector,
-               dflash_accept_commit_sampled_q,
-               _check, load_library)
+               dflash_accept_commit_sampled_q, dflash_append_kv, dflash_paged_attention,
+               dflash_paged_attention_workspace_size, dflash_target_probs, dflash_sample_tokens,
+               DflashSampling, _check, load_library)
+from .target import check, dtype_code, rows_of
 
 
 def _stream():
@@ -171,6 +173,97 @@ class DraftSession:
         batch = kv.batch if batch is None else batch
         dflash_draft_block_selector(self.h, kv.struct, batch, anchor, exp_noise, draft_ids,
                                     cand_ids, q_rows, _stream())
+
+    # ---- the target's side of a cycle (include/dflash.h)
+    def _ragged(self, layer, row_start, kv_len):
+        batch = kv_len.shape[0]
+        if batch > layer.batch:
+            raise ValueError(f"kv_len: at most the page table's {layer.batch} requests")
+        check(row_start, "row_start", torch.int32, layer.device, (batch + 1,))
+        check(kv_len, "kv_len", torch.int32, layer.device, (batch,))
+        return batch
+
+    def append_kv(self, layer, q, k, v, row_start, kv_len, rope, q_gain=None, k_gain=None,
+                  eps=1e-6, q_out=None):
+        """Head norms, rotary positions, append to layer's pages: q [rows, H, D]
+        (or None), k, v [rows, KVH, D], rows of any stride; q_out like q."""
+        batch = self._ragged(layer, row_start, kv_len)
+        dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, k.shape[0]
+        ks = rows_of(k, "k", layer.n_kv_heads, D, dt, dev)
+        vs = rows_of(v, "v", layer.n_kv_heads, D, dt, dev, rows)
+        qs = qos = 0
+        if q is not None:
+            qs = rows_of(q, "q", layer.n_heads, D, dt, dev, rows)
+            if q_out is None:
+                raise ValueError("q_out: where the rotated queries go is needed")
+            qos = rows_of(q_out, "q_out", layer.n_heads, D, dt, dev, rows)
+        for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+            if g is not None:
+                check(g, name, dt, dev, (D,))
+        dflash_append_kv(self.h, layer.struct, batch, rows, row_start, kv_len, q, qs, k, ks, v, vs,
+                         q_gain, k_gain, eps, rope, q_out, qos, _stream())
+
+    def attention_workspace(self, layer, batch, total_rows):
+        """Device workspace for paged_attention calls of at most this size."""
+        n = dflash_paged_attention_workspace_size(layer.struct, batch, total_rows)
+        return torch.empty(n, dtype=torch.uint8, device=layer.device)
+
+    def paged_attention(self, layer, q, row_start, kv_len, out, workspace, scale=None, causal=True):
+        """Attention of q [rows, H, D] over layer's cache (kv_len rows before
+        the new ones, the new ones appended already) into out."""
+        batch = self._ragged(layer, row_start, kv_len)
+        dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, q.shape[0]
+        qs = rows_of(q, "q", layer.n_heads, D, dt, dev)
+        os_ = rows_of(out, "out", layer.n_heads, D, dt, dev, rows)
+        check(workspace, "workspace", torch.uint8, dev)
+        dflash_paged_attention(self.h, layer.struct, batch, rows, row_start, kv_len, q, qs,
+                               D ** -0.5 if scale is None else scale, 1 if causal else 0, out, os_,
+                               workspace, workspace.numel(), _stream())
+
+    def _sampling(self, logits, temperature, top_k, top_p, min_p):
+        if logits.dim() < 2 or logits.stride(-1) != 1:
+            raise ValueError("logits: rows of contiguous values are needed")
+        flat = logits.flatten(0, -2) if logits.dim() > 2 else logits
+        if flat.data_ptr() != logits.data_ptr():
+            raise ValueError("logits: leading dims must flatten without a copy")
+        rows, vocab = flat.shape
+        n = None
+        for t, name, dt in ((temperature, "temperature", torch.float32),
+                            (top_k, "top_k", torch.int32), (top_p, "top_p", torch.float32),
+                            (min_p, "min_p", torch.float32)):
+            if t is None:
+                continue
+            check(t, name, dt, logits.device)
+            if n is not None and t.numel() != n:
+                raise ValueError(f"{name}: as many entries as the other parameters are needed")
+            n = t.numel()
+        if n is not None and (n == 0 or rows % n):
+            raise ValueError("sampling parameters: their count must divide the rows")
+        ptr = [t.data_ptr() if t is not None else None for t in (temperature, top_k, top_p, min_p)]
+        sp = DflashSampling(*ptr, max(1, rows // n if n else 1))
+        return flat, rows, vocab, flat.stride(0) if rows > 1 else vocab, sp
+
+    def target_probs(self, logits, probs, temperature=None, top_k=None, top_p=None, min_p=None):
+        """Sampling distribution of logits [..., V] into probs float32 of the
+        same shape; parameters are device arrays whose length divides the rows
+        (one entry a request for a [B, S, V] block)."""
+        flat, rows, vocab, ld, sp = self._sampling(logits, temperature, top_k, top_p, min_p)
+        check(probs, "probs", torch.float32, logits.device, logits.shape)
+        dflash_target_probs(self.h, rows, vocab, flat, dtype_code(logits, "logits"), ld, sp, probs,
+                            _stream())
+
+    def sample_tokens(self, logits, exp_noise, ids, prob=None, temperature=None, top_k=None,
+                      top_p=None, min_p=None):
+        """Tokens drawn from that distribution: exp_noise float32 like logits,
+        ids int32 (and prob float32) without the last dim."""
+        flat, rows, vocab, ld, sp = self._sampling(logits, temperature, top_k, top_p, min_p)
+        dev, lead = logits.device, logits.shape[:-1]
+        check(exp_noise, "exp_noise", torch.float32, dev, logits.shape)
+        check(ids, "ids", torch.int32, dev, lead)
+        if prob is not None:
+            check(prob, "prob", torch.float32, dev, lead)
+        dflash_sample_tokens(self.h, rows, vocab, flat, dtype_code(logits, "logits"), ld, sp,
+                             exp_noise, ids, prob, _stream())
 
     def set_fusion(self, on):
         """Dependent GEMMs as one fused launch (True) or one launch each (False)."""

@@ -70,6 +70,10 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 } dflash_dtype;
 #define DFLASH_DERR_OUTPUT_ROW 0x10u  /* output_ids write past out_stride */
 #define DFLASH_DERR_TIMEOUT 0x20u     /* a bounded wait inside a kernel gave up */
 #define DFLASH_DERR_ROW_RANGE 0x40u   /* inject: negative n_rows, or rows outside [0, total_rows) */
+                                      /* target side: a row_start pair that is no range of rows, or
+                                         a row that two requests claim */
+#define DFLASH_DERR_SAMPLING 0x80u    /* a sampling parameter outside its range */
+#define DFLASH_DERR_EMPTY_ROW 0x100u  /* a row of logits with nothing to sample from */
 
 /*
  * Draft model shape.  The draft shares the target's embedding and lm_head,
@@ -434,6 +438,195 @@ int dflash_profile_collect(dflash_handle *h, dflash_profile_entry *out, int32_t 
  */
 int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hidden, int32_t *ids,
                                  uint32_t *status, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The target's side of a draft-verify cycle.
+ *
+ * Verification runs the target over each request's block: the projected
+ * queries, keys and values of every layer go through dflash_append_kv (head
+ * norms, rotary positions, append to the layer's paged cache) and
+ * dflash_paged_attention; the target's logits become the distribution that
+ * dflash_accept_commit_sampled takes through dflash_target_probs, or tokens
+ * (the first anchor after a prompt, decoding without a draft) through
+ * dflash_sample_tokens.  The calls serve prompts (many rows a request) and
+ * single tokens alike.  The handle gives them the device error word, the
+ * bound workspace's device and the per-kernel timing; the target's shape
+ * comes with the call and is independent of the draft's.
+ *
+ * Rows of a batch are ragged: request b owns rows row_start[b] ..
+ * row_start[b+1]-1 (possibly none) of the row-major inputs, at positions
+ * kv_len[b], kv_len[b]+1, ...  Rows before row_start[0] and from
+ * row_start[batch] on belong to nobody and are never written.  A row_start
+ * pair that decreases or leaves [0, total_rows] sets DFLASH_DERR_ROW_RANGE
+ * and its request is skipped; so are rows that two requests would own.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * One target layer's paged K/V cache (device memory of the caller).
+ *   k_pages/v_pages  [n_pages, 64, n_kv_heads, head_dim] of `dtype`, 16-byte
+ *                    aligned
+ *   page_table       int32 [batch, pages_per_req]
+ *   prefix_pages     int32 [prefix_len / 64]: pages of a prefix that every
+ *                    request of the batch shares (a system prompt, a prompt
+ *                    sampled many times); NULL with prefix_len 0
+ *   prefix_len       rows of that prefix, a multiple of 64
+ * Position p of request b is row p % 64 of page prefix_pages[p / 64] when p <
+ * prefix_len, else of page page_table[b][(p - prefix_len) / 64].  kv_len[b]
+ * counts the prefix and must be at least prefix_len wherever request b has
+ * rows (else DFLASH_DERR_KV_CAPACITY and the request is skipped, as for rows
+ * past the page table).
+ * n_heads a multiple of n_kv_heads, at most 128 query heads per KV head;
+ * head_dim 64 or 128.
+ */
+typedef struct {
+  dflash_dtype dtype;
+  int32_t n_heads, n_kv_heads, head_dim;
+  void *k_pages, *v_pages;
+  int32_t n_pages;
+  const int32_t *page_table;
+  int32_t pages_per_req;
+  const int32_t *prefix_pages;
+  int32_t prefix_len;
+} dflash_layer_kv;
+
+/*
+ * Rotary positions.  The leading rotary_dim dims of a head (even, at most the
+ * head's; 0: none) are rotated as pairs (i, i + rotary_dim/2), or (2i, 2i+1)
+ * when interleaved: pair i of position p turns by p * f_i, and cos and sin are
+ * multiplied by amplitude.  f_i is held in turns per position as a 64-bit
+ * fraction, so the angle of any position is reduced exactly (the product
+ * wraps modulo one turn) and needs no table.  dflash_rope_init fills the plan
+ * from a base theta, f_i = theta^(-2i/rotary_dim), scaled by
+ *   DFLASH_ROPE_LINEAR  f_i / factor
+ *   DFLASH_ROPE_BANDS   with r = original_positions f_i / 2 pi (turns over the
+ *                       original context) and s = clamp((r - low) / (high -
+ *                       low), 0, 1): f_i ((1 - s) / factor + s)
+ *   DFLASH_ROPE_YARN    f_i (a / factor + 1 - a), a = clamp((i - lo) / max(hi -
+ *                       lo, 0.001), 0, 1), lo = max(floor(c(high)), 0), hi =
+ *                       min(ceil(c(low)), rotary_dim - 1), c(r) = rotary_dim
+ *                       ln(original_positions / (2 pi r)) / (2 ln theta);
+ *                       amplitude 0.1 ln(factor) + 1 (factor >= 1)
+ * low / high: 0 takes the usual 1 and 4 (BANDS), 1 and 32 (YARN).
+ */
+typedef enum {
+  DFLASH_ROPE_NONE = 0,
+  DFLASH_ROPE_LINEAR = 1,
+  DFLASH_ROPE_BANDS = 2,
+  DFLASH_ROPE_YARN = 3
+} dflash_rope_scaling;
+
+typedef struct {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float amplitude;
+  uint64_t turns[64];
+} dflash_rope;
+
+int dflash_rope_init(int32_t rotary_dim, int32_t interleaved, double theta,
+                     dflash_rope_scaling scaling, double factor, double original_positions,
+                     double low, double high, dflash_rope *out);
+
+/*
+ * Head norms, rotary positions and the append of new rows to a layer's cache
+ * in one pass.  For every owned row and head, y = rope(RMSNorm(x) * gain) for
+ * queries and keys (fp32 arithmetic, rounded once), values as they are; keys
+ * and values go to their cache rows, queries to q_out.  kv_len is read only:
+ * every layer of the step appends at the same positions and the caller
+ * advances it (after acceptance, by the committed rows).
+ *   q, k, v   [total_rows, heads, head_dim] with a row stride in elements
+ *             (slices of one fused projection); q may be NULL with q_out
+ *   q_gain, k_gain  [head_dim], NULL for no norm; eps >= 0
+ *   rope      host, read during the call
+ *   q_out     [total_rows, n_heads, head_dim], its own row stride; may be q
+ * Pointers 16-byte aligned (gains too), strides multiples of 16 bytes.
+ * Rows whose cache row does not exist are flagged (DFLASH_DERR_KV_CAPACITY,
+ * DFLASH_DERR_PAGE_RANGE) and skipped whole.  Two rows of one call must not
+ * fall on one cache row (pages shared by requests past their prefix).
+ */
+int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch, int32_t total_rows,
+                     const int32_t *row_start, const int32_t *kv_len, const void *q,
+                     int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                     int64_t v_stride, const void *q_gain, const void *k_gain, float eps,
+                     const dflash_rope *rope, void *q_out, int64_t q_out_stride,
+                     dflash_stream_t stream);
+
+/*
+ * Attention of the new rows over the cache that dflash_append_kv filled:
+ *   out[t, h] = sum_p softmax_p(scale q[t, h] . K[p, h / group]) V[p, h / group]
+ * over positions p <= that row's own (causal), or over all kv_len[b] +
+ * (row_start[b+1] - row_start[b]) positions of its request (causal 0).  A
+ * shared prefix is read once for the whole batch: its keys meet the query
+ * rows of all requests as one matrix, and the partial softmax results of the
+ * prefix and of the requests' own rows are joined at the end.
+ *   q, out    [total_rows, n_heads, head_dim], row strides in elements
+ *             (multiples of 16 bytes, pointers 16-byte aligned); out is not q
+ *   workspace device memory, 256-byte aligned, of at least
+ *             dflash_paged_attention_workspace_size bytes; written by the
+ *             call, nothing is kept in it between calls.  Calls that may
+ *             overlap on the GPU (two streams, two captured graphs) need one
+ *             each.
+ * batch <= 1024.  A page id outside the pool sets DFLASH_DERR_PAGE_RANGE and
+ * page 0 is read in its place.  Cache rows past a request's last are never
+ * used, whatever they hold.
+ */
+int dflash_paged_attention_workspace_size(const dflash_layer_kv *kv, int32_t batch,
+                                          int32_t total_rows, size_t *bytes);
+int dflash_paged_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                           int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                           const void *q, int64_t q_stride, float scale, int32_t causal, void *out,
+                           int64_t out_stride, void *workspace, size_t bytes,
+                           dflash_stream_t stream);
+
+/*
+ * Sampling parameters: device arrays of rows / rows_per_entry entries (row r
+ * uses entry r / rows_per_entry; block_size rows an entry for a verify
+ * block), NULL for the value that does nothing.
+ *   temperature  (1) >= 0, finite; weights w_v = exp((x_v - max x) / T).
+ *                0 (or below 2^-126): the largest logit alone, lowest id on ties
+ *   top_k        (0) the k largest logits, lower ids first among equal ones; <=
+ *                0 or >= vocab: all
+ *   top_p        (1) of those, in that order, the tokens whose predecessors'
+ *                share of the weight is below p (always the first); >= 1: all
+ *   min_p        (0) of those, the tokens with w_v >= min_p; at most 1
+ * A NaN logit counts as -infinity, +infinity as the type's largest finite
+ * value; -infinity is never kept.  A parameter out of range (NaN too) sets
+ * DFLASH_DERR_SAMPLING and the row is skipped; a row of -infinities sets
+ * DFLASH_DERR_EMPTY_ROW and gets zero probabilities, id -1.
+ */
+typedef struct {
+  const float *temperature;
+  const int32_t *top_k;
+  const float *top_p;
+  const float *min_p;
+  int32_t rows_per_entry;
+} dflash_sampling;
+
+/*
+ * The target's sampling distribution: probs[r][v] = w_v / sum of the kept w,
+ * 0 for tokens that the filters drop (float32 [rows, vocab], the layout that
+ * dflash_accept_commit_sampled reads).  logits: [rows, vocab] of `dtype` with
+ * a row stride in elements; any alignment of the type.  probs must not
+ * overlap logits.  The borders of top-p and min-p are decided on weights and
+ * sums of about 2^-28 relative error, the same in every run.
+ * vocab <= 524288 (bf16) or 262144 (fp32).
+ */
+int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
+                        dflash_dtype dtype, int64_t row_stride, const dflash_sampling *params,
+                        float *probs, dflash_stream_t stream);
+
+/*
+ * Tokens drawn from that distribution without storing it: ids[r] = argmax over
+ * the kept v of w_v / exp_noise[r][v] (the exponential race of
+ * dflash_accept_commit_sampled: an exact draw, lowest id on ties, float32
+ * IEEE division), read only where v is kept.
+ *   exp_noise  device float32 [rows, vocab] Exp(1) variates (> 0)
+ *   ids        device int32 [rows]
+ *   prob       optional device float32 [rows]: the drawn token's probability
+ */
+int dflash_sample_tokens(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
+                         dflash_dtype dtype, int64_t row_stride, const dflash_sampling *params,
+                         const float *exp_noise, int32_t *ids, float *prob,
+                         dflash_stream_t stream);
 
 /* Static description of a status code. */
 const char *dflash_status_string(int status);
