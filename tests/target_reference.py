@@ -143,5 +143,5 @@ def sample64(x, T, k, p, mp):
     out = torch.zeros_like(x)
     out[at] = torch.where(keep, w, 0.0)
     full = torch.zeros_like(x)
-    full[at] = a
+    full[at] = torch.where(keep, a, 0.0)
     return out, full, near
