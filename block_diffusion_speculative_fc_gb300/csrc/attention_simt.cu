@@ -156,6 +156,7 @@ cudaError_t prepare_kernels() {
   if (e == cudaSuccess) e = prepare_selector();
   if (e == cudaSuccess) e = prepare_sampling();
   if (e == cudaSuccess) e = prepare_paged_attention_simt();
+  if (e == cudaSuccess) e = prepare_paged_attention_tc();
   return e;
 }
 

@@ -1,5 +1,5 @@
-// CUDA-core attention of new rows over a paged cache (the tensor cores have
-// no exact-fp32 kind).  One CTA per (row, KV head) holds the group's query
+// CUDA-core attention of new rows over a paged fp32 cache (the tensor cores
+// have no exact-fp32 kind).  One CTA per (row, KV head) holds the group's query
 // heads and streams the row's keys in tiles of 32 with an online softmax: a
 // lane per key for the scores, a lane per dim for the weighted sum.
 #include <math.h>
@@ -112,17 +112,13 @@ template <typename T, int D> cudaError_t prepare() {
 
 }  // namespace
 
-cudaError_t launch_paged_attention_simt(int dtype, const PagedAttnParams &p, cudaStream_t s) {
-  if (dtype == DFLASH_BF16) return p.D == 64 ? launch<bf16, 64>(p, s) : launch<bf16, 128>(p, s);
+cudaError_t launch_paged_attention_simt(const PagedAttnParams &p, cudaStream_t s) {
   return p.D == 64 ? launch<float, 64>(p, s) : launch<float, 128>(p, s);
 }
 
 cudaError_t prepare_paged_attention_simt() {
-  cudaError_t e = prepare<bf16, 64>();
-  if (e == cudaSuccess) e = prepare<bf16, 128>();
-  if (e == cudaSuccess) e = prepare<float, 64>();
-  if (e == cudaSuccess) e = prepare<float, 128>();
-  return e;
+  const cudaError_t e = prepare<float, 64>();
+  return e == cudaSuccess ? prepare<float, 128>() : e;
 }
 
 }  // namespace dflash

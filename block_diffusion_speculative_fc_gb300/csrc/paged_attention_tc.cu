@@ -1,0 +1,1019 @@
+// bf16 attention of new rows over a paged cache with a shared prefix, on the
+// tensor cores (tcgen05 + TMEM).
+//
+// Per KV head g, query row r = (token, head of g's group) attends to a list of
+// keys; the rows of a batch fall into segments that share their keys: the
+// shared prefix (the rows of all requests) and each request's own rows (its
+// rows).  A work item is up to 256 rows of a segment times a range of 128-key
+// tiles (two cache pages).  Partial results (o / l, log2 of the weight) of a
+// row that several items hold are joined by a last launch.
+//
+// The softmax is the running one: tile by tile S = Q K^T, w = 2^(S c - m), O +=
+// w V, l += sum w, with c = scale log2 e; m is a running reference that follows
+// the row maximum only when that exceeds it by more than 2^8 (the result o / l
+// does not depend on m; w <= 2^8 keeps fp32 sums far from overflow), so that
+// O in TMEM is rarely rescaled.
+//
+// Two streams of 128 threads (a thread per row: TMEM lane = row, no exchange
+// between threads) alternate on the tensor cores: while one takes the softmax
+// of its tile, the other's products run.  With more than 128 rows the streams
+// hold 128 rows each and share every K/V tile (32 bytes of K/V per SM clock at
+// full tensor rate; 128 rows would need the 64 that L2 can just deliver).  With
+// fewer, both hold the same rows and take even and odd tiles, which halves the
+// serial chain of a tile: those items are bound by the K/V bytes.  S and the
+// rounded weights w share their TMEM columns (w is the second product's A
+// operand, read from TMEM; V is read as staged, keys by dims).
+//
+// Warps 0-3, 4-7: the streams; 8: TMA producer (a ring of K and V tiles, one
+// copy per page and 64 dims); 9: issues the MMAs; 10, 11 complete the register
+// split of the last warpgroup.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "paged_rows.cuh"
+#include "target_ops.h"
+
+namespace dflash {
+namespace {
+
+constexpr int KT = 128;                   // keys of a tile
+constexpr int ROWS = 256;                 // rows of an item, 128 a stream
+constexpr int THREADS = 384;
+// registers a thread: 168 at launch (384 threads), then 208 for the streams and 80 for the rest
+// (256 * 208 + 128 * 80 <= 384 * 168)
+constexpr int REGS_STREAM = 208, REGS_REST = 80;
+constexpr int PLAN_THREADS = 1024;
+constexpr int ITEMS_PER_SM = 3;           // what splits aim at
+constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile)
+constexpr float TAU = 8.f;
+constexpr uint32_t WAIT_LIMIT = 1u << 22;
+
+template <int D> struct Cfg {
+  static constexpr int TILE = KT * D * 2;             // K (or V) tile
+  static constexpr int NSLOT = D == 128 ? 5 : 10;
+  static constexpr int Q_TILE = 128 * D * 2;
+  static constexpr int OFF_RING = 2 * Q_TILE;
+  static constexpr int OFF_ML = OFF_RING + NSLOT * TILE;      // [128] float2
+  static constexpr int OFF_BARS = OFF_ML + 128 * 8;
+  // full[NSLOT], empty[NSLOT], s_full[2], p_full[2], o_full[2], o_read[2], q_full, q_free,
+  // ml_full, ml_free, done
+  static constexpr int N_BARS = 2 * NSLOT + 13;
+  static constexpr int SMEM = 1024 + OFF_BARS + N_BARS * 8 + 16;
+  static_assert(SMEM <= 227 * 1024, "one CTA per SM");
+};
+
+struct Item {
+  int g, r0, nrows, req;                  // KV head, first row (token * G + head), rows, request (-1: prefix)
+  int page0, ntiles, keys_left, part;     // first page, tiles, keys from the first to the segment's end, partial rows (-1: final)
+  int lim_base, lim_slope, pad0, pad1;    // keys that row's token sees: lim_base + lim_slope * token
+};
+struct Request {
+  int start, n, ctx, splits;              // first row, rows (0: skipped), own rows before them
+  int tiles, part, pad0, pad1;            // key tiles of a split, first partial row (-1: none)
+};
+struct Head {
+  int items, merge, prefix_splits, prefix_tiles;
+  int first_row, rows, pad0, pad1;        // rows that meet the prefix
+};
+
+struct Params {
+  CUtensorMap tmK, tmV;                   // dims {D, KVH, n_pages * 64}, box {64, 1, 64}
+  PagedAttnParams a;
+  Head *head;
+  Item *items;
+  Request *req;
+  int *row_req;                           // [total_rows]
+  float *part_o, *part_lse;               // [cap][D], [cap]
+  int cap, max_items, sms;
+  float scale_log2;                       // |scale| log2 e
+  uint32_t q_sign;                        // 0x80008000 when scale < 0
+};
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait for the phase of parity `parity`; false = gave up.
+__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity) {
+  for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if (i > 64) __nanosleep(64);
+  }
+  return false;
+}
+__device__ __forceinline__ void tma3(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
+      "l"((uint64_t)tm), "r"(su32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// D += A B^T: both operands in shared memory, or A in TMEM
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
+               : "memory");
+}
+// 32 columns of the warp's TMEM lanes, without the wait
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Shared-memory operand descriptors, 128-byte swizzle: K-major (rows of 128
+// bytes along K, 8-row groups 1 KB apart); MN-major (a row per K index, 64
+// elements along N; `lbo` bytes between 64-element blocks).
+__device__ __forceinline__ uint64_t desc_base(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) { return desc_base(saddr) | ((uint64_t)1 << 16); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return desc_base(saddr) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16);
+}
+// kind::f16: bf16 A and B, fp32 D; b_mn: B is MN-major
+constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// Place of V(t) and K(t) in an item's load order: the first `ahead` K tiles,
+// then V(0), K(ahead), V(1), K(ahead + 1), ...
+__device__ __forceinline__ int order_v(int t, int n, int ahead) {
+  return min(ahead, n) + t + min(t, max(0, n - ahead));
+}
+__device__ __forceinline__ int order_k(int t, int n, int ahead) {
+  return t < ahead ? t : order_v(t - ahead, n, ahead) + 1;
+}
+
+__device__ __forceinline__ Item load_item(const Item *p) {
+  const int4 *s = reinterpret_cast<const int4 *>(p);
+  const int4 a = __ldg(s), b = __ldg(s + 1), c = __ldg(s + 2);
+  Item it;
+  it.g = a.x, it.r0 = a.y, it.nrows = a.z, it.req = a.w;
+  it.page0 = b.x, it.ntiles = b.y, it.keys_left = b.z, it.part = b.w;
+  it.lim_base = c.x, it.lim_slope = c.y;
+  return it;
+}
+
+// ------------------------------------------------------------------ plan
+// One CTA: checks every request, chooses the key split of every segment (items
+// of at least U tile-units, U such that about ITEMS_PER_SM items an SM come
+// out; a unit is one 128-row tile), lays out partial rows and lists the items,
+// row tiles that see more keys first.
+__device__ __forceinline__ long long block_sum(long long v, long long *s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// exclusive scan; total in `total`
+__device__ __forceinline__ int block_scan(int v, int *s, int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();
+  if (lane == 31) s[warp] = inc;
+  __syncthreads();
+  int w = s[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += x;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + inc - v;
+}
+struct Split {
+  int tiles, splits;
+};
+__device__ __forceinline__ Split split_keys(int nkt, int R, long long U) {
+  const int unit = R > 128 ? 2 : 1;
+  long long per = (U + unit - 1) / unit;
+  per = per < 1 ? 1 : per;
+  const int ns = nkt > 0 ? (int)((nkt + per - 1) / per) : 0;
+  Split s;
+  s.tiles = ns > 0 ? (nkt + ns - 1) / ns : 1;
+  s.splits = (nkt + s.tiles - 1) / s.tiles;
+  return s;
+}
+__device__ __forceinline__ int row_units(int R) { return R / ROWS * 2 + (R % ROWS > 128 ? 2 : R % ROWS > 0); }
+
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ Params p) {
+  pdl_wait();
+  __shared__ long long s_sum[32];
+  __shared__ int s_scan[32];
+  __shared__ int s_first[PLAN_THREADS + 2];     // first item of every segment (prefix, requests)
+  __shared__ int s_start[PLAN_THREADS], s_n[PLAN_THREADS], s_ctx[PLAN_THREADS], s_tiles[PLAN_THREADS];
+  __shared__ int s_part[PLAN_THREADS], s_splits[PLAN_THREADS];
+  __shared__ int s_lo, s_hi;
+  const PagedRows &r = p.a.rows;
+  const int b = threadIdx.x, G = p.a.H / p.a.KVH, KVH = p.a.KVH, prefix = r.prefix_len;
+  if (b == 0) {
+    s_lo = r.total_rows;
+    s_hi = 0;
+  }
+  __syncthreads();
+  int start = 0, n = 0, ctx = 0;
+  if (b < r.B) {
+    const int a = r.row_start[b], e = r.row_start[b + 1], kv = r.kv_len[b];
+    if (a < 0 || a > e || e > r.total_rows) {
+      raise_error(p.a.err, DFLASH_DERR_ROW_RANGE);
+    } else if (e > a) {
+      if (kv < prefix || (int64_t)kv + (e - a) - prefix > (int64_t)r.pages_per_req * kPageRows) {
+        raise_error(p.a.err, DFLASH_DERR_KV_CAPACITY);
+      } else {
+        start = a;
+        n = e - a;
+        ctx = kv - prefix;
+        atomicMin(&s_lo, a);
+        atomicMax(&s_hi, e);
+      }
+    }
+  }
+  __syncthreads();
+  const int lo = s_lo, rows = max(0, s_hi - s_lo);
+  const int R = n * G, keys = ctx + n, nkt = n > 0 ? (keys + KT - 1) / KT : 0;
+  const int Rp = prefix > 0 ? rows * G : 0, nktp = Rp > 0 ? prefix / KT + (prefix % KT != 0) : 0;
+  const long long W = block_sum((long long)KVH * nkt * row_units(R), s_sum) +
+                      (long long)KVH * nktp * row_units(Rp);
+  long long U = (W + (long long)ITEMS_PER_SM * p.sms - 1) / ((long long)ITEMS_PER_SM * p.sms);
+  U = U < 2 ? 2 : U;
+  Split sp, spp;
+  int part = 0, items = 0, total_rows = 0, total_items = 0;
+  bool joined = false;
+  const int nrt = (R + ROWS - 1) / ROWS, nrtp = (Rp + ROWS - 1) / ROWS;
+  for (int pass = 0; pass < 2; ++pass) {
+    sp = split_keys(nkt, R, U);
+    spp = split_keys(nktp, Rp, U);
+    joined = n > 0 && (prefix > 0 || sp.splits > 1);
+    part = block_scan(joined ? sp.splits * KVH * R : 0, s_scan, total_rows);
+    items = block_scan(KVH * nrt * sp.splits, s_scan, total_items);
+    const int prefix_rows = spp.splits * KVH * Rp, prefix_items = KVH * nrtp * spp.splits;
+    part += prefix_rows;
+    items += prefix_items;
+    total_rows += prefix_rows;
+    total_items += prefix_items;
+    if (total_rows <= p.cap && total_items <= p.max_items) break;
+    U = 1LL << 40;   // one split each always fits (the bound on splits makes this unreachable)
+  }
+  s_first[b + 1] = items;
+  if (b == 0) {
+    s_first[0] = 0;
+    Head h;
+    h.items = total_items;
+    h.prefix_splits = spp.splits;
+    h.prefix_tiles = spp.tiles;
+    h.first_row = lo;
+    h.rows = rows;
+    h.merge = total_rows > 0;
+    h.pad0 = h.pad1 = 0;
+    *p.head = h;
+  }
+  s_start[b] = start;
+  s_n[b] = n;
+  s_ctx[b] = ctx;
+  s_tiles[b] = sp.tiles;
+  s_splits[b] = sp.splits;
+  s_part[b] = joined ? part : -1;
+  if (b < r.B) {
+    Request q;
+    q.start = start, q.n = n, q.ctx = ctx, q.splits = sp.splits;
+    q.tiles = sp.tiles, q.part = joined ? part : -1, q.pad0 = q.pad1 = 0;
+    p.req[b] = q;
+  }
+  __syncthreads();
+  for (int i = b; i < total_items; i += PLAN_THREADS) {
+    // last segment whose first item is <= i (empty segments share a first item)
+    int s0 = 0, s1 = r.B;
+    while (s0 < s1) {
+      const int mid = (s0 + s1 + 1) >> 1;
+      if (s_first[mid] <= i) s0 = mid;
+      else s1 = mid - 1;
+    }
+    Item it;
+    const int j = i - s_first[s0];
+    if (s0 == 0) {
+      const int per = KVH * spp.splits, rt = j / per, g = j % per / spp.splits, s = j % spp.splits;
+      it.g = g;
+      it.r0 = lo * G + rt * ROWS;
+      it.nrows = min(ROWS, Rp - rt * ROWS);
+      it.req = -1;
+      it.page0 = s * spp.tiles * 2;
+      it.ntiles = min(spp.tiles, nktp - s * spp.tiles);
+      it.keys_left = prefix - s * spp.tiles * KT;
+      it.part = (g * spp.splits + s) * Rp + rt * ROWS;
+      it.lim_base = it.keys_left;
+      it.lim_slope = 0;
+    } else {
+      const int q = s0 - 1, ns = s_splits[q], tiles = s_tiles[q], nq = s_n[q], c = s_ctx[q], st = s_start[q];
+      const int Rq = nq * G, per = KVH * ns, nt = (Rq + ROWS - 1) / ROWS;
+      const int rt = nt - 1 - j / per, g = j % per / ns, s = j % ns;
+      const int last = (min(Rq, (rt + 1) * ROWS) - 1) / G;     // last token of the row tile
+      const int seen = p.a.causal ? c + last + 1 : c + nq;
+      it.g = g;
+      it.r0 = st * G + rt * ROWS;
+      it.nrows = min(ROWS, Rq - rt * ROWS);
+      it.req = q;
+      it.page0 = s * tiles * 2;
+      it.ntiles = max(0, min(tiles, (seen + KT - 1) / KT - s * tiles));
+      it.keys_left = c + nq - s * tiles * KT;
+      it.part = s_part[q] >= 0 ? s_part[q] + (g * ns + s) * Rq + rt * ROWS : -1;
+      it.lim_slope = p.a.causal;
+      it.lim_base = (p.a.causal ? c + 1 - st : c + nq) - s * tiles * KT;
+    }
+    it.pad0 = it.pad1 = 0;
+    p.items[i] = it;
+  }
+  if (total_rows > 0) {   // the owner of every row, for the join
+    for (int t = b; t < r.total_rows; t += PLAN_THREADS) p.row_req[t] = -1;
+    __syncthreads();
+    for (int q = b >> 5; q < r.B; q += PLAN_THREADS / 32)
+      for (int t = b & 31; t < s_n[q]; t += 32) p.row_req[s_start[q] + t] = q;
+  }
+}
+
+// ------------------------------------------------------------------ attention
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  constexpr int NS = C::NSLOT, NB = D / 64, CH = D / 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *ring = smem + C::OFF_RING;
+  float2 *s_ml = (float2 *)(smem + C::OFF_ML);
+  uint64_t *full = (uint64_t *)(smem + C::OFF_BARS), *empty = full + NS;
+  uint64_t *s_full = empty + NS, *p_full = s_full + 2, *o_full = p_full + 2, *o_read = o_full + 2;
+  uint64_t *q_full = o_read + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *ml_free = ml_full + 1;
+  uint64_t *done = ml_free + 1;
+  uint32_t *s_tmem = (uint32_t *)(done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.a.H / p.a.KVH;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_read[i], 128);
+    }
+    mbar_init(q_full, 256);
+    mbar_init(q_free, 1);
+    mbar_init(ml_full, 128);
+    mbar_init(ml_free, 128);
+    mbar_init(done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 8 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmK) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmV) : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_wait();
+  const int n_items = __ldg(&p.head->items);
+  bool ok = true;
+  // the CTA's items in order, empty ones left out; false at the end
+  int next_index = blockIdx.x;
+  auto next_item = [&](Item &it) {
+    while (next_index < n_items) {
+      it = load_item(p.items + next_index);
+      next_index += gridDim.x;
+      if (it.ntiles > 0) return true;
+    }
+    return false;
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    if (warp == 8) {
+      // ------------------------------------------------------------ producer (one warp)
+      uint32_t u = 0;                       // tiles issued
+      Item it;
+      int prev0 = 0, prev1 = 0, cur0 = 0, cur1 = 0;   // pages of the last two K tiles
+      while (ok && next_item(it)) {
+        const int n = it.ntiles, ahead = it.nrows > 128 ? 1 : 2;
+        const int npages = (min(it.keys_left, n * KT) + kPageRows - 1) / kPageRows;
+        const int *list = (it.req < 0 ? p.a.rows.prefix_pages
+                                      : p.a.rows.page_table + (int64_t)it.req * p.a.rows.pages_per_req) + it.page0;
+        int batch = 0;
+        auto issue = [&](const CUtensorMap *tm, int t, int pg0, int pg1) {
+          const int slot = u % NS;
+          bool good = true;
+          if (lane == 0) {
+            good = mbar_wait(&empty[slot], ((u / NS) & 1) ^ 1);
+            if (good) {
+              const bool two = 2 * t + 1 < npages;
+              asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[slot])),
+                           "r"(two ? C::TILE : C::TILE / 2)
+                           : "memory");
+              uint8_t *dst = ring + slot * C::TILE;
+  #pragma unroll
+              for (int k = 0; k < NB; ++k) {
+                tma3(dst + k * (KT * 128), tm, &full[slot], 64 * k, it.g, pg0 * kPageRows);
+                if (two) tma3(dst + k * (KT * 128) + 8192, tm, &full[slot], 64 * k, it.g, pg1 * kPageRows);
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+          if (ok) ++u;
+        };
+        auto issue_k = [&](int t) {
+          const int j = 2 * t;
+          if (j % 32 == 0) {                // the next 32 pages, one a lane
+            int pg = 0;
+            if (j + lane < npages) {
+              pg = __ldg(list + j + lane);
+              if (pg < 0 || pg >= p.a.rows.n_pages) {
+                raise_error(p.a.err, DFLASH_DERR_PAGE_RANGE);
+                pg = 0;
+              }
+            }
+            batch = pg;
+          }
+          prev0 = cur0, prev1 = cur1;
+          cur0 = __shfl_sync(0xffffffffu, batch, j % 32);
+          cur1 = __shfl_sync(0xffffffffu, batch, j % 32 + 1);
+          issue(&p.tmK, t, cur0, cur1);
+        };
+        for (int t = 0; t < min(ahead, n) && ok; ++t) issue_k(t);
+        for (int t = 0; t < n && ok; ++t) {
+          // K(t) is the last K tile issued, or the one before it
+          const bool older = ahead == 2 && t + 1 < n;
+          issue(&p.tmV, t, older ? prev0 : cur0, older ? prev1 : cur1);
+          if (ok && t + ahead < n) issue_k(t + ahead);
+        }
+      }
+      if (lane == 0) {
+        if (!ok) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
+        // every copy has landed before the CTA exits
+        for (uint32_t v = u > (uint32_t)NS ? u - NS : 0; v < u; ++v) mbar_wait(&full[v % NS], (v / NS) & 1);
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ MMA issuer (one thread)
+      if (lane == 0) {
+        constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
+        const uint32_t q_addr = su32(smem), ring_addr = su32(ring);
+        uint32_t u = 0, k = 0;              // ring tiles and number of the items before
+        uint32_t p_par = 0;                 // bit x: parity of p_full[x]
+        uint32_t o_used = 0, o_par = 3;     // bit x: stream x has had an item; parity of its o_read
+        auto wait = [&](uint64_t *b, uint32_t parity) {
+          if (ok && !mbar_wait(b, parity)) ok = false;
+        };
+        Item it;
+        while (ok && next_item(it)) {
+          // Steps (t, x): stream x takes tile t.  A pair takes every tile in both
+          // streams, a single row tile alternates.  A step is O_x += w V(t), then S_x
+          // of the stream's next tile t + ahead (the first S before the loop).
+          const int n = it.ntiles, pair = it.nrows > 128 ? 1 : 0, ahead = 2 - pair;
+          const int steps = n << pair;
+          auto slot_of = [&](int order) { return (int)((u + order) % NS); };
+          auto issue_s = [&](int x, int t) {
+            const int order = order_k(t, n, ahead), slot = slot_of(order);
+            wait(&full[slot], ((u + order) / NS) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t qd = desc_k(q_addr + (pair & x) * C::Q_TILE), kd = desc_k(ring_addr + slot * C::TILE);
+  #pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              umma_ss(tmem + x * KT, qd + (i >> 2) * ((128 * 128) >> 4) + 2 * (i & 3),
+                      kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3), ID_S, i ? 1u : 0u);
+            umma_commit(&s_full[x]);
+            if (x == 1 || !pair) {          // the tile's last use
+              umma_commit(&empty[slot]);
+              if (t == n - 1) umma_commit(q_free);
+            }
+          };
+          wait(q_full, k & 1);
+  #pragma unroll 1
+          for (int i = 0; i < min(2, steps) && ok; ++i) issue_s(i, pair ? 0 : i);
+  #pragma unroll 1
+          for (int i = 0; i < steps && ok; ++i) {
+            const int x = i & 1, t = i >> pair;
+            const int order = order_v(t, n, ahead), slot = slot_of(order);
+            wait(&p_full[x], (p_par >> x) & 1);
+            p_par ^= 1u << x;
+            if (t < ahead) {                // the item before has read this stream's O
+              if ((o_used >> x) & 1) wait(&o_read[x], (o_par >> x) & 1);
+              o_used |= 1u << x;
+              o_par ^= 1u << x;
+            }
+            wait(&full[slot], ((u + order) / NS) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = desc_mn(ring_addr + slot * C::TILE, KT * 128);
+  #pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              umma_ts(tmem + 256 + x * 128, tmem + x * KT + kk * 8, vd + kk * (2048 >> 4), ID_O,
+                      (t < ahead && kk == 0) ? 0u : 1u);
+            if (x == 1 || !pair) umma_commit(&empty[slot]);
+            if (t + ahead < n) issue_s(x, t + ahead);
+            else umma_commit(&o_full[x]);
+          }
+          u += 2 * n;
+          ++k;
+        }
+        umma_commit(done);
+        if (!mbar_wait(done, 0)) ok = false;   // every MMA has ended before TMEM is freed
+        if (!ok) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_STREAM));
+    // ------------------------------------------------------------ softmax, a row a thread
+    const int x = warp >> 2, row = threadIdx.x & 127;          // stream, row of its tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + x * KT;
+    const float sl = p.scale_log2;
+    // every wait is one for the warp, so that its lanes stay together
+    auto wait = [&](uint64_t *b, uint32_t parity) {
+      if (ok && !mbar_wait(b, parity)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    // the item's query rows: 128 of this stream, or half of the 128 of both
+    auto load_q = [&](const Item &it) {
+      const bool pair = it.nrows > 128;
+      constexpr int RP = 128 / CH;        // rows a pass of 128 threads
+      const int i0 = pair ? 0 : x * (CH / 2), i1 = pair ? CH : (x + 1) * (CH / 2);
+      const int first = pair ? x * 128 : 0, ch = row % CH;
+      uint8_t *dst = smem + (pair ? x : 0) * C::Q_TILE + (ch >> 3) * (128 * 128);
+      for (int i = i0; i < i1; i += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rr = (i + j) * RP + row / CH, r = it.r0 + first + rr;
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (first + rr < it.nrows) {
+            const int tok = r / G, h = it.g * G + r % G;
+            v[j] = __ldg(reinterpret_cast<const uint4 *>((const bf16 *)p.a.q + (int64_t)tok * p.a.q_stride +
+                                                         (int64_t)h * D) + ch);
+            v[j].x ^= p.q_sign;
+            v[j].y ^= p.q_sign;
+            v[j].z ^= p.q_sign;
+            v[j].w ^= p.q_sign;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rr = (i + j) * RP + row / CH;
+          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[j];
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(q_full);
+    };
+
+    uint32_t c = 0, u = 0, k = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
+    Item it, nit;
+    bool have = next_item(it);
+    if (have) load_q(it);
+    while (have) {
+      const int n = it.ntiles;
+      const bool pair = it.nrows > 128;
+      const int ahead = pair ? 1 : 2;
+      const int mine = pair ? x * 128 + row : row;             // this thread's row of the item
+      const bool live = (pair ? x * 128 : 0) + (warp & 3) * 32 < it.nrows;   // any row of the warp
+      const int tok = (it.r0 + mine) / G, h = it.g * G + (it.r0 + mine) % G;
+      const int lim = mine < it.nrows ? it.lim_base + it.lim_slope * tok : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int t = pair ? 0 : x; t < n && ok; t += pair ? 1 : 2) {
+        wait(&s_full[x], c & 1);
+        if (!ok) break;
+        ++c;
+        tc_fence_after();
+        if (live) {
+          uint32_t sv[KT];
+#pragma unroll
+          for (int i = 0; i < KT; i += 32) tmem_ld32(t_s + i, sv + i);
+          tmem_ld_wait();
+          const int vis = lim - t * KT;                        // visible keys of this tile
+          const bool whole = __all_sync(0xffffffffu, vis >= KT);
+          float mx;
+          if (whole) {
+            float a0 = __uint_as_float(sv[0]), a1 = __uint_as_float(sv[1]);
+            float a2 = __uint_as_float(sv[2]), a3 = __uint_as_float(sv[3]);
+#pragma unroll
+            for (int i = 4; i < KT; i += 4) {
+              a0 = fmaxf(a0, __uint_as_float(sv[i]));
+              a1 = fmaxf(a1, __uint_as_float(sv[i + 1]));
+              a2 = fmaxf(a2, __uint_as_float(sv[i + 2]));
+              a3 = fmaxf(a3, __uint_as_float(sv[i + 3]));
+            }
+            mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl;
+          } else {
+            mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < KT; ++i) mx = i < vis ? fmaxf(mx, __uint_as_float(sv[i])) : mx;
+            mx = vis > 0 ? mx * sl : -INFINITY;
+          }
+          float alpha = 1.f;
+          if (mx > m + TAU || m == -INFINITY) {
+            if (m != -INFINITY) alpha = ex2(m - mx);
+            m = mx;
+          }
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            // S of this tile was issued after the last O product of the stream: O is at rest
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(tmem + lanes + 256 + x * 128 + i, o);
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = half * 64 + 2 * i;
+              float p0 = ex2(fmaf(__uint_as_float(sv[e]), sl, -mm));
+              float p1 = ex2(fmaf(__uint_as_float(sv[e + 1]), sl, -mm));
+              if (!whole) {
+                p0 = e < vis ? p0 : 0.f;
+                p1 = e + 1 < vis ? p1 : 0.f;
+              }
+              l0 += p0;
+              l1 += p1;
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+              w[i] = *reinterpret_cast<uint32_t *>(&h2);
+            }
+            tmem_st32(t_s + half * 32, w);
+          }
+          l = fmaf(l, alpha, l0 + l1);
+          tmem_st_wait();
+        }
+        if (t == n - 1 && it.keys_left < n * KT) {
+          // V rows past the segment's last key may hold anything: 0 times it has to be 0
+          const int ov = u + order_v(t, n, ahead);
+          wait(&full[ov % NS], (ov / NS) & 1);
+          if (!ok) break;
+          uint8_t *vt = ring + (ov % NS) * C::TILE;
+          const int v0 = it.keys_left - t * KT;
+          for (int i = v0 * 8 + row; i < KT * 8; i += 128)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+      }
+      u += 2 * n;
+      const bool more = next_item(nit);
+      if (more && ok) {                    // the last S of the item has read Q
+        wait(q_free, k & 1);
+        if (ok) load_q(nit);
+      }
+      ++k;
+      if (!ok) break;
+      // ---- the item's rows: o / l and log2 of their weight, or the result
+      const bool both = !pair && n > 1;    // the other stream holds the odd tiles' share
+      if (both && x == 1) {
+        if (n_ml > 0) wait(ml_free, (n_ml - 1) & 1);
+        if (!ok) break;
+        s_ml[row] = make_float2(m, l);
+        mbar_arrive(ml_full);
+      }
+      if (pair || x == 0) {
+        wait(&o_full[x], (o_par >> x) & 1);
+        float a0 = 1.f, a1 = 0.f;
+        if (both) {
+          wait(&o_full[1], (o_par >> 1) & 1);
+          wait(ml_full, n_ml & 1);
+          if (!ok) break;
+          const float2 ml = s_ml[row];
+          const float ms = fmaxf(m, ml.x), base = ms == -INFINITY ? 0.f : ms;
+          a0 = ex2(m - base);
+          a1 = ex2(ml.x - base);
+          l = l * a0 + ml.y * a1;
+          m = ms;
+          mbar_arrive(ml_free);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          a0 *= inv;
+          a1 *= inv;
+          const bool store = mine < it.nrows;
+          bf16 *out = (bf16 *)p.a.out + (int64_t)tok * p.a.out_stride + (int64_t)h * D;
+          float *po = p.part_o + (int64_t)(it.part + mine) * D;
+          if (store && it.part >= 0) p.part_lse[it.part + mine] = l > 0.f ? m + log2f(l) : -INFINITY;
+#pragma unroll
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(a0 != 0.f ? __uint_as_float(o[j]) * a0 : 0.f);
+            if (both) {
+              uint32_t q[32];
+              tmem_ld32(tmem + lanes + 256 + 128 + i, q);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) + (a1 != 0.f ? __uint_as_float(q[j]) * a1 : 0.f));
+            }
+            if (!store) continue;
+            if (it.part >= 0) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4 *>(po + i + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]),
+                                                            __uint_as_float(o[j + 2 * e + 1]));
+                  w[e] = *reinterpret_cast<uint32_t *>(&h2);
+                }
+                *reinterpret_cast<uint4 *>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&o_read[x]);
+        if (both) mbar_arrive(&o_read[1]);
+      }
+      // streams that took part in this item
+      o_par ^= pair || n > 1 ? 3u : 1u;
+      if (both) ++n_ml;
+      it = nit;
+      have = more;
+    }
+    if (!ok && lane == 0) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  pdl_trigger();   // every global write of this CTA is done
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ join
+// A warp a (row, head): out = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max)
+// over the prefix splits and the own splits whose first key the row sees.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
+  pdl_wait();
+  if (!__ldg(&p.head->merge)) return;
+  constexpr int V = D / 32;                // floats a lane
+  const int lane = threadIdx.x & 31, H = p.a.H, KVH = p.a.KVH, G = H / KVH;
+  const int nsp = __ldg(&p.head->prefix_splits), first = __ldg(&p.head->first_row);
+  const int Rp = p.a.rows.prefix_len > 0 ? __ldg(&p.head->rows) * G : 0;
+  const int total = p.a.rows.total_rows * H, step = gridDim.x * (blockDim.x >> 5);
+  for (int idx = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); idx < total; idx += step) {
+    const int t = idx / H, h = idx % H, g = h / G;
+    const int b = __ldg(p.row_req + t);
+    if (b < 0) continue;
+    const int4 r0 = __ldg(reinterpret_cast<const int4 *>(p.req + b));
+    const int4 r1 = __ldg(reinterpret_cast<const int4 *>(p.req + b) + 1);
+    if (r1.y < 0) continue;                // written by its one item
+    const int R = r0.y * G, seen = p.a.causal ? r0.z + (t - r0.x) + 1 : r0.z + r0.y;
+    const int span = r1.x * KT, own = min(r0.w, (seen + span - 1) / span);
+    const int64_t at_p = (int64_t)g * nsp * Rp + (int64_t)(t - first) * G + h % G;
+    const int64_t at_o = r1.y + (int64_t)g * r0.w * R + (int64_t)(t - r0.x) * G + h % G;
+    const int parts = (Rp > 0 ? nsp : 0) + own, np = parts - own;
+    auto place = [&](int i) { return i < np ? at_p + (int64_t)i * Rp : at_o + (int64_t)(i - np) * R; };
+    float mx = -INFINITY;
+    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + place(i)));
+    mx = warp_max(mx);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float acc[V], den = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const float wl = i0 + lane < parts ? ex2(__ldcg(p.part_lse + place(i0 + lane)) - base) : 0.f;
+      const int m = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wl, i);
+        den += w;
+        const float *o = p.part_o + place(i0 + i) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(o));
+          acc[0] = fmaf(w, x.x, acc[0]);
+          acc[1] = fmaf(w, x.y, acc[1]);
+          acc[2] = fmaf(w, x.z, acc[2]);
+          acc[3] = fmaf(w, x.w, acc[3]);
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2 *>(o));
+          acc[0] = fmaf(w, x.x, acc[0]);
+          acc[1] = fmaf(w, x.y, acc[1]);
+        }
+      }
+    }
+    const float inv = 1.f / den;
+    __nv_bfloat162 *out = reinterpret_cast<__nv_bfloat162 *>((bf16 *)p.a.out + (int64_t)t * p.a.out_stride +
+                                                             (int64_t)h * D + lane * V);
+#pragma unroll
+    for (int v = 0; v < V / 2; ++v) out[v] = __floats2bfloat162_rn(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+EncodeTiledFn encoder() {
+  static EncodeTiledFn fn = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return (EncodeTiledFn)ptr;
+  }();
+  return fn;
+}
+bool encode_pages(CUtensorMap *tm, const void *base, int n_pages, int kvh, int D) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)kvh, (cuuint64_t)n_pages * kPageRows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)kvh * D * 2};
+  cuuint32_t box[3] = {64, 1, 64};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout {
+  size_t head, items, req, row_req, part_o, part_lse, total;
+  int64_t cap;
+  int max_items;
+};
+// Partial rows: at most one per row and segment plus 256 for every item beyond
+// one per (segment, head, row tile).
+Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
+  Layout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows * (H / KVH) / ROWS + 1;
+  L.max_items = (int)(KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA);
+  L.cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * ROWS;
+  L.head = take(sizeof(Head));
+  L.items = take(sizeof(Item) * L.max_items);
+  L.req = take(sizeof(Request) * B);
+  L.row_req = take(4 * (size_t)total_rows);
+  L.part_lse = take(4 * L.cap);
+  L.part_o = take(4 * L.cap * D);
+  L.total = o;
+  return L;
+}
+
+template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, cudaStream_t s) {
+  const Layout L = layout(a.rows.B, a.rows.total_rows, a.H, a.KVH, D, a.rows.prefix_len);
+  char *ws = (char *)workspace;
+  Params p;
+  memset(&p, 0, sizeof(p));
+  if (!encode_pages(&p.tmK, a.k_pages, a.rows.n_pages, a.KVH, D) ||
+      !encode_pages(&p.tmV, a.v_pages, a.rows.n_pages, a.KVH, D))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  p.a = a;
+  p.head = (Head *)(ws + L.head);
+  p.items = (Item *)(ws + L.items);
+  p.req = (Request *)(ws + L.req);
+  p.row_req = (int *)(ws + L.row_req);
+  p.part_o = (float *)(ws + L.part_o);
+  p.part_lse = (float *)(ws + L.part_lse);
+  p.cap = (int)L.cap;
+  p.max_items = L.max_items;
+  p.sms = sms > 0 ? sms : 1;
+  p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
+  p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
+  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, p);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attention_kernel<D>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = (int64_t)a.rows.total_rows * a.H;
+  const int grid = (int)std::min<int64_t>((warps + 7) / 8, 8LL * p.sms);
+  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(256), 0, s, p);
+}
+template <int D> cudaError_t prepare() {
+  return cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<D>::SMEM);
+}
+
+}  // namespace
+
+size_t paged_attention_tc_workspace(int B, int total_rows, int H, int KVH, int D, int prefix) {
+  return layout(B, total_rows, H, KVH, D, prefix).total;
+}
+
+cudaError_t launch_paged_attention_tc(const PagedAttnParams &p, void *workspace, cudaStream_t s) {
+  return p.D == 64 ? launch<64>(p, workspace, s) : launch<128>(p, workspace, s);
+}
+
+cudaError_t prepare_paged_attention_tc() {
+  const cudaError_t e = prepare<64>();
+  return e == cudaSuccess ? prepare<128>() : e;
+}
+
+}  // namespace dflash

@@ -44,8 +44,8 @@ int check_layer(const dflash_layer_kv *kv, int32_t batch, int32_t total_rows) {
   if (kv->prefix_len > 0 && !kv->prefix_pages) return fail(DFLASH_EINVAL, "prefix_pages is NULL");
   if (batch < 0 || total_rows < 0) return fail(DFLASH_EINVAL, "negative batch or total_rows");
   if (batch > 1024) return fail(DFLASH_ECAPACITY, "batch > 1024");
-  if ((int64_t)total_rows * kv->n_heads > (1 << 30))
-    return fail(DFLASH_ECAPACITY, "total_rows * n_heads > 2^30");
+  if ((int64_t)total_rows * kv->n_heads > (1 << 28))
+    return fail(DFLASH_ECAPACITY, "total_rows * n_heads > 2^28");
   return DFLASH_OK;
 }
 
@@ -206,7 +206,10 @@ int dflash_paged_attention_workspace_size(const dflash_layer_kv *kv, int32_t bat
                                           int32_t total_rows, size_t *bytes) {
   if (!bytes) return fail(DFLASH_EINVAL, "bytes is NULL");
   if (int st = check_layer(kv, batch, total_rows)) return st;
-  *bytes = 256;
+  *bytes = kv->dtype == DFLASH_BF16
+               ? paged_attention_tc_workspace(batch, total_rows, kv->n_heads, kv->n_kv_heads,
+                                              kv->head_dim, kv->prefix_len)
+               : 256;
   return DFLASH_OK;
 }
 
@@ -249,7 +252,8 @@ int dflash_paged_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t 
   cudaStream_t s = (cudaStream_t)stream;
   const int idx = handle_timed_begin(h, "paged_attention", s);
   return handle_timed_end(h, idx, "paged_attention", s,
-                          launch_paged_attention_simt(kv->dtype, p, s));
+                          kv->dtype == DFLASH_BF16 ? launch_paged_attention_tc(p, workspace, s)
+                                                   : launch_paged_attention_simt(p, s));
 }
 
 int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,

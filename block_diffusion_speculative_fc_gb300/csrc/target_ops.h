@@ -51,8 +51,12 @@ struct PagedAttnParams {
   int causal;
   unsigned int *err;
 };
-cudaError_t launch_paged_attention_simt(int dtype, const PagedAttnParams &p, cudaStream_t s);
+cudaError_t launch_paged_attention_simt(const PagedAttnParams &p, cudaStream_t s);   // fp32
 cudaError_t prepare_paged_attention_simt();
+// bf16 on the tensor cores; device scratch of the size below.
+size_t paged_attention_tc_workspace(int B, int total_rows, int H, int KVH, int D, int prefix);
+cudaError_t launch_paged_attention_tc(const PagedAttnParams &p, void *workspace, cudaStream_t s);
+cudaError_t prepare_paged_attention_tc();
 
 struct SampleParams {
   const void *logits;

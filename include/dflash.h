@@ -458,7 +458,9 @@ int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hid
  * kv_len[b], kv_len[b]+1, ...  Rows before row_start[0] and from
  * row_start[batch] on belong to nobody and are never written.  A row_start
  * pair that decreases or leaves [0, total_rows] sets DFLASH_DERR_ROW_RANGE
- * and its request is skipped; so are rows that two requests would own.
+ * and its request is skipped.  No row may belong to two requests:
+ * dflash_append_kv flags such rows and skips them, the outputs that
+ * dflash_paged_attention writes for them are unspecified.
  * ------------------------------------------------------------------------ */
 
 /*
