@@ -11,18 +11,28 @@
 // A row belongs to one thread-block cluster, whose CTAs hold its slices in
 // shared memory: the logits are read from HBM once and the result written
 // once, which bounds the operator (6 or 8 bytes an element); every pass in
-// between runs on shared memory.  Cuts are found without sorting the row: a
-// histogram over a (32 bins per unit, so a bin's weights are alike) gives
-// counts and weights above every bin; the few tokens of the bin that holds
-// the cut are gathered in the cluster's first CTA, sorted, and walked.  A bin
-// with more tokens than that list holds is split by key until it fits (equal
-// logits split by id).
+// between runs on shared memory.
 //
-// Sums that decide a border are whole numbers: a weight is rounded once to a
-// multiple of 2^-28 of its bin's octave (about 2^-28 relative), so they do not
+// Most rows keep few tokens, and those are found without a histogram or a
+// sort of the row.  Every CTA takes the j-th largest of its threads' maxima
+// (j C >= k, so at least k tokens of the row reach the smallest of the C
+// values, L); one pass gathers the tokens >= L in the cluster's first CTA --
+// a few times k -- and adds up the weight of the rest where top-p needs it.
+// That CTA sorts and walks the list; the others have written zeros by then
+// and leave.
+//
+// Rows whose list overflows, or whose nucleus is larger than it, take a
+// histogram over a (32 bins per unit, so a bin's weights are alike) of counts
+// and weights; the tokens of the bin that holds the cut are gathered, sorted
+// and walked, and a bin with more tokens than the list holds is split by key
+// until it fits (equal logits split by id).
+//
+// Sums that decide a border are whole numbers: a weight is rounded once to
+// about 2^-28 relative and sums are exact multiples of 2^-44, so they do not
 // go by the order of atomics, and a border falls where 64-bit arithmetic puts
 // it except within about 1e-9 of a tie.  min-p compares logits with m + T ln
-// min_p formed in 64 bits.
+// min_p formed in 64 bits (by one thread: fp64 runs at 2 lanes a clock here,
+// so everything else stays out of it).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -41,6 +51,8 @@ constexpr int NT = 512;          // threads of a CTA
 constexpr int NB = 1024;         // histogram bins: a = 0 .. 31.97 and one for the rest
 constexpr int PB = NB / NT;      // bins of a thread in a scan
 constexpr int CAP = 1024;        // gathered tokens (two a thread)
+constexpr int MAX_K = 512;       // top-k of the short way
+constexpr int TOP_P_LIST = 192;  // tokens that its list holds at least for top-p alone
 constexpr int MAXC = 8;          // CTAs of a cluster
 constexpr int MAX_SMEM = 220 * 1024;
 
@@ -49,25 +61,32 @@ struct Tables {
   float f[32];                   // 2^28 2^(-i/32)
 };
 
+typedef unsigned long long u64;
+
 struct Fixed {
-  unsigned long long list[CAP];
-  uint32_t cnt[NB], lo[NB], hi[NB];   // tokens, and weight as a 64-bit sum
-  double warp_m[NT / 32];
+  u64 list[CAP];
+  union {
+    struct {
+      uint32_t cnt[NB], lo[NB], hi[NB];   // tokens, and weight as a 64-bit sum
+    };
+    u64 sorted[CAP];
+  };
+  u64 warp_m[NT / 32];
   int warp_c[NT / 32];
   float fred[NT / 32];
-  unsigned long long kred[NT / 32];
+  u64 kred[NT / 32];
+  float x_min;                   // min-p: the smallest logit kept
   // exchanged between the CTAs of the cluster, one slot per rank
-  float x_max[MAXC];
-  unsigned long long x_arg[MAXC], x_race[MAXC];
-  double x_sum[MAXC];
-  float pruned;                  // weight this CTA left out of the histogram
+  float x_max[MAXC], x_low[MAXC], x_sum[MAXC];
+  int x_n[MAXC];
+  u64 x_rest[MAXC], x_listed[MAXC], x_race[MAXC];
+  int n_list;
   // the leader's command to every CTA
   int cmd, bin, sh;
-  unsigned long long range_lo, range_hi, cut;
-  int n_list;
+  u64 range_lo, range_hi, cut;
   // leader: the bin that holds a cut
   int sel_bin, sel_n, sel_above;
-  double sel_above_m, sel_through;
+  u64 sel_above_m, target;
 };
 
 enum { CMD_GATHER = 0, CMD_SPLIT = 1, CMD_DONE = 2 };
@@ -119,8 +138,16 @@ struct Weigher {
     u = t.u[bin & 31] + __float2int_rn(__fmul_rn(t.f[bin & 31], q));
   }
 };
-__device__ __forceinline__ double octave_scale(int bin) {   // 2^-(28 + octave)
-  return __longlong_as_double((long long)(1023 - 28 - (bin >> 5)) << 52);
+// A sum of weights of one octave in units of 2^-44.
+__device__ __forceinline__ u64 units(u64 sum, int bin) {
+  const int octave = bin >> 5;
+  return octave <= 16 ? sum << (16 - octave) : sum >> (octave - 16);
+}
+// p of a sum, rounded up: "below" it as whole numbers is below p of it.
+__device__ __forceinline__ u64 share_of(u64 total, float p) {
+  if (!(p > 0.f)) return 1;
+  const double t = ceil((double)p * (double)total);
+  return t < 1.0 ? 1 : (u64)t;
 }
 
 template <typename T> struct Elem;
@@ -147,7 +174,7 @@ template <> struct Elem<float> {
   static __device__ __forceinline__ float largest() { return FLT_MAX; }
 };
 
-__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k) {
+__device__ __forceinline__ u64 warp_max_key(u64 k) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const unsigned long long other = __shfl_xor_sync(0xffffffffu, k, o);
@@ -156,15 +183,15 @@ __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k)
   return k;
 }
 
-// Exclusive scan over the CTA of a thread's (count, mass); returns the totals.
-__device__ void block_scan(Fixed &f, int &c, double &m, int &total_c, double &total_m) {
+// Exclusive scan over the CTA of a thread's (count, weight); returns the totals.
+__device__ void block_scan(Fixed &f, int &c, u64 &m, int &total_c, u64 &total_m) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = c;
-  const double m0 = m;
+  const u64 m0 = m;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int oc = __shfl_up_sync(0xffffffffu, c, o);
-    const double om = __shfl_up_sync(0xffffffffu, m, o);
+    const u64 om = __shfl_up_sync(0xffffffffu, m, o);
     if (lane >= o) {
       c += oc;
       m += om;
@@ -176,20 +203,42 @@ __device__ void block_scan(Fixed &f, int &c, double &m, int &total_c, double &to
     f.warp_m[warp] = m;
   }
   __syncthreads();
-  int bc = 0;
-  double bm = 0;
-  total_c = 0;
-  total_m = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w == warp) {
-      bc = total_c;
-      bm = total_m;
+  int wc = lane < NT / 32 ? f.warp_c[lane] : 0;
+  u64 wm = lane < NT / 32 ? f.warp_m[lane] : 0;
+  const int own_c = wc;
+  const u64 own_m = wm;
+#pragma unroll
+  for (int o = 1; o < NT / 32; o <<= 1) {
+    const int oc = __shfl_up_sync(0xffffffffu, wc, o);
+    const u64 om = __shfl_up_sync(0xffffffffu, wm, o);
+    if (lane >= o) {
+      wc += oc;
+      wm += om;
     }
-    total_c += f.warp_c[w];
-    total_m += f.warp_m[w];
   }
-  c = bc + c - c0;
-  m = bm + (m - m0);
+  total_c = __shfl_sync(0xffffffffu, wc, NT / 32 - 1);
+  total_m = __shfl_sync(0xffffffffu, wm, NT / 32 - 1);
+  c = __shfl_sync(0xffffffffu, wc - own_c, warp) + c - c0;
+  m = __shfl_sync(0xffffffffu, wm - own_m, warp) + m - m0;
+}
+
+// f.list[0 .. n) in descending order to f.sorted: a key's place is the number
+// of larger ones (n is mostly a few hundred; keys are distinct).
+__device__ void sort_list(Fixed &f, int n) {
+  if (threadIdx.x == 0 && (n & 1)) f.list[n] = 0;   // n < CAP when odd
+  __syncthreads();
+  const ulonglong2 *l2 = reinterpret_cast<const ulonglong2 *>(f.list);
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const u64 k = f.list[i];
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < (n + 1) / 2; ++j) {
+      const ulonglong2 o = l2[j];
+      place += (o.x > k ? 1 : 0) + (o.y > k ? 1 : 0);
+    }
+    f.sorted[place] = k;
+  }
+  __syncthreads();
 }
 
 struct KernelParams {
@@ -198,8 +247,225 @@ struct KernelParams {
   int per;                       // tokens of a slice
 };
 
+// The general cut (the histogram way); every CTA of the cluster calls it.
+template <typename Each>
+__device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const Tables &tab, const Weigher &weigh,
+                                        float temp, int top_k, float top_p, int vocab, u64 cut, unsigned int *err,
+                                        const Each &each) {
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x;
+  const float m = weigh.m;
+  Fixed &lead = *cl.map_shared_rank(&f, 0);
+  auto clear = [&] {
+    for (int i = tid; i < NB; i += NT) f.cnt[i] = f.lo[i] = f.hi[i] = 0;
+    if (tid == 0) f.n_list = 0;
+    __syncthreads();
+  };
+  auto add = [&](int b, uint32_t u) {
+    atomicAdd(&f.cnt[b], 1u);
+    const uint32_t old = atomicAdd(&f.lo[b], u);
+    if (old + u < old) atomicAdd(&f.hi[b], 1u);
+  };
+  __syncthreads();
+  clear();
+  each([&](float x, int) {
+    if (x == -INFINITY) return;
+    int b;
+    uint32_t u;
+    weigh(x, tab, b, u);
+    add(b, u);
+  });
+  cl.sync();
+
+  // The leader keeps its bins' (tokens, weight) above them; the others follow its commands.
+  int n0[PB], above0[PB];
+  u64 above_m0[PB];
+  int stage = 0;               // leader: 0 top-k, 1 top-p
+  int bin = 0, above = 0;      // leader: the current range and what lies above it
+  u64 above_m = 0, target = 0; // leader: the weight that the cut's predecessors stay below
+  u64 lo = 0, hi = 0;
+  // bins tid * PB ..: sums over the cluster (of: the bin whose octave they have, -1: their own)
+  auto totals = [&](int *nn, u64 *mm, int of) {
+    for (int i = 0; i < PB; ++i) {
+      const int b = tid * PB + i;
+      nn[i] = 0;
+      u64 s = 0;
+      for (int r = 0; r < C; ++r) {
+        const Fixed &o = *cl.map_shared_rank(&f, r);
+        nn[i] += (int)o.cnt[b];
+        s += ((u64)o.hi[b] << 32) + o.lo[b];
+      }
+      mm[i] = units(s, of < 0 ? b : of);
+    }
+  };
+  auto scan = [&](const int *nn, const u64 *mm, int *ab, u64 *abm, int &tc, u64 &tm) {
+    int c = 0;
+    u64 w = 0;
+    for (int i = 0; i < PB; ++i) {
+      c += nn[i];
+      w += mm[i];
+    }
+    block_scan(f, c, w, tc, tm);
+    for (int i = 0; i < PB; ++i) {
+      ab[i] = c;
+      abm[i] = w;
+      c += nn[i];
+      w += mm[i];
+    }
+  };
+  // the bin that holds the cut, given what lies above every bin
+  auto select = [&](const int *nn, const int *ab, const u64 *abm, int base, u64 base_m) {
+    if (tid == 0) f.sel_bin = -1;
+    __syncthreads();
+    int mine = -1;
+    for (int i = 0; i < PB; ++i)
+      if (nn[i] > 0 && (stage == 0 ? base + ab[i] < top_k : base_m + abm[i] < target)) mine = tid * PB + i;
+    if (mine >= 0) atomicMax(&f.sel_bin, mine);
+    __syncthreads();
+    const int s = f.sel_bin;
+    if (s >= 0 && s / PB == tid) {
+      const int i = s % PB;
+      f.sel_n = nn[i];
+      f.sel_above = base + ab[i];
+      f.sel_above_m = base_m + abm[i];
+    }
+    __syncthreads();
+    above = f.sel_above;
+    above_m = f.sel_above_m;
+    return s;
+  };
+  // thread r of the leader: command to CTA r
+  auto tell = [&](int cmd, int sh) {
+    if (tid < C) {
+      Fixed &o = *cl.map_shared_rank(&f, tid);
+      o.cmd = cmd;
+      o.bin = bin;
+      o.sh = sh;
+      o.range_lo = lo;
+      o.range_hi = hi;
+      o.cut = cut;
+    }
+  };
+  auto tell_range = [&](int count) {
+    int sh = 0;
+    while (((hi - lo - 1) >> sh) >= NB) ++sh;
+    tell(count <= CAP ? CMD_GATHER : CMD_SPLIT, sh);
+  };
+  // start of a stage: the first histogram's bin, and its range of keys (somewhat wider than it)
+  auto begin = [&] {
+    bin = select(n0, above0, above_m0, 0, 0);
+    float x_hi = FLT_MAX, x_lo = -FLT_MAX;
+    if (tid < C) {
+      const double inv = (double)temp * 0.6931471805599453 / 32.0;
+      x_hi = __double2float_ru(fmax((double)m - fmax(0.0, (bin - 0.51) * inv), -(double)FLT_MAX));
+      if (bin < NB - 1) x_lo = __double2float_rd(fmax((double)m - (bin + 0.51) * inv, -(double)FLT_MAX));
+    }
+    x_hi = __shfl_sync(0xffffffffu, x_hi, 0);
+    x_lo = __shfl_sync(0xffffffffu, x_lo, 0);
+    if (tid == 0) {
+      f.range_lo = (u64)order_image(x_lo) << 32;
+      f.range_hi = ((u64)order_image(x_hi) + 1) << 32;
+    }
+    __syncthreads();
+    lo = f.range_lo;
+    hi = f.range_hi;
+    __syncthreads();
+    tell_range(f.sel_n);
+  };
+  auto set_target = [&](u64 total) {
+    if (tid == 0) f.target = share_of(total, top_p);
+    __syncthreads();
+    target = f.target;
+  };
+  for (int guard = 0;; ++guard) {
+    if (rank == 0) {
+      if (guard == 0) {
+        u64 mm[PB], total_m;
+        int total;
+        totals(n0, mm, -1);
+        scan(n0, mm, above0, above_m0, total, total_m);
+        stage = top_k > 0 && top_k < total ? 0 : 1;
+        set_target(total_m);
+        if (stage == 1 && !(top_p < 1.f)) tell(CMD_DONE, 0);
+        else begin();
+      } else if (f.cmd == CMD_SPLIT) {
+        int nn[PB], ab[PB], tc;
+        u64 mm[PB], abm[PB], tm;
+        totals(nn, mm, bin);
+        scan(nn, mm, ab, abm, tc, tm);
+        const int s = select(nn, ab, abm, above, above_m);
+        const int sh = f.sh;
+        const u64 v = (u64)(NB - 1 - s);
+        const u64 l = lo + (v << sh), h = l + (1ull << sh);
+        lo = l;
+        hi = h < hi ? h : hi;
+        __syncthreads();   // sh has been read
+        tell_range(f.sel_n);
+      } else {
+        // the gathered tokens: sort, then walk to the cut
+        const int cnt = min(f.n_list, CAP);
+        sort_list(f, cnt);
+        int nn[2], ab[2], tc;
+        u64 mm[2], abm[2], tm;
+        static_assert(CAP == 2 * NT && PB == 2, "two tokens and two bins a thread");
+        for (int i = 0; i < 2; ++i) {
+          const int at = 2 * tid + i;
+          nn[i] = at < cnt ? 1 : 0;
+          mm[i] = 0;
+          if (at < cnt) {
+            int b;
+            uint32_t u;
+            weigh(order_value((uint32_t)(f.sorted[at] >> 32)), tab, b, u);
+            mm[i] = units(u, bin);
+          }
+        }
+        scan(nn, mm, ab, abm, tc, tm);
+        const int s = select(nn, ab, abm, above, above_m);   // the cut's place in the list
+        cut = f.sorted[s];
+        if (stage == 0 && top_p < 1.f) {
+          if (s / 2 == tid) f.range_lo = above_m + mm[s % 2];   // weight through the cut
+          __syncthreads();
+          const u64 through = f.range_lo;
+          __syncthreads();
+          stage = 1;
+          set_target(through);
+          begin();
+        } else {
+          tell(CMD_DONE, 0);
+        }
+      }
+    }
+    cl.sync();
+    const int cmd = f.cmd;
+    if (cmd == CMD_DONE) break;
+    const int want = f.bin, sh = f.sh;
+    const u64 r_lo = f.range_lo, r_hi = f.range_hi;
+    if (guard > 24) {   // 64-bit keys end long before
+      if (rank == 0 && tid == 0) raise_error(err, DFLASH_DERR_TIMEOUT);
+      break;
+    }
+    clear();
+    if (cmd == CMD_GATHER) cl.sync();   // the leader's list is empty before anyone adds to it
+    each([&](float x, int id) {
+      const u64 k = key_of(x, id);
+      if (k < r_lo || k >= r_hi) return;
+      int b;
+      uint32_t u;
+      weigh(x, tab, b, u);
+      if (b != want) return;
+      if (cmd == CMD_GATHER) {
+        const int at = atomicAdd(&lead.n_list, 1);
+        if (at < CAP) lead.list[at] = k;
+      } else {
+        add(NB - 1 - (int)((k - r_lo) >> sh), u);
+      }
+    });
+    cl.sync();
+  }
+  return f.cut;
+}
+
 template <typename T, bool DRAW>
-__global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ KernelParams kp) {
+__global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__ KernelParams kp) {
   constexpr int E = Elem<T>::E;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Tables tab;
@@ -217,16 +483,10 @@ __global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ Ke
   }
 
   const int entry = row / p.rows_per_entry;
-  const float temp = p.temperature ? p.temperature[entry] : 1.f;
-  const int top_k = p.top_k ? p.top_k[entry] : 0;
-  const float top_p = p.top_p ? p.top_p[entry] : 1.f;
-  const float min_p = p.min_p ? p.min_p[entry] : 0.f;
-  if (!(temp >= 0.f) || isinf(temp) || isnan(top_p) || !(min_p <= 1.f)) {
-    if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
-    return;   // the whole cluster
-  }
-  const bool greedy = temp < FLT_MIN;
-  cl.barrier_arrive();   // every CTA of the cluster runs before the first remote access
+  float temp = p.temperature ? p.temperature[entry] : 1.f;
+  int top_k = p.top_k ? p.top_k[entry] : 0;
+  float top_p = p.top_p ? p.top_p[entry] : 1.f;
+  float min_p = p.min_p ? p.min_p[entry] : 0.f;
 
   // ---- the slice, cleaned (NaN to -inf, +inf to the largest finite value), and its maximum
   const int start = min(rank * kp.per, V), n = min(kp.per, V - start);
@@ -278,38 +538,88 @@ __global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ Ke
       }
     }
   }
-  mx = warp_max(mx);
-  if (lane == 0) f.fred[warp] = mx;
+  if (!(temp >= 0.f) || isinf(temp) || isnan(top_p) || !(min_p <= 1.f)) {
+    if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
+    return;   // the whole cluster, before any of its barriers
+  }
+  cl.barrier_arrive();   // every CTA of the cluster runs before the first remote access
+  if (temp < FLT_MIN) {  // the largest logit alone: one token, whatever the weights
+    temp = 1.f;
+    top_k = 1;
+    top_p = 1.f;
+    min_p = 0.f;
+  }
+  if (top_k <= 0 || top_k >= V) top_k = 0;
+  const bool filtered = top_k > 0 || top_p < 1.f;
+  const bool brief = filtered && top_k <= MAX_K;
+  // the j-th largest of the CTA's thread maxima, cut to its upper bits (a lower bound)
+  const int j = brief ? ((top_k > 0 ? top_k : TOP_P_LIST) + C - 1) / C : 0;
+  float low = -INFINITY;
+  if (j > 1) {
+    const uint32_t own = order_image(mx);
+    uint32_t found = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 12; --bit) {
+      const uint32_t want = found | (1u << bit);
+      if (__syncthreads_count(own >= want) >= j) found = want;
+    }
+    low = found >= order_image(-FLT_MAX) ? order_value(found) : -INFINITY;
+  }
+  const float cta_max = warp_max(mx);
+  if (lane == 0) f.fred[warp] = cta_max;
+  if (tid == 0) f.n_list = 0;
   __syncthreads();
-  mx = f.fred[0];
-  for (int w = 1; w < NT / 32; ++w) mx = fmaxf(mx, f.fred[w]);
+  mx = f.fred[lane & (NT / 32 - 1)];
+  mx = warp_max(mx);
   cl.barrier_wait();
-  if (tid < C) cl.map_shared_rank(&f, tid)->x_max[rank] = mx;
+  if (tid < C) {
+    Fixed &o = *cl.map_shared_rank(&f, tid);
+    o.x_max[rank] = mx;
+    o.x_low[rank] = j == 1 ? mx : low;
+  }
   cl.sync();
   float m = f.x_max[0];
-  for (int r = 1; r < C; ++r) m = fmaxf(m, f.x_max[r]);
+  low = f.x_low[0];
+  for (int r = 1; r < C; ++r) {
+    m = fmaxf(m, f.x_max[r]);
+    low = fminf(low, f.x_low[r]);
+  }
+  if (top_k == 1) low = m;
 
   float *out = DRAW ? nullptr : p.probs + (int64_t)row * V + start;
+  const int head = DRAW ? 0 : min(n, (int)((16 - ((uintptr_t)out & 15)) & 15) / 4);
+  const int quads = DRAW ? 0 : (n - head) / 4, done = head + 4 * quads;
+  auto write_zeros = [&] {
+    if (tid < head) out[tid] = 0.f;
+    for (int q = tid; q < quads; q += NT)
+      *reinterpret_cast<float4 *>(out + head + 4 * q) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < n - done) out[done + tid] = 0.f;
+  };
   if (m == -INFINITY) {
-    if (DRAW) {
-      if (rank == 0 && tid == 0) {
+    if (!DRAW) write_zeros();
+    if (rank == 0 && tid == 0) {
+      if (DRAW) {
         p.ids[row] = -1;
         if (p.prob) p.prob[row] = 0.f;
       }
-    } else {
-      for (int i = tid; i < n; i += NT) out[i] = 0.f;
+      raise_error(p.err, DFLASH_DERR_EMPTY_ROW);
     }
-    if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_EMPTY_ROW);
     return;   // the whole cluster, nothing remote in flight
   }
 
   Weigher weigh;
   weigh.m = m;
   {
-    const double c = greedy ? 1.0 : 1.4426950408889634 / (double)temp;
-    weigh.c_hi = (float)c;
-    weigh.c_lo = (float)(c - (double)weigh.c_hi);
+    // log2(e) / T as a pair: quotient, and its remainder over T
+    const float l2e = 1.44269502f, l2e_lo = 1.92596299e-8f;
+    weigh.c_hi = __fdiv_rn(l2e, temp);
+    weigh.c_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-weigh.c_hi, temp, l2e), l2e_lo), temp);
   }
+  const float c = weigh.c_hi;
+  // min-p: w >= min_p is x >= m + T ln min_p
+  if (tid == 0)
+    f.x_min = min_p > 0.f ? __double2float_ru(fmax((double)m + (double)temp * log((double)min_p), -(double)FLT_MAX))
+                          : -FLT_MAX;
   // every token of the slice: fn(x, id); ids before and past the slice hold -inf
   auto each = [&](auto fn) {
     for (int v = tid; v < nv; v += NT) {
@@ -319,263 +629,143 @@ __global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ Ke
       for (int e = 0; e < E; ++e) fn(x[e], start + v * E + e - mis);
     }
   };
+  const float *noise = DRAW ? p.noise + (int64_t)row * V : nullptr;
 
-  unsigned long long cut = (unsigned long long)order_image(-FLT_MAX) << 32;   // every finite logit
-  if (greedy) {
-    unsigned long long best = 0;
-    each([&](float x, int id) {
-      if (x == m) {
-        const unsigned long long k = key_of(x, id);
-        best = k > best ? k : best;
-      }
-    });
-    best = warp_max_key(best);
-    if (lane == 0) f.kred[warp] = best;
-    __syncthreads();
-    if (tid < C) {
-      for (int w = 0; w < NT / 32; ++w) best = f.kred[w] > best ? f.kred[w] : best;
-      cl.map_shared_rank(&f, tid)->x_arg[rank] = best;
-    }
-    cl.sync();
-    for (int r = 0; r < C; ++r) cut = f.x_arg[r] > cut ? f.x_arg[r] : cut;
-  } else if ((top_k > 0 && top_k < V) || top_p < 1.f) {
+  u64 cut = (u64)order_image(-FLT_MAX) << 32;   // every finite logit
+  if (brief) {
+    // ---- the short way: tokens >= low to the leader's list, the weight of the others
     Fixed &lead = *cl.map_shared_rank(&f, 0);
-    // Tokens that cannot be in the nucleus whatever the rest is (V of them
-    // weigh less than half of 1 - p, and the maximum alone weighs 1) add
-    // to the total without the histogram.
-    float far = 3.0e38f;
-    if (!(top_k > 0 && top_k < V))
-      far = log2f((float)V) - log2f(fmaxf(1.f - top_p, 1e-9f)) + 1.f;
-    auto is_far = [&](float x) { return __fmul_rn(__fsub_rn(m, x), weigh.c_hi) > far; };
-    auto clear = [&] {
-      for (int i = tid; i < NB; i += NT) f.cnt[i] = f.lo[i] = f.hi[i] = 0;
-      if (tid == 0) f.n_list = 0;
-      __syncthreads();
-    };
-    auto add = [&](int b, uint32_t u) {
-      atomicAdd(&f.cnt[b], 1u);
-      const uint32_t old = atomicAdd(&f.lo[b], u);
-      if (old + u < old) atomicAdd(&f.hi[b], 1u);
-    };
-    clear();
-    float pruned = 0.f;
-    each([&](float x, int) {
+    const bool weights = top_k == 0;
+    u64 listed = 0, rest = 0;
+    int count = 0;
+    each([&](float x, int id) {
       if (x == -INFINITY) return;
-      if (is_far(x)) {
-        pruned += ex2((x - m) * weigh.c_hi);
-        return;
-      }
-      int b;
-      uint32_t u;
-      weigh(x, tab, b, u);
-      add(b, u);
-    });
-    pruned = warp_sum(pruned);
-    if (lane == 0) f.fred[warp] = pruned;
-    __syncthreads();
-    if (tid == 0) {
-      float s = 0.f;
-      for (int w = 0; w < NT / 32; ++w) s += f.fred[w];
-      f.pruned = s;
-    }
-    cl.sync();
-
-    // The leader keeps its bins' (tokens, weight) above them; the others follow its commands.
-    int n0[PB], above0[PB];
-    double above_m0[PB], total_m = 0;
-    int stage = 0;               // leader: 0 top-k, 1 top-p
-    bool started = false;
-    double target = 0;           // leader: weight that the cut's predecessors stay below
-    int kth = 0;                 // leader: or the cut's place
-    int bin = 0, above = 0;      // leader: the current range and what lies above it
-    double above_m = 0;
-    unsigned long long lo = 0, hi = 0;
-    // bins tid * PB ..: sums over the cluster (scale: of a split bin, else the bin's own)
-    auto totals = [&](int *nn, double *mm, double scale) {
-      for (int i = 0; i < PB; ++i) {
-        const int b = tid * PB + i;
-        nn[i] = 0;
-        unsigned long long s = 0;
-        for (int r = 0; r < C; ++r) {
-          const Fixed &o = *cl.map_shared_rank(&f, r);
-          nn[i] += (int)o.cnt[b];
-          s += ((unsigned long long)o.hi[b] << 32) + o.lo[b];
-        }
-        mm[i] = (double)s * (scale > 0 ? scale : octave_scale(b));
-      }
-    };
-    auto scan = [&](const int *nn, const double *mm, int *ab, double *abm, int &tc, double &tm) {
-      int c = 0;
-      double w = 0;
-      for (int i = 0; i < PB; ++i) {
-        c += nn[i];
-        w += mm[i];
-      }
-      block_scan(f, c, w, tc, tm);
-      for (int i = 0; i < PB; ++i) {
-        ab[i] = c;
-        abm[i] = w;
-        c += nn[i];
-        w += mm[i];
-      }
-    };
-    // the bin that holds the cut, given what lies above every bin
-    auto select = [&](const int *nn, const int *ab, const double *abm, int base, double base_m) {
-      if (tid == 0) f.sel_bin = -1;
-      __syncthreads();
-      int mine = -1;
-      for (int i = 0; i < PB; ++i)
-        if (nn[i] > 0 && (stage == 0 ? base + ab[i] < kth : base_m + abm[i] < target)) mine = tid * PB + i;
-      if (mine >= 0) atomicMax(&f.sel_bin, mine);
-      __syncthreads();
-      const int s = f.sel_bin;
-      if (s >= 0 && s / PB == tid) {
-        const int i = s % PB;
-        f.sel_n = nn[i];
-        f.sel_above = base + ab[i];
-        f.sel_above_m = base_m + abm[i];
-      }
-      __syncthreads();
-      above = f.sel_above;
-      above_m = f.sel_above_m;
-      return s;
-    };
-    // thread r of the leader: command to CTA r
-    auto tell = [&](int cmd, int sh) {
-      if (tid < C) {
-        Fixed &o = *cl.map_shared_rank(&f, tid);
-        o.cmd = cmd;
-        o.bin = bin;
-        o.sh = sh;
-        o.range_lo = lo;
-        o.range_hi = hi;
-        o.cut = cut;
-      }
-    };
-    auto tell_range = [&](int count) {
-      int sh = 0;
-      while (((hi - lo - 1) >> sh) >= NB) ++sh;
-      tell(count <= CAP ? CMD_GATHER : CMD_SPLIT, sh);
-    };
-    // start of a stage: the first histogram's bin, and its range of keys
-    auto begin = [&] {
-      const int s = select(n0, above0, above_m0, 0, 0);
-      bin = s;
-      const double inv = (double)temp * 0.6931471805599453 / 32.0;
-      const double x_hi = (double)m - fmax(0.0, (bin - 0.51) * inv);
-      const double x_lo = bin == NB - 1 ? -(double)FLT_MAX : (double)m - (bin + 0.51) * inv;
-      lo = (unsigned long long)order_image(__double2float_rd(fmax(x_lo, -(double)FLT_MAX))) << 32;
-      hi = ((unsigned long long)order_image(__double2float_ru(fmax(x_hi, -(double)FLT_MAX))) + 1) << 32;
-      tell_range(f.sel_n);
-    };
-    for (int guard = 0;; ++guard) {
-      if (rank == 0) {
-        if (!started) {
-          started = true;
-          double mm[PB];
-          int total;
-          totals(n0, mm, 0);
-          scan(n0, mm, above0, above_m0, total, total_m);
-          for (int r = 0; r < C; ++r) total_m += (double)cl.map_shared_rank(&f, r)->pruned;
-          stage = top_k > 0 && top_k < total ? 0 : 1;
-          kth = top_k;
-          target = fmax((double)top_p * total_m, 1e-300);
-          if (stage == 1 && !(top_p < 1.f)) tell(CMD_DONE, 0);
-          else begin();
-        } else if (f.cmd == CMD_SPLIT) {
-          int nn[PB], ab[PB], tc;
-          double mm[PB], abm[PB], tm;
-          totals(nn, mm, octave_scale(bin));
-          scan(nn, mm, ab, abm, tc, tm);
-          const int s = select(nn, ab, abm, above, above_m);
-          const int sh = f.sh;
-          const unsigned long long v = (unsigned long long)(NB - 1 - s);
-          const unsigned long long l = lo + (v << sh), h = l + (1ull << sh);
-          lo = l;
-          hi = h < hi ? h : hi;
-          __syncthreads();   // sh has been read
-          tell_range(f.sel_n);
-        } else {
-          // the gathered tokens: sort, then walk to the cut
-          const int cnt = min(f.n_list, CAP);
-          int size = 2;
-          while (size < cnt) size <<= 1;
-          for (int i = cnt + tid; i < size; i += NT) f.list[i] = 0;
-          __syncthreads();
-          for (int k = 2; k <= size; k <<= 1)
-            for (int j = k >> 1; j > 0; j >>= 1) {
-              for (int i = tid; i < size / 2; i += NT) {
-                const int a = 2 * i - (i & (j - 1)), b = a + j;   // pair (a, a + j)
-                const unsigned long long x = f.list[a], y = f.list[b];
-                const bool down = (a & k) == 0;
-                if ((x < y) == down) {
-                  f.list[a] = y;
-                  f.list[b] = x;
-                }
-              }
-              __syncthreads();
-            }
-          int nn[2], ab[2], tc;
-          double mm[2], abm[2], tm;
-          static_assert(CAP == 2 * NT && PB == 2, "two tokens and two bins a thread");
-          for (int i = 0; i < 2; ++i) {
-            const int at = 2 * tid + i;
-            nn[i] = at < cnt ? 1 : 0;
-            mm[i] = 0;
-            if (at < cnt) {
-              int b;
-              uint32_t u;
-              weigh(order_value((uint32_t)(f.list[at] >> 32)), tab, b, u);
-              mm[i] = (double)u * octave_scale(bin);
-            }
-          }
-          scan(nn, mm, ab, abm, tc, tm);
-          const int s = select(nn, ab, abm, above, above_m);   // the cut's place in the list
-          cut = f.list[s];
-          if (s / 2 == tid) f.sel_through = above_m + mm[s % 2];   // weight through the cut
-          __syncthreads();
-          if (stage == 0 && top_p < 1.f) {
-            stage = 1;
-            target = fmax((double)top_p * f.sel_through, 1e-300);
-            begin();
-          } else {
-            tell(CMD_DONE, 0);
-          }
-        }
-      }
-      cl.sync();
-      const int cmd = f.cmd;
-      if (cmd == CMD_DONE) break;
-      const int want = f.bin, sh = f.sh;
-      const unsigned long long r_lo = f.range_lo, r_hi = f.range_hi;
-      if (guard > 24) {   // 64-bit keys end long before
-        if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_TIMEOUT);
-        break;
-      }
-      clear();
-      if (cmd == CMD_GATHER) cl.sync();   // the leader's list is empty before anyone adds to it
-      each([&](float x, int id) {
-        const unsigned long long k = key_of(x, id);
-        if (k < r_lo || k >= r_hi || is_far(x)) return;
+      u64 w = 0;
+      if (weights) {
         int b;
         uint32_t u;
         weigh(x, tab, b, u);
-        if (b != want) return;
-        if (cmd == CMD_GATHER) {
-          const int at = atomicAdd(&lead.n_list, 1);
-          if (at < CAP) lead.list[at] = k;
-        } else {
-          add(NB - 1 - (int)((k - r_lo) >> sh), u);
-        }
-      });
-      cl.sync();
+        w = units(u, b);
+      }
+      if (x >= low) {
+        listed += w;
+        ++count;
+        const int at = atomicAdd(&lead.n_list, 1);
+        if (at < CAP) lead.list[at] = key_of(x, id);
+      } else {
+        rest += w;
+      }
+    });
+    if (!DRAW) write_zeros();
+    int c0 = count, total_n;
+    u64 sum = rest, total_rest, total_listed = 0;
+    block_scan(f, c0, sum, total_n, total_rest);
+    if (weights) {
+      int zero = 0, none;
+      sum = listed;
+      block_scan(f, zero, sum, none, total_listed);
     }
-    cut = f.cut;
+    if (tid < C) {
+      Fixed &o = *cl.map_shared_rank(&f, tid);
+      o.x_n[rank] = total_n;
+      o.x_rest[rank] = total_rest;
+      o.x_listed[rank] = total_listed;
+    }
+    cl.sync();   // zeros and list are in place
+    int all = 0;
+    u64 all_rest = 0, all_listed = 0;
+    for (int r = 0; r < C; ++r) {
+      all += f.x_n[r];
+      all_rest += f.x_rest[r];
+      all_listed += f.x_listed[r];
+    }
+    // with top-k the list holds the k largest (or every finite logit); for top-p alone the
+    // nucleus is inside when the list's weight reaches p of the total
+    bool inside = all <= CAP;
+    if (inside && weights) {
+      if (tid == 0) f.target = share_of(all_rest + all_listed, top_p);
+      __syncthreads();
+      inside = all_listed >= f.target || all_rest == 0;
+    }
+    if (inside) {
+      if (rank != 0) return;
+      sort_list(f, all);
+      const int kk = top_k > 0 ? min(top_k, all) : all;
+      u64 w[2], sum2 = 0, total;
+      float x[2];
+      for (int i = 0; i < 2; ++i) {
+        const int at = 2 * tid + i;
+        w[i] = 0;
+        x[i] = -INFINITY;
+        if (at < kk) {
+          x[i] = order_value((uint32_t)(f.sorted[at] >> 32));
+          int b;
+          uint32_t u;
+          weigh(x[i], tab, b, u);
+          w[i] = units(u, b);
+        }
+        sum2 += w[i];
+      }
+      int zero = 0, none;
+      u64 before = sum2;
+      block_scan(f, zero, before, none, total);
+      u64 target = ~0ull;
+      if (top_p < 1.f) {
+        if (tid == 0) f.target = share_of(total + (weights ? all_rest : 0), top_p);
+        __syncthreads();
+        target = f.target;
+      }
+      const float x_min = f.x_min;
+      bool keep[2];
+      float e[2], sum_f = 0.f;
+      for (int i = 0; i < 2; ++i) {
+        const int at = 2 * tid + i;
+        keep[i] = at < kk && (before < target || at == 0) && x[i] >= x_min;
+        before += w[i];
+        e[i] = keep[i] ? ex2((x[i] - m) * c) : 0.f;
+        sum_f += e[i];
+      }
+      u64 best = 0;
+      int ids[2];
+      for (int i = 0; i < 2; ++i) {
+        ids[i] = keep[i] ? (int)~(uint32_t)f.sorted[2 * tid + i] : 0;
+        if (DRAW && keep[i]) {
+          const u64 k = argmax_key(e[i] / noise[ids[i]], ids[i]);
+          best = k > best ? k : best;
+        }
+      }
+      sum_f = warp_sum(sum_f);
+      if (DRAW) best = warp_max_key(best);
+      if (lane == 0) {
+        f.fred[warp] = sum_f;
+        f.kred[warp] = best;
+      }
+      __syncthreads();
+      const float inv = 1.f / warp_sum(lane < NT / 32 ? f.fred[lane] : 0.f);
+      if (!DRAW) {
+        for (int i = 0; i < 2; ++i)
+          if (keep[i]) p.probs[(int64_t)row * V + ids[i]] = e[i] * inv;
+      } else if (warp == 0) {
+        best = warp_max_key(f.kred[lane & (NT / 32 - 1)]);
+        if (lane == 0) {
+          const int id = argmax_key_index(best);
+          p.ids[row] = id;
+          if (p.prob) {
+            const float xd = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
+            p.prob[row] = ex2((fminf(xd, Elem<T>::largest()) - m) * c) * inv;
+          }
+        }
+      }
+      return;
+    }
   }
-  if (!greedy && min_p > 0.f) {
-    const double x = (double)m + (double)temp * log((double)min_p);
-    const unsigned long long k =
-        (unsigned long long)order_image(__double2float_ru(fmax(x, -(double)FLT_MAX))) << 32;
+  if (filtered) {
+    cl.sync();   // the list and the exchange slots of the short way have been read
+    cut = general_cut(cl, f, tab, weigh, temp, top_k, top_p, V, cut, p.err, each);
+  }
+  __syncthreads();   // x_min
+  {
+    const u64 k = (u64)order_image(f.x_min) << 32;
     cut = k > cut ? k : cut;
   }
 
@@ -584,15 +774,14 @@ __global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ Ke
   const uint32_t idc = ~(uint32_t)cut;
   auto kept = [&](float x, int id) { return x > xc || (x == xc && (uint32_t)id <= idc); };
   float s0 = 0.f, s1 = 0.f;
-  unsigned long long best = 0;
-  const float *noise = DRAW ? p.noise + (int64_t)row * V : nullptr;
+  u64 best = 0;
   each([&](float x, int id) {
     if (!kept(x, id)) return;
-    const float w = ex2((x - m) * weigh.c_hi);
+    const float w = ex2((x - m) * c);
     if (id & 1) s1 += w;
     else s0 += w;
     if (DRAW) {
-      const unsigned long long k = argmax_key(w / noise[id], id);
+      const u64 k = argmax_key(w / noise[id], id);
       best = k > best ? k : best;
     }
   });
@@ -604,47 +793,61 @@ __global__ void __launch_bounds__(NT) sampling_kernel(const __grid_constant__ Ke
     if (DRAW) f.kred[warp] = best;
   }
   __syncthreads();
-  if (tid < C) {
-    double s = 0;
-    for (int w = 0; w < NT / 32; ++w) s += (double)f.fred[w];
-    Fixed &o = *cl.map_shared_rank(&f, tid);
-    o.x_sum[rank] = s;
-    if (DRAW) {
-      for (int w = 0; w < NT / 32; ++w) best = f.kred[w] > best ? f.kred[w] : best;
-      o.x_race[rank] = best;
+  if (tid < 32) {
+    const float s = warp_sum(lane < NT / 32 ? f.fred[lane] : 0.f);
+    if (DRAW) best = warp_max_key(f.kred[lane & (NT / 32 - 1)]);
+    if (tid < C) {
+      Fixed &o = *cl.map_shared_rank(&f, tid);
+      o.x_sum[rank] = s;
+      if (DRAW) o.x_race[rank] = best;
     }
   }
   cl.sync();   // the last exchange: nothing remote after it
-  double total = 0;
+  float total = 0;
   for (int r = 0; r < C; ++r) total += f.x_sum[r];
-  const float inv = (float)(1.0 / total);
+  const float inv = 1.f / total;
   if (DRAW) {
     if (rank == 0 && tid == 0) {
+      best = 0;
       for (int r = 0; r < C; ++r) best = f.x_race[r] > best ? f.x_race[r] : best;
       const int id = argmax_key_index(best);
       p.ids[row] = id;
       if (p.prob) {
         float x = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
         x = fminf(x, Elem<T>::largest());
-        p.prob[row] = ex2((x - m) * weigh.c_hi) * inv;
+        p.prob[row] = ex2((x - m) * c) * inv;
       }
     }
     return;
   }
   // ---- probabilities: 16-byte stores from the row's first aligned element
-  auto prob_at = [&](int i) {
-    const float x = to_f32(slice[mis + i]);
-    return kept(x, start + i) ? ex2((x - m) * weigh.c_hi) * inv : 0.f;
-  };
-  const int head = min(n, (int)((16 - ((uintptr_t)out & 15)) & 15) / 4);
-  const int quads = (n - head) / 4;
+  auto prob_of = [&](float x, int id) { return kept(x, id) ? ex2((x - m) * c) * inv : 0.f; };
+  auto prob_at = [&](int i) { return prob_of(to_f32(slice[mis + i]), start + i); };
   if (tid < head) out[tid] = prob_at(tid);
-  for (int q = tid; q < quads; q += NT) {
-    const int i = head + 4 * q;
-    *reinterpret_cast<float4 *>(out + i) =
-        make_float4(prob_at(i), prob_at(i + 1), prob_at(i + 2), prob_at(i + 3));
+  if ((mis + head) % 4 == 0) {
+    for (int q = tid; q < quads; q += NT) {
+      const int i = head + 4 * q, id = start + i;
+      float x[4];
+      if constexpr (sizeof(T) == 2) {
+        const uint2 t = *reinterpret_cast<const uint2 *>(slice + mis + i);
+        x[0] = __uint_as_float(t.x << 16);
+        x[1] = __uint_as_float(t.x & 0xffff0000u);
+        x[2] = __uint_as_float(t.y << 16);
+        x[3] = __uint_as_float(t.y & 0xffff0000u);
+      } else {
+        const float4 t = *reinterpret_cast<const float4 *>(slice + mis + i);
+        x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+      }
+      *reinterpret_cast<float4 *>(out + i) =
+          make_float4(prob_of(x[0], id), prob_of(x[1], id + 1), prob_of(x[2], id + 2), prob_of(x[3], id + 3));
+    }
+  } else {
+    for (int q = tid; q < quads; q += NT) {
+      const int i = head + 4 * q;
+      *reinterpret_cast<float4 *>(out + i) =
+          make_float4(prob_at(i), prob_at(i + 1), prob_at(i + 2), prob_at(i + 3));
+    }
   }
-  const int done = head + 4 * quads;
   if (tid < n - done) out[done + tid] = prob_at(done + tid);
 }
 
