@@ -18,8 +18,8 @@
 // (j C >= k, so at least k tokens of the row reach the smallest of the C
 // values, L); one pass gathers the tokens >= L in the cluster's first CTA --
 // a few times k -- and adds up the weight of the rest where top-p needs it.
-// That CTA sorts and walks the list; the others have written zeros by then
-// and leave.
+// That CTA sorts and walks the list while the others write zeros; then every
+// CTA writes its kept tokens over them.
 //
 // Rows whose list overflows, or whose nucleus is larger than it, take a
 // histogram over a (32 bins per unit, so a bin's weights are alike) of counts
@@ -29,8 +29,10 @@
 //
 // Sums that decide a border are whole numbers: a weight is rounded once to
 // about 2^-28 relative and sums are exact multiples of 2^-44, so they do not
-// go by the order of atomics, and a border falls where 64-bit arithmetic puts
-// it except within about 1e-9 of a tie.  min-p compares logits with m + T ln
+// go by the order of atomics (the weight of the tokens outside a list, which
+// lie beyond the border, comes from the hardware's exponential, good to
+// 2^-22).  A border falls where 64-bit arithmetic puts it except within about
+// 1e-9 of the total plus 2^-22 of the weight outside the list.  min-p compares logits with m + T ln
 // min_p formed in 64 bits (by one thread: fp64 runs at 2 lanes a clock here,
 // so everything else stays out of it).
 #include <cooperative_groups.h>
@@ -138,6 +140,17 @@ struct Weigher {
     u = t.u[bin & 31] + __float2int_rn(__fmul_rn(t.f[bin & 31], q));
   }
 };
+// 2^-a of a token outside the list: a split into its nearest whole number and
+// a rest formed with one rounding, so that only the error of the hardware's
+// exponential (2^-22) is left.
+__device__ __forceinline__ float rest_weight(const Weigher &g, float x) {
+  const float d = __fsub_rn(g.m, x);
+  const float a = fminf(__fmul_rn(d, g.c_hi), 120.f);   // below 2^-120: nothing in units of 2^-44
+  const float big = __fadd_rn(a, 12582912.f);
+  const float r = __fmaf_rn(d, g.c_lo, __fmaf_rn(d, g.c_hi, __fsub_rn(12582912.f, big)));
+  const float w = __uint_as_float(__float_as_uint(ex2(-r)) - (__float_as_uint(big) << 23));
+  return a < 120.f ? w : 0.f;
+}
 // A sum of weights of one octave in units of 2^-44.
 __device__ __forceinline__ u64 units(u64 sum, int bin) {
   const int octave = bin >> 5;
@@ -148,6 +161,10 @@ __device__ __forceinline__ u64 share_of(u64 total, float p) {
   if (!(p > 0.f)) return 1;
   const double t = ceil((double)p * (double)total);
   return t < 1.0 ? 1 : (u64)t;
+}
+
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 template <typename T> struct Elem;
@@ -497,7 +514,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   float mx = -INFINITY;
   {
     const uint4 *gv = reinterpret_cast<const uint4 *>(src - mis);
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int v0 = tid; v0 < nv; v0 += U * NT) {
       uint4 t[U];
 #pragma unroll
@@ -638,28 +655,32 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     const bool weights = top_k == 0;
     u64 listed = 0, rest = 0;
     int count = 0;
-    each([&](float x, int id) {
-      if (x == -INFINITY) return;
-      u64 w = 0;
+    float part[2] = {0.f, 0.f};
+    auto list_token = [&](float x, int id) {
+      ++count;
       if (weights) {
         int b;
         uint32_t u;
         weigh(x, tab, b, u);
-        w = units(u, b);
+        listed += units(u, b);
       }
-      if (x >= low) {
-        listed += w;
-        ++count;
-        const int at = atomicAdd(&lead.n_list, 1);
-        if (at < CAP) lead.list[at] = key_of(x, id);
-      } else {
-        rest += w;
-      }
-    });
-    if (!DRAW) write_zeros();
-    int c0 = count, total_n;
+      const int at = atomicAdd(&lead.n_list, 1);
+      if (at < CAP) lead.list[at] = key_of(x, id);
+    };
+    if (weights) {
+      each([&](float x, int id) {
+        if (x >= low && x > -INFINITY) list_token(x, id);
+        else part[id & 1] += rest_weight(weigh, x);
+      });
+      rest = (u64)((part[0] + part[1]) * 0x1p44f);
+    } else {
+      each([&](float x, int id) {
+        if (x >= low && x > -INFINITY) list_token(x, id);
+      });
+    }
+    int total_n;
     u64 sum = rest, total_rest, total_listed = 0;
-    block_scan(f, c0, sum, total_n, total_rest);
+    block_scan(f, count, sum, total_n, total_rest);
     if (weights) {
       int zero = 0, none;
       sum = listed;
@@ -671,7 +692,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       o.x_rest[rank] = total_rest;
       o.x_listed[rank] = total_listed;
     }
-    cl.sync();   // zeros and list are in place
+    cl.sync();   // the list is complete
     int all = 0;
     u64 all_rest = 0, all_listed = 0;
     for (int r = 0; r < C; ++r) {
@@ -688,73 +709,93 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       inside = all_listed >= f.target || all_rest == 0;
     }
     if (inside) {
-      if (rank != 0) return;
-      sort_list(f, all);
-      const int kk = top_k > 0 ? min(top_k, all) : all;
-      u64 w[2], sum2 = 0, total;
-      float x[2];
-      for (int i = 0; i < 2; ++i) {
-        const int at = 2 * tid + i;
-        w[i] = 0;
-        x[i] = -INFINITY;
-        if (at < kk) {
-          x[i] = order_value((uint32_t)(f.sorted[at] >> 32));
-          int b;
-          uint32_t u;
-          weigh(x[i], tab, b, u);
-          w[i] = units(u, b);
+      if (rank != 0) {
+        if (DRAW) return;
+        // zeros meanwhile; this arrival passes nothing on, so it does not wait for them
+        cluster_arrive_relaxed();
+        write_zeros();
+      } else {
+        sort_list(f, all);
+        const int kk = top_k > 0 ? min(top_k, all) : all;
+        u64 w[2], sum2 = 0, total;
+        float x[2];
+        for (int i = 0; i < 2; ++i) {
+          const int at = 2 * tid + i;
+          w[i] = 0;
+          x[i] = -INFINITY;
+          if (at < kk) {
+            x[i] = order_value((uint32_t)(f.sorted[at] >> 32));
+            int b;
+            uint32_t u;
+            weigh(x[i], tab, b, u);
+            w[i] = units(u, b);
+          }
+          sum2 += w[i];
         }
-        sum2 += w[i];
-      }
-      int zero = 0, none;
-      u64 before = sum2;
-      block_scan(f, zero, before, none, total);
-      u64 target = ~0ull;
-      if (top_p < 1.f) {
-        if (tid == 0) f.target = share_of(total + (weights ? all_rest : 0), top_p);
-        __syncthreads();
-        target = f.target;
-      }
-      const float x_min = f.x_min;
-      bool keep[2];
-      float e[2], sum_f = 0.f;
-      for (int i = 0; i < 2; ++i) {
-        const int at = 2 * tid + i;
-        keep[i] = at < kk && (before < target || at == 0) && x[i] >= x_min;
-        before += w[i];
-        e[i] = keep[i] ? ex2((x[i] - m) * c) : 0.f;
-        sum_f += e[i];
-      }
-      u64 best = 0;
-      int ids[2];
-      for (int i = 0; i < 2; ++i) {
-        ids[i] = keep[i] ? (int)~(uint32_t)f.sorted[2 * tid + i] : 0;
-        if (DRAW && keep[i]) {
-          const u64 k = argmax_key(e[i] / noise[ids[i]], ids[i]);
-          best = k > best ? k : best;
+        u64 target = ~0ull, before = 0;
+        if (top_p < 1.f) {
+          int zero = 0, none;
+          before = sum2;
+          block_scan(f, zero, before, none, total);
+          if (tid == 0) f.target = share_of(total + (weights ? all_rest : 0), top_p);
+          __syncthreads();
+          target = f.target;
         }
-      }
-      sum_f = warp_sum(sum_f);
-      if (DRAW) best = warp_max_key(best);
-      if (lane == 0) {
-        f.fred[warp] = sum_f;
-        f.kred[warp] = best;
-      }
-      __syncthreads();
-      const float inv = 1.f / warp_sum(lane < NT / 32 ? f.fred[lane] : 0.f);
-      if (!DRAW) {
-        for (int i = 0; i < 2; ++i)
-          if (keep[i]) p.probs[(int64_t)row * V + ids[i]] = e[i] * inv;
-      } else if (warp == 0) {
-        best = warp_max_key(f.kred[lane & (NT / 32 - 1)]);
-        if (lane == 0) {
-          const int id = argmax_key_index(best);
-          p.ids[row] = id;
-          if (p.prob) {
-            const float xd = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
-            p.prob[row] = ex2((fminf(xd, Elem<T>::largest()) - m) * c) * inv;
+        const float x_min = f.x_min;
+        bool keep[2];
+        float e[2], sum_f = 0.f;
+        int ids[2];
+        u64 best = 0;
+        for (int i = 0; i < 2; ++i) {
+          const int at = 2 * tid + i;
+          keep[i] = at < kk && (before < target || at == 0) && x[i] >= x_min;
+          before += w[i];
+          e[i] = keep[i] ? ex2((x[i] - m) * c) : 0.f;
+          sum_f += e[i];
+          ids[i] = keep[i] ? (int)~(uint32_t)f.sorted[at] : 0;
+          if (DRAW && keep[i]) {
+            const u64 k = argmax_key(e[i] / noise[ids[i]], ids[i]);
+            best = k > best ? k : best;
           }
         }
+        sum_f = warp_sum(sum_f);
+        if (DRAW) best = warp_max_key(best);
+        if (lane == 0) {
+          f.fred[warp] = sum_f;
+          f.kred[warp] = best;
+        }
+        const int n_kept = __syncthreads_count(keep[0]) + __syncthreads_count(keep[1]);
+        const float inv = 1.f / warp_sum(lane < NT / 32 ? f.fred[lane] : 0.f);
+        if (DRAW) {
+          if (warp == 0) {
+            best = warp_max_key(f.kred[lane & (NT / 32 - 1)]);
+            if (lane == 0) {
+              const int id = argmax_key_index(best);
+              p.ids[row] = id;
+              if (p.prob) {
+                const float xd = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
+                p.prob[row] = ex2((fminf(xd, Elem<T>::largest()) - m) * c) * inv;
+              }
+            }
+          }
+          return;
+        }
+        // the kept tokens are a prefix of the sorted list: (probability, id) to every CTA
+        for (int r = 0; r < C; ++r) {
+          Fixed &o = *cl.map_shared_rank(&f, r);
+          for (int i = 0; i < 2; ++i)
+            if (keep[i]) o.list[2 * tid + i] = ((u64)__float_as_uint(e[i] * inv) << 32) | (uint32_t)ids[i];
+          if (tid == 0) o.n_list = n_kept;
+        }
+        cl.barrier_arrive();
+        write_zeros();
+      }
+      cl.barrier_wait();
+      __syncthreads();   // this CTA's zeros come before its tokens
+      for (int i = tid; i < f.n_list; i += NT) {
+        const u64 t = f.list[i];
+        const int id = (int)(uint32_t)t - start;
+        if (id >= 0 && id < n) out[id] = __uint_as_float((uint32_t)(t >> 32));
       }
       return;
     }
