@@ -54,8 +54,9 @@ constexpr int NB = 1024;         // histogram bins: a = 0 .. 31.97 and one for t
 constexpr int PB = NB / NT;      // bins of a thread in a scan
 constexpr int CAP = 1024;        // gathered tokens (two a thread)
 constexpr int MAX_K = 512;       // top-k of the short way
-constexpr int TOP_P_LIST = 192;  // tokens that its list holds at least for top-p alone
+constexpr int TOP_P_LIST = 128;  // tokens that its list holds at least for top-p alone
 constexpr int MAXC = 8;          // CTAs of a cluster
+constexpr int GROUPS = NT / 4;
 constexpr int MAX_SMEM = 220 * 1024;
 
 struct Tables {
@@ -75,6 +76,9 @@ struct Fixed {
   };
   u64 warp_m[NT / 32];
   int warp_c[NT / 32];
+  float group[GROUPS];           // maxima of groups of four threads
+  int own_n;                     // tokens that this CTA lists, their weight and the others'
+  u64 own_rest, own_listed;
   float fred[NT / 32];
   u64 kred[NT / 32];
   float x_min;                   // min-p: the smallest logit kept
@@ -179,6 +183,12 @@ template <> struct Elem<bf16> {
     }
   }
   static __device__ __forceinline__ float largest() { return __uint_as_float(0x7f7f0000u); }
+  // the largest of a vector, NaN if any is
+  static __device__ __forceinline__ float max_of(const uint4 &v) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return __bfloat162float(__hmax_nan(__low2bfloat16(t), __high2bfloat16(t)));
+  }
 };
 template <> struct Elem<float> {
   static constexpr int E = 4;
@@ -189,6 +199,14 @@ template <> struct Elem<float> {
     x[3] = __uint_as_float(v.w);
   }
   static __device__ __forceinline__ float largest() { return FLT_MAX; }
+  static __device__ __forceinline__ float max_of(const uint4 &v) {
+    float t;
+    asm("{\n\t.reg .f32 a, b;\n\tmax.NaN.f32 a, %1, %2;\n\tmax.NaN.f32 b, %3, %4;\n\tmax.NaN.f32 %0, a, b;\n\t}"
+        : "=f"(t)
+        : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)),
+          "f"(__uint_as_float(v.w)));
+    return t;
+  }
 };
 
 __device__ __forceinline__ u64 warp_max_key(u64 k) {
@@ -264,11 +282,68 @@ struct KernelParams {
   int per;                       // tokens of a slice
 };
 
+// A CTA's tokens of a row.  RESIDENT: in shared memory, cleaned (NaN to -inf,
+// +inf to the largest finite value, -inf around the ends); otherwise read from
+// the logits (L2) in every pass and cleaned where an element needs it.
+template <typename T, bool RESIDENT> struct Slice {
+  static constexpr int E = Elem<T>::E;
+  const T *src;                  // the slice's first token
+  T *held;                       // its place in shared memory, -mis elements (16-byte aligned)
+  int start, n, mis, nv;         // first id, tokens, elements before it in its first vector, vectors
+  bool dirty;
+  __device__ __forceinline__ const uint4 *vectors() const {
+    return RESIDENT ? reinterpret_cast<const uint4 *>(held) : reinterpret_cast<const uint4 *>(src - mis);
+  }
+  __device__ __forceinline__ bool whole(int v) const { return v * E >= mis && (v + 1) * E <= mis + n; }
+  static __device__ __forceinline__ float clean(float x) {
+    return isnan(x) ? -INFINITY : fminf(x, Elem<T>::largest());
+  }
+  __device__ __forceinline__ float slow(int v, int e) const {   // an element at an end or in need of cleaning
+    const int i = v * E + e - mis;
+    return i >= 0 && i < n ? clean(to_f32(src[i])) : -INFINITY;
+  }
+  // fn(first id, E values) of every vector, U of them in flight
+  template <int U, typename F> __device__ __forceinline__ void each_vector(F fn) const {
+    const uint4 *at = vectors();
+    for (int v0 = threadIdx.x; v0 < nv; v0 += U * NT) {
+      uint4 t[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT;
+        t[u] = make_uint4(0, 0, 0, 0);
+        if (RESIDENT ? v < nv : v < nv && whole(v)) t[u] = at[v];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT;
+        if (v < nv) {
+          float x[E];
+          Elem<T>::unpack(t[u], x);
+          if (!RESIDENT && (dirty || !whole(v))) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = slow(v, e);
+          }
+          fn(start + v * E - mis, x);
+        }
+      }
+    }
+  }
+  template <typename F> __device__ __forceinline__ void each(F fn) const {   // fn(x, id)
+    each_vector<2>([&](int id, const float *x) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) fn(x[e], id + e);
+    });
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return RESIDENT ? to_f32(held[mis + i]) : clean(to_f32(src[i]));
+  }
+};
+
 // The general cut (the histogram way); every CTA of the cluster calls it.
-template <typename Each>
-__device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const Tables &tab, const Weigher &weigh,
-                                        float temp, int top_k, float top_p, int vocab, u64 cut, unsigned int *err,
-                                        const Each &each) {
+template <typename Row>
+__device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigher weigh, float temp, int top_k,
+                                        float top_p, int vocab, u64 cut, unsigned int *err, const Row tokens) {
+  cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x;
   const float m = weigh.m;
   Fixed &lead = *cl.map_shared_rank(&f, 0);
@@ -282,15 +357,31 @@ __device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const T
     const uint32_t old = atomicAdd(&f.lo[b], u);
     if (old + u < old) atomicAdd(&f.hi[b], 1u);
   };
+  // With top-p alone, tokens beyond this exponent are outside the nucleus
+  // whatever the rest is (vocab of them weigh half of 1 - p at most, the
+  // maximum alone weighs 1): their sum is all that counts.
+  const float far = top_k > 0 ? INFINITY : log2f((float)vocab) - log2f(fmaxf(1.f - top_p, 1e-9f)) + 1.f;
+  auto is_far = [&](float x) { return __fmul_rn(__fsub_rn(m, x), weigh.c_hi) > far; };
+  if (tid == 0) f.own_rest = 0;
   __syncthreads();
   clear();
-  each([&](float x, int) {
-    if (x == -INFINITY) return;
-    int b;
-    uint32_t u;
-    weigh(x, tab, b, u);
-    add(b, u);
+  float part = 0.f;
+  tokens.each([&](float x, int) {
+    if (is_far(x)) {
+      part += rest_weight(weigh, x);
+    } else if (x > -INFINITY) {
+      int b;
+      uint32_t u;
+      weigh(x, tab, b, u);
+      add(b, u);
+    }
   });
+  {
+    u64 rest = (u64)(part * 0x1p44f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    if ((tid & 31) == 0) atomicAdd(&f.own_rest, rest);
+  }
   cl.sync();
 
   // The leader keeps its bins' (tokens, weight) above them; the others follow its commands.
@@ -400,6 +491,7 @@ __device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const T
         int total;
         totals(n0, mm, -1);
         scan(n0, mm, above0, above_m0, total, total_m);
+        for (int r = 0; r < C; ++r) total_m += cl.map_shared_rank(&f, r)->own_rest;
         stage = top_k > 0 && top_k < total ? 0 : 1;
         set_target(total_m);
         if (stage == 1 && !(top_p < 1.f)) tell(CMD_DONE, 0);
@@ -462,7 +554,9 @@ __device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const T
     }
     clear();
     if (cmd == CMD_GATHER) cl.sync();   // the leader's list is empty before anyone adds to it
-    each([&](float x, int id) {
+    const float x_lo = order_value((uint32_t)(r_lo >> 32)), x_hi = order_value((uint32_t)((r_hi - 1) >> 32));
+    tokens.each([&](float x, int id) {
+      if (x < x_lo || x > x_hi || is_far(x)) return;
       const u64 k = key_of(x, id);
       if (k < r_lo || k >= r_hi) return;
       int b;
@@ -481,7 +575,9 @@ __device__ __noinline__ u64 general_cut(cg::cluster_group &cl, Fixed &f, const T
   return f.cut;
 }
 
-template <typename T, bool DRAW>
+// RESIDENT: the row's slices stay in the cluster's shared memory.  Otherwise a
+// CTA a row, which reads it again from L2 in every pass.
+template <typename T, bool DRAW, bool RESIDENT>
 __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__ KernelParams kp) {
   constexpr int E = Elem<T>::E;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -505,55 +601,51 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   float top_p = p.top_p ? p.top_p[entry] : 1.f;
   float min_p = p.min_p ? p.min_p[entry] : 0.f;
 
-  // ---- the slice, cleaned (NaN to -inf, +inf to the largest finite value), and its maximum
-  const int start = min(rank * kp.per, V), n = min(kp.per, V - start);
-  const T *src = (const T *)p.logits + (int64_t)row * p.ld + start;
-  const int mis = (int)(((uintptr_t)src & 15) / sizeof(T));
-  const int nv = n > 0 ? (mis + n + E - 1) / E : 0;
-  uint4 *sv = reinterpret_cast<uint4 *>(slice);
+  // ---- the slice and its maximum
+  Slice<T, RESIDENT> tokens;
+  tokens.start = min(rank * kp.per, V);
+  tokens.n = min(kp.per, V - tokens.start);
+  tokens.src = (const T *)p.logits + (int64_t)row * p.ld + tokens.start;
+  tokens.held = slice;
+  tokens.mis = (int)(((uintptr_t)tokens.src & 15) / sizeof(T));
+  tokens.nv = tokens.n > 0 ? (tokens.mis + tokens.n + E - 1) / E : 0;
+  tokens.dirty = false;
+  const int start = tokens.start, n = tokens.n, mis = tokens.mis, nv = tokens.nv;
   float mx = -INFINITY;
   {
-    const uint4 *gv = reinterpret_cast<const uint4 *>(src - mis);
+    const uint4 *gv = reinterpret_cast<const uint4 *>(tokens.src - mis);
+    uint4 *sv = reinterpret_cast<uint4 *>(slice);
+    bool dirty = false;
     constexpr int U = 8;
     for (int v0 = tid; v0 < nv; v0 += U * NT) {
       uint4 t[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int v = v0 + u * NT;
-        // whole vectors only; the ends come element by element
-        if (v < nv && v * E >= mis && (v + 1) * E <= mis + n) t[u] = __ldcs(gv + v);
+        t[u] = make_uint4(~0u, ~0u, ~0u, ~0u);        // NaN: the ends come element by element
+        if (v < nv && tokens.whole(v)) t[u] = RESIDENT ? __ldcs(gv + v) : gv[v];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int v = v0 + u * NT;
-        if (v >= nv) break;
-        float x[E];
-        bool dirty = false;
-        if (v * E >= mis && (v + 1) * E <= mis + n) {
-          Elem<T>::unpack(t[u], x);
-          sv[v] = t[u];
-        } else {
+        if (v < nv) {
+          const float vm = Elem<T>::max_of(t[u]);
+          if (vm <= Elem<T>::largest()) {
+            if (RESIDENT) sv[v] = t[u];
+            mx = fmaxf(mx, vm);
+          } else {                                    // an end, a NaN or an infinity
+            if (tokens.whole(v)) dirty = true;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int i = v * E + e - mis;
-            x[e] = i >= 0 && i < n ? to_f32(src[i]) : -INFINITY;
+            for (int e = 0; e < E; ++e) {
+              const float x = tokens.slow(v, e);
+              mx = fmaxf(mx, x);
+              if (RESIDENT) slice[v * E + e] = from_f32<T>(x);
+            }
           }
-          dirty = true;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if (!(x[e] <= Elem<T>::largest())) {
-            x[e] = isnan(x[e]) ? -INFINITY : Elem<T>::largest();
-            dirty = true;
-          }
-          mx = fmaxf(mx, x[e]);
-        }
-        if (dirty) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) slice[v * E + e] = from_f32<T>(x[e]);
         }
       }
     }
+    if (!RESIDENT) tokens.dirty = __syncthreads_or(dirty) != 0;
   }
   if (!(temp >= 0.f) || isinf(temp) || isnan(top_p) || !(min_p <= 1.f)) {
     if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
@@ -569,10 +661,11 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   if (top_k <= 0 || top_k >= V) top_k = 0;
   const bool filtered = top_k > 0 || top_p < 1.f;
   const bool brief = filtered && top_k <= MAX_K;
-  // the j-th largest of the CTA's thread maxima, cut to its upper bits (a lower bound)
+  // a value that j tokens of the CTA reach: the j-th largest of the maxima of its groups of four
+  // threads (or of its threads, cut to the upper bits), and the CTA's maximum
   const int j = brief ? ((top_k > 0 ? top_k : TOP_P_LIST) + C - 1) / C : 0;
   float low = -INFINITY;
-  if (j > 1) {
+  if (j > GROUPS * 3 / 4) {
     const uint32_t own = order_image(mx);
     uint32_t found = 0;
 #pragma unroll 1
@@ -582,17 +675,42 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     }
     low = found >= order_image(-FLT_MAX) ? order_value(found) : -INFINITY;
   }
-  const float cta_max = warp_max(mx);
-  if (lane == 0) f.fred[warp] = cta_max;
-  if (tid == 0) f.n_list = 0;
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  if ((tid & 3) == 0) f.group[tid >> 2] = mx;
+  if (tid == 0) {
+    f.n_list = 0;
+    f.own_n = 0;
+    f.own_rest = f.own_listed = 0;
+  }
   __syncthreads();
-  mx = f.fred[lane & (NT / 32 - 1)];
-  mx = warp_max(mx);
+  if (j > 1 && j <= GROUPS * 3 / 4) {
+    // the j-th largest is the smallest with fewer than j larger ones
+    if (tid < GROUPS) {
+      const float own = f.group[tid];
+      int place = 0;
+#pragma unroll 8
+      for (int i = 0; i < GROUPS / 4; ++i) {
+        const float4 o = reinterpret_cast<const float4 *>(f.group)[i];
+        place += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
+      }
+      const float l = -warp_max(place < j ? -own : -INFINITY);
+      if (lane == 0) f.fred[warp] = l;
+    }
+    __syncthreads();
+    low = f.fred[0];
+    for (int w = 1; w < GROUPS / 32; ++w) low = fminf(low, f.fred[w]);
+  }
+  {
+    const float4 g = reinterpret_cast<const float4 *>(f.group)[lane];
+    mx = warp_max(fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)));
+  }
+  if (j == 1) low = mx;
   cl.barrier_wait();
   if (tid < C) {
     Fixed &o = *cl.map_shared_rank(&f, tid);
     o.x_max[rank] = mx;
-    o.x_low[rank] = j == 1 ? mx : low;
+    o.x_low[rank] = low;
   }
   cl.sync();
   float m = f.x_max[0];
@@ -637,15 +755,6 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   if (tid == 0)
     f.x_min = min_p > 0.f ? __double2float_ru(fmax((double)m + (double)temp * log((double)min_p), -(double)FLT_MAX))
                           : -FLT_MAX;
-  // every token of the slice: fn(x, id); ids before and past the slice hold -inf
-  auto each = [&](auto fn) {
-    for (int v = tid; v < nv; v += NT) {
-      float x[E];
-      Elem<T>::unpack(sv[v], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) fn(x[e], start + v * E + e - mis);
-    }
-  };
   const float *noise = DRAW ? p.noise + (int64_t)row * V : nullptr;
 
   u64 cut = (u64)order_image(-FLT_MAX) << 32;   // every finite logit
@@ -655,7 +764,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     const bool weights = top_k == 0;
     u64 listed = 0, rest = 0;
     int count = 0;
-    float part[2] = {0.f, 0.f};
+    float part0 = 0.f, part1 = 0.f;
     auto list_token = [&](float x, int id) {
       ++count;
       if (weights) {
@@ -667,30 +776,46 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       const int at = atomicAdd(&lead.n_list, 1);
       if (at < CAP) lead.list[at] = key_of(x, id);
     };
+    // most vectors hold no token of the list
+    auto list_some = [&](int id, const float *x) {
+      float vm = x[0];
+#pragma unroll
+      for (int e = 1; e < E; ++e) vm = fmaxf(vm, x[e]);
+      if (vm >= low && vm > -INFINITY) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (x[e] >= low && x[e] > -INFINITY) list_token(x[e], id + e);
+      }
+    };
     if (weights) {
-      each([&](float x, int id) {
-        if (x >= low && x > -INFINITY) list_token(x, id);
-        else part[id & 1] += rest_weight(weigh, x);
+      tokens.template each_vector<2>([&](int id, const float *x) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float w = rest_weight(weigh, x[e]);
+          if (e & 1) part1 += x[e] >= low ? 0.f : w;
+          else part0 += x[e] >= low ? 0.f : w;
+        }
+        list_some(id, x);
       });
-      rest = (u64)((part[0] + part[1]) * 0x1p44f);
     } else {
-      each([&](float x, int id) {
-        if (x >= low && x > -INFINITY) list_token(x, id);
-      });
+      tokens.template each_vector<4>(list_some);
     }
-    int total_n;
-    u64 sum = rest, total_rest, total_listed = 0;
-    block_scan(f, count, sum, total_n, total_rest);
+    if (count) {
+      atomicAdd(&f.own_n, count);
+      if (weights) atomicAdd(&f.own_listed, listed);
+    }
     if (weights) {
-      int zero = 0, none;
-      sum = listed;
-      block_scan(f, zero, sum, none, total_listed);
+      rest = (u64)((part0 + part1) * 0x1p44f);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+      if (lane == 0) atomicAdd(&f.own_rest, rest);
     }
+    __syncthreads();
     if (tid < C) {
       Fixed &o = *cl.map_shared_rank(&f, tid);
-      o.x_n[rank] = total_n;
-      o.x_rest[rank] = total_rest;
-      o.x_listed[rank] = total_listed;
+      o.x_n[rank] = f.own_n;
+      o.x_rest[rank] = f.own_rest;
+      o.x_listed[rank] = f.own_listed;
     }
     cl.sync();   // the list is complete
     int all = 0;
@@ -802,7 +927,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   }
   if (filtered) {
     cl.sync();   // the list and the exchange slots of the short way have been read
-    cut = general_cut(cl, f, tab, weigh, temp, top_k, top_p, V, cut, p.err, each);
+    cut = general_cut(f, tab, weigh, temp, top_k, top_p, V, cut, p.err, tokens);
   }
   __syncthreads();   // x_min
   {
@@ -813,10 +938,11 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   // ---- the kept tokens' sum (and the race)
   const float xc = order_value((uint32_t)(cut >> 32));
   const uint32_t idc = ~(uint32_t)cut;
-  auto kept = [&](float x, int id) { return x > xc || (x == xc && (uint32_t)id <= idc); };
+  const bool ties = idc != 0xffffffffu;   // some tokens equal to the cut are dropped
+  auto kept = [&](float x, int id) { return x >= xc && !(ties && x == xc && (uint32_t)id > idc); };
   float s0 = 0.f, s1 = 0.f;
   u64 best = 0;
-  each([&](float x, int id) {
+  tokens.each([&](float x, int id) {
     if (!kept(x, id)) return;
     const float w = ex2((x - m) * c);
     if (id & 1) s1 += w;
@@ -863,21 +989,26 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   }
   // ---- probabilities: 16-byte stores from the row's first aligned element
   auto prob_of = [&](float x, int id) { return kept(x, id) ? ex2((x - m) * c) * inv : 0.f; };
-  auto prob_at = [&](int i) { return prob_of(to_f32(slice[mis + i]), start + i); };
+  auto prob_at = [&](int i) { return prob_of(tokens.at(i), start + i); };
   if (tid < head) out[tid] = prob_at(tid);
   if ((mis + head) % 4 == 0) {
     for (int q = tid; q < quads; q += NT) {
       const int i = head + 4 * q, id = start + i;
+      const T *at = RESIDENT ? slice + mis + i : tokens.src + i;
       float x[4];
       if constexpr (sizeof(T) == 2) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(slice + mis + i);
+        const uint2 t = *reinterpret_cast<const uint2 *>(at);
         x[0] = __uint_as_float(t.x << 16);
         x[1] = __uint_as_float(t.x & 0xffff0000u);
         x[2] = __uint_as_float(t.y << 16);
         x[3] = __uint_as_float(t.y & 0xffff0000u);
       } else {
-        const float4 t = *reinterpret_cast<const float4 *>(slice + mis + i);
+        const float4 t = *reinterpret_cast<const float4 *>(at);
         x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+      }
+      if (!RESIDENT && tokens.dirty) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = tokens.clean(x[e]);
       }
       *reinterpret_cast<float4 *>(out + i) =
           make_float4(prob_of(x[0], id), prob_of(x[1], id + 1), prob_of(x[2], id + 2), prob_of(x[3], id + 3));
@@ -897,16 +1028,8 @@ size_t smem_bytes(int per, int es) {
 }
 int slice_of(int vocab, int C) { return ((vocab + C - 1) / C + 15) / 16 * 16; }
 
-template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaStream_t s) {
-  const int es = sizeof(T);
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // the fewest CTAs whose slices leave room for two of them on an SM; more
-  // while rows are too few to fill the GPU and a slice stays worth a CTA
-  int C = 1;
-  while (C < MAXC && smem_bytes(slice_of(p.vocab, C), es) > 108 * 1024) C *= 2;
-  while (C < MAXC && (int64_t)p.rows * C * 2 <= sms && slice_of(p.vocab, C) > 4096) C *= 2;
+template <typename T, bool DRAW, bool RESIDENT>
+cudaError_t launch(const SampleParams &p, int C, cudaStream_t s) {
   KernelParams kp;
   kp.p = p;
   kp.per = slice_of(p.vocab, C);
@@ -918,7 +1041,7 @@ template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaS
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.rows * C));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem_bytes(kp.per, es);
+  cfg.dynamicSmemBytes = smem_bytes(RESIDENT ? kp.per : 0, sizeof(T));
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -928,11 +1051,25 @@ template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaS
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sampling_kernel<T, DRAW>, kp);
+  return cudaLaunchKernelEx(&cfg, sampling_kernel<T, DRAW, RESIDENT>, kp);
+}
+
+template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaStream_t s) {
+  const int es = sizeof(T);
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (p.rows >= 2 * sms) return launch<T, DRAW, false>(p, 1, s);
+  // the fewest CTAs whose slices leave room for two of them on an SM; more
+  // while rows are too few to fill the GPU and a slice stays worth a CTA
+  int C = 1;
+  while (C < MAXC && smem_bytes(slice_of(p.vocab, C), es) > 108 * 1024) C *= 2;
+  while (C < MAXC && (int64_t)p.rows * C * 2 <= sms && slice_of(p.vocab, C) > 4096) C *= 2;
+  return launch<T, DRAW, true>(p, C, s);
 }
 
 template <typename T, bool DRAW> cudaError_t prepare() {
-  return cudaFuncSetAttribute(sampling_kernel<T, DRAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(sampling_kernel<T, DRAW, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               MAX_SMEM);
 }
 
