@@ -31,8 +31,8 @@
 // about 2^-28 relative and sums are exact multiples of 2^-44, so they do not
 // go by the order of atomics (the weight of the tokens outside a list, which
 // lie beyond the border, comes from the hardware's exponential, good to
-// 2^-22).  A border falls where 64-bit arithmetic puts it except within about
-// 1e-9 of the total plus 2^-22 of the weight outside the list.  min-p compares logits with m + T ln
+// 2^-20).  A border falls where 64-bit arithmetic puts it except within about
+// 1e-9 of the total plus 2^-20 of the weight outside the list.  min-p compares logits with m + T ln
 // min_p formed in 64 bits (by one thread: fp64 runs at 2 lanes a clock here,
 // so everything else stays out of it).
 #include <cooperative_groups.h>
@@ -81,7 +81,8 @@ struct Fixed {
   u64 own_rest, own_listed;
   float fred[NT / 32];
   u64 kred[NT / 32];
-  float x_min;                   // min-p: the smallest logit kept
+  double t_log;                  // min-p: T ln min_p
+  float x_min;                   // and the smallest logit kept
   // exchanged between the CTAs of the cluster, one slot per rank
   float x_max[MAXC], x_low[MAXC], x_sum[MAXC];
   int x_n[MAXC];
@@ -144,17 +145,6 @@ struct Weigher {
     u = t.u[bin & 31] + __float2int_rn(__fmul_rn(t.f[bin & 31], q));
   }
 };
-// 2^-a of a token outside the list: a split into its nearest whole number and
-// a rest formed with one rounding, so that only the error of the hardware's
-// exponential (2^-22) is left.
-__device__ __forceinline__ float rest_weight(const Weigher &g, float x) {
-  const float d = __fsub_rn(g.m, x);
-  const float a = fminf(__fmul_rn(d, g.c_hi), 120.f);   // below 2^-120: nothing in units of 2^-44
-  const float big = __fadd_rn(a, 12582912.f);
-  const float r = __fmaf_rn(d, g.c_lo, __fmaf_rn(d, g.c_hi, __fsub_rn(12582912.f, big)));
-  const float w = __uint_as_float(__float_as_uint(ex2(-r)) - (__float_as_uint(big) << 23));
-  return a < 120.f ? w : 0.f;
-}
 // A sum of weights of one octave in units of 2^-44.
 __device__ __forceinline__ u64 units(u64 sum, int bin) {
   const int octave = bin >> 5;
@@ -368,7 +358,7 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
   float part = 0.f;
   tokens.each([&](float x, int) {
     if (is_far(x)) {
-      part += rest_weight(weigh, x);
+      part += ex2((x - m) * weigh.c_hi);
     } else if (x > -INFINITY) {
       int b;
       uint32_t u;
@@ -611,7 +601,22 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   tokens.nv = tokens.n > 0 ? (tokens.mis + tokens.n + E - 1) / E : 0;
   tokens.dirty = false;
   const int start = tokens.start, n = tokens.n, mis = tokens.mis, nv = tokens.nv;
-  float mx = -INFINITY;
+  if (temp < FLT_MIN) {  // the largest logit alone: one token, whatever the weights
+    if (temp >= 0.f && !isnan(top_p) && min_p <= 1.f) {
+      temp = 1.f;
+      top_k = 1;
+      top_p = 1.f;
+      min_p = 0.f;
+    }
+  }
+  if (top_k <= 0 || top_k >= V) top_k = 0;
+  const bool filtered = top_k > 0 || top_p < 1.f;
+  // nothing is dropped: the sum of the weights goes along with the first pass, relative to the
+  // thread's running maximum
+  const bool plain = !DRAW && !filtered && !(min_p > 0.f);
+  const float c0 = __fdiv_rn(1.44269502f, temp);
+  if (min_p > 0.f && tid == NT - 1) f.t_log = (double)temp * log((double)min_p);
+  float mx = -INFINITY, sum_x = 0.f;
   {
     const uint4 *gv = reinterpret_cast<const uint4 *>(tokens.src - mis);
     uint4 *sv = reinterpret_cast<uint4 *>(slice);
@@ -632,12 +637,25 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
           const float vm = Elem<T>::max_of(t[u]);
           if (vm <= Elem<T>::largest()) {
             if (RESIDENT) sv[v] = t[u];
+            if (plain && vm > mx) {
+              if (mx > -INFINITY) sum_x *= ex2((mx - vm) * c0);
+              mx = vm;
+            }
+            if (plain && mx > -INFINITY) {
+              float x[E], s0 = 0.f;
+              Elem<T>::unpack(t[u], x);
+#pragma unroll
+              for (int e = 0; e < E; ++e) s0 += ex2((x[e] - mx) * c0);
+              sum_x += s0;
+            }
             mx = fmaxf(mx, vm);
           } else {                                    // an end, a NaN or an infinity
             if (tokens.whole(v)) dirty = true;
-#pragma unroll
             for (int e = 0; e < E; ++e) {
               const float x = tokens.slow(v, e);
+              if (plain && x > -INFINITY)
+                sum_x = x > mx ? (mx > -INFINITY ? sum_x * ex2((mx - x) * c0) : 0.f) + 1.f
+                               : sum_x + ex2((x - mx) * c0);
               mx = fmaxf(mx, x);
               if (RESIDENT) slice[v * E + e] = from_f32<T>(x);
             }
@@ -652,18 +670,10 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     return;   // the whole cluster, before any of its barriers
   }
   cl.barrier_arrive();   // every CTA of the cluster runs before the first remote access
-  if (temp < FLT_MIN) {  // the largest logit alone: one token, whatever the weights
-    temp = 1.f;
-    top_k = 1;
-    top_p = 1.f;
-    min_p = 0.f;
-  }
-  if (top_k <= 0 || top_k >= V) top_k = 0;
-  const bool filtered = top_k > 0 || top_p < 1.f;
-  const bool brief = filtered && top_k <= MAX_K;
-  // a value that j tokens of the CTA reach: the j-th largest of the maxima of its groups of four
-  // threads (or of its threads, cut to the upper bits), and the CTA's maximum
-  const int j = brief ? ((top_k > 0 ? top_k : TOP_P_LIST) + C - 1) / C : 0;
+  const float own_mx = mx;   // what sum_x is relative to
+  const bool by_min_p = !filtered && min_p > 0.f;   // min-p alone: its border is known once the maximum is
+  const bool brief = (filtered && top_k <= MAX_K) || by_min_p;
+  const int j = brief && !by_min_p ? ((top_k > 0 ? top_k : TOP_P_LIST) + C - 1) / C : 0;
   float low = -INFINITY;
   if (j > GROUPS * 3 / 4) {
     const uint32_t own = order_image(mx);
@@ -752,16 +762,18 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   }
   const float c = weigh.c_hi;
   // min-p: w >= min_p is x >= m + T ln min_p
-  if (tid == 0)
-    f.x_min = min_p > 0.f ? __double2float_ru(fmax((double)m + (double)temp * log((double)min_p), -(double)FLT_MAX))
-                          : -FLT_MAX;
+  if (tid == 0) f.x_min = min_p > 0.f ? __double2float_ru(fmax((double)m + f.t_log, -(double)FLT_MAX)) : -FLT_MAX;
+  if (by_min_p) {
+    __syncthreads();
+    low = f.x_min;
+  }
   const float *noise = DRAW ? p.noise + (int64_t)row * V : nullptr;
 
   u64 cut = (u64)order_image(-FLT_MAX) << 32;   // every finite logit
   if (brief) {
     // ---- the short way: tokens >= low to the leader's list, the weight of the others
     Fixed &lead = *cl.map_shared_rank(&f, 0);
-    const bool weights = top_k == 0;
+    const bool weights = top_k == 0 && !by_min_p;
     u64 listed = 0, rest = 0;
     int count = 0;
     float part0 = 0.f, part1 = 0.f;
@@ -791,7 +803,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       tokens.template each_vector<2>([&](int id, const float *x) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float w = rest_weight(weigh, x[e]);
+          const float w = ex2((x[e] - m) * c);
           if (e & 1) part1 += x[e] >= low ? 0.f : w;
           else part0 += x[e] >= low ? 0.f : w;
         }
@@ -942,7 +954,8 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   auto kept = [&](float x, int id) { return x >= xc && !(ties && x == xc && (uint32_t)id > idc); };
   float s0 = 0.f, s1 = 0.f;
   u64 best = 0;
-  tokens.each([&](float x, int id) {
+  if (plain) s0 = own_mx > -INFINITY ? sum_x * ex2((own_mx - m) * c) : 0.f;
+  else tokens.each([&](float x, int id) {
     if (!kept(x, id)) return;
     const float w = ex2((x - m) * c);
     if (id & 1) s1 += w;
