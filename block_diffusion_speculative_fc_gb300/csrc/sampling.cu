@@ -28,11 +28,12 @@
 // until it fits (equal logits split by id).
 //
 // Sums that decide a border are whole numbers: a weight is rounded once to
-// about 2^-28 relative and sums are exact multiples of 2^-44, so they do not
+// about 2^-26 relative and sums are exact multiples of 2^-44, so they do not
 // go by the order of atomics (the weight of the tokens outside a list, which
 // lie beyond the border, comes from the hardware's exponential, good to
 // 2^-20).  A border falls where 64-bit arithmetic puts it except within about
-// 1e-9 of the total plus 2^-20 of the weight outside the list.  min-p compares logits with m + T ln
+// 1e-9 of the total (single roundings of 2^-27 average out) plus 2^-20 of the
+// weight outside the list.  min-p compares logits with m + T ln
 // min_p formed in 64 bits (by one thread: fp64 runs at 2 lanes a clock here,
 // so everything else stays out of it).
 #include <cooperative_groups.h>
@@ -57,11 +58,12 @@ constexpr int MAX_K = 512;       // top-k of the short way
 constexpr int TOP_P_LIST = 128;  // tokens that its list holds at least for top-p alone
 constexpr int MAXC = 8;          // CTAs of a cluster
 constexpr int GROUPS = NT / 4;
+constexpr int STREAM_VOCAB = 1 << 18;   // tokens of a CTA at most (sums of the histogram)
 constexpr int MAX_SMEM = 220 * 1024;
 
 struct Tables {
-  uint32_t u[32];                // round(2^28 2^(-i/32))
-  float f[32];                   // 2^28 2^(-i/32)
+  uint32_t u[32];                // round(2^26 2^(-i/32))
+  float f[32];                   // 2^26 2^(-i/32)
 };
 
 typedef unsigned long long u64;
@@ -70,15 +72,16 @@ struct Fixed {
   u64 list[CAP];
   union {
     struct {
-      uint32_t cnt[NB], lo[NB], hi[NB];   // tokens, and weight as a 64-bit sum
+      uint32_t cnt[NB], lo[NB], hi[NB];   // tokens (top-k only), sums of u % 2^13 and u / 2^13
     };
     u64 sorted[CAP];
   };
   u64 warp_m[NT / 32];
   int warp_c[NT / 32];
   float group[GROUPS];           // maxima of groups of four threads
-  int own_n;                     // tokens that this CTA lists, their weight and the others'
-  u64 own_rest, own_listed;
+  int own_n;                     // tokens that this CTA lists
+  u64 own_rest;                  // weight outside the histogram
+  u64 w_rest[NT / 32], w_listed[NT / 32];
   float fred[NT / 32];
   u64 kred[NT / 32];
   double t_log;                  // min-p: T ln min_p
@@ -114,7 +117,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Bin and weight of a token.  The weight is u 2^-(28 + octave(bin)).  a is
+// Bin and weight of a token.  The weight is u 2^-(26 + octave(bin)).  a is
 // carried as a pair of floats; 2^-r on |r| <= 1/64 is a Taylor polynomial in r
 // ln 2 (next term below 2e-12).  Explicit roundings: every pass gets the same
 // bin for a token.
@@ -132,7 +135,7 @@ struct Weigher {
     distance(x, a, al);
     if (!(a < 31.95f)) {                // far tail (a may be infinite, al then NaN)
       bin = NB - 1;
-      u = (uint32_t)(ex2(31.f - a) * 0x1p28f);
+      u = (uint32_t)(ex2(31.f - a) * 0x1p26f);
       return;
     }
     const float big = __fmaf_rn(a, 32.f, 12582912.f);   // 1.5 2^23: rounds 32 a to a whole number
@@ -148,7 +151,7 @@ struct Weigher {
 // A sum of weights of one octave in units of 2^-44.
 __device__ __forceinline__ u64 units(u64 sum, int bin) {
   const int octave = bin >> 5;
-  return octave <= 16 ? sum << (16 - octave) : sum >> (octave - 16);
+  return octave <= 18 ? sum << (18 - octave) : sum >> (octave - 18);
 }
 // p of a sum, rounded up: "below" it as whole numbers is below p of it.
 __device__ __forceinline__ u64 share_of(u64 total, float p) {
@@ -339,20 +342,19 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
   Fixed &lead = *cl.map_shared_rank(&f, 0);
   auto clear = [&] {
     for (int i = tid; i < NB; i += NT) f.cnt[i] = f.lo[i] = f.hi[i] = 0;
-    if (tid == 0) f.n_list = 0;
     __syncthreads();
   };
+  // u < 2^26.1 and at most 2^18 tokens a CTA: both sums fit 32 bits, and nothing is read back
   auto add = [&](int b, uint32_t u) {
-    atomicAdd(&f.cnt[b], 1u);
-    const uint32_t old = atomicAdd(&f.lo[b], u);
-    if (old + u < old) atomicAdd(&f.hi[b], 1u);
+    if (top_k > 0) atomicAdd(&f.cnt[b], 1u);
+    atomicAdd(&f.lo[b], u & 0x1fffu);
+    atomicAdd(&f.hi[b], u >> 13);
   };
   // With top-p alone, tokens beyond this exponent are outside the nucleus
   // whatever the rest is (vocab of them weigh half of 1 - p at most, the
   // maximum alone weighs 1): their sum is all that counts.
   const float far = top_k > 0 ? INFINITY : log2f((float)vocab) - log2f(fmaxf(1.f - top_p, 1e-9f)) + 1.f;
   auto is_far = [&](float x) { return __fmul_rn(__fsub_rn(m, x), weigh.c_hi) > far; };
-  if (tid == 0) f.own_rest = 0;
   __syncthreads();
   clear();
   float part = 0.f;
@@ -370,7 +372,13 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
     u64 rest = (u64)(part * 0x1p44f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-    if ((tid & 31) == 0) atomicAdd(&f.own_rest, rest);
+    if ((tid & 31) == 0) f.w_rest[tid >> 5] = rest;
+    __syncthreads();
+    if (tid == 0) {
+      u64 r = 0;
+      for (int w = 0; w < NT / 32; ++w) r += f.w_rest[w];
+      f.own_rest = r;
+    }
   }
   cl.sync();
 
@@ -390,9 +398,10 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       for (int r = 0; r < C; ++r) {
         const Fixed &o = *cl.map_shared_rank(&f, r);
         nn[i] += (int)o.cnt[b];
-        s += ((u64)o.hi[b] << 32) + o.lo[b];
+        s += ((u64)o.hi[b] << 13) + o.lo[b];
       }
       mm[i] = units(s, of < 0 ? b : of);
+      if (top_k <= 0) nn[i] = s > 0;   // not counted: a list that overflows tells
     }
   };
   auto scan = [&](const int *nn, const u64 *mm, int *ab, u64 *abm, int &tc, u64 &tm) {
@@ -446,6 +455,7 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
   auto tell_range = [&](int count) {
     int sh = 0;
     while (((hi - lo - 1) >> sh) >= NB) ++sh;
+    if (tid == 0) f.n_list = 0;
     tell(count <= CAP ? CMD_GATHER : CMD_SPLIT, sh);
   };
   // start of a stage: the first histogram's bin, and its range of keys (somewhat wider than it)
@@ -499,9 +509,13 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         hi = h < hi ? h : hi;
         __syncthreads();   // sh has been read
         tell_range(f.sel_n);
+      } else if (f.n_list > CAP) {
+        const int over = f.n_list;
+        __syncthreads();
+        tell_range(over);
       } else {
         // the gathered tokens: sort, then walk to the cut
-        const int cnt = min(f.n_list, CAP);
+        const int cnt = f.n_list;
         sort_list(f, cnt);
         int nn[2], ab[2], tc;
         u64 mm[2], abm[2], tm;
@@ -542,8 +556,7 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       if (rank == 0 && tid == 0) raise_error(err, DFLASH_DERR_TIMEOUT);
       break;
     }
-    clear();
-    if (cmd == CMD_GATHER) cl.sync();   // the leader's list is empty before anyone adds to it
+    if (cmd == CMD_SPLIT) clear();
     const float x_lo = order_value((uint32_t)(r_lo >> 32)), x_hi = order_value((uint32_t)((r_hi - 1) >> 32));
     tokens.each([&](float x, int id) {
       if (x < x_lo || x > x_hi || is_far(x)) return;
@@ -691,7 +704,6 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   if (tid == 0) {
     f.n_list = 0;
     f.own_n = 0;
-    f.own_rest = f.own_listed = 0;
   }
   __syncthreads();
   if (j > 1 && j <= GROUPS * 3 / 4) {
@@ -812,22 +824,33 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     } else {
       tokens.template each_vector<4>(list_some);
     }
-    if (count) {
-      atomicAdd(&f.own_n, count);
-      if (weights) atomicAdd(&f.own_listed, listed);
-    }
+    if (count) atomicAdd(&f.own_n, count);
     if (weights) {
       rest = (u64)((part0 + part1) * 0x1p44f);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-      if (lane == 0) atomicAdd(&f.own_rest, rest);
+      for (int o = 16; o > 0; o >>= 1) {
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        listed += __shfl_xor_sync(0xffffffffu, listed, o);
+      }
+      if (lane == 0) {
+        f.w_rest[warp] = rest;
+        f.w_listed[warp] = listed;
+      }
     }
     __syncthreads();
     if (tid < C) {
       Fixed &o = *cl.map_shared_rank(&f, tid);
+      u64 r = 0, l = 0;
+      if (weights) {
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+          r += f.w_rest[w];
+          l += f.w_listed[w];
+        }
+      }
       o.x_n[rank] = f.own_n;
-      o.x_rest[rank] = f.own_rest;
-      o.x_listed[rank] = f.own_listed;
+      o.x_rest[rank] = r;
+      o.x_listed[rank] = l;
     }
     cl.sync();   // the list is complete
     int all = 0;
@@ -1047,7 +1070,7 @@ cudaError_t launch(const SampleParams &p, int C, cudaStream_t s) {
   kp.p = p;
   kp.per = slice_of(p.vocab, C);
   for (int i = 0; i < 32; ++i) {
-    const double w = std::exp2(28.0 - i / 32.0);
+    const double w = std::exp2(26.0 - i / 32.0);
     kp.t.u[i] = (uint32_t)std::llround(w);
     kp.t.f[i] = (float)w;
   }
@@ -1072,7 +1095,7 @@ template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaS
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (p.rows >= 2 * sms) return launch<T, DRAW, false>(p, 1, s);
+  if (p.rows >= 2 * sms && p.vocab <= STREAM_VOCAB) return launch<T, DRAW, false>(p, 1, s);
   // the fewest CTAs whose slices leave room for two of them on an SM; more
   // while rows are too few to fill the GPU and a slice stays worth a CTA
   int C = 1;

@@ -608,9 +608,9 @@ typedef struct {
  * 0 for tokens that the filters drop (float32 [rows, vocab], the layout that
  * dflash_accept_commit_sampled reads).  logits: [rows, vocab] of `dtype` with
  * a row stride in elements; any alignment of the type.  probs must not
- * overlap logits.  The border of top-p is decided on weights of about 2^-28
- * relative error (2^-22 for the tail that lies far beyond it), that of min-p
- * in 64 bits; the same in every run.
+ * overlap logits.  The border of top-p is decided on sums of about 1e-9
+ * relative error (2^-20 for the weight of the tail that lies far beyond it),
+ * that of min-p in 64 bits; the same in every run.
  * vocab <= 524288 (bf16) or 262144 (fp32).
  */
 int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
