@@ -167,6 +167,13 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 template <typename T> struct Elem;
 template <> struct Elem<bf16> {
   static constexpr int E = 8;
+  typedef uint2 Quad;
+  static __device__ __forceinline__ void unpack4(const Quad &t, float *x) {
+    x[0] = __uint_as_float(t.x << 16);
+    x[1] = __uint_as_float(t.x & 0xffff0000u);
+    x[2] = __uint_as_float(t.y << 16);
+    x[3] = __uint_as_float(t.y & 0xffff0000u);
+  }
   static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -185,6 +192,10 @@ template <> struct Elem<bf16> {
 };
 template <> struct Elem<float> {
   static constexpr int E = 4;
+  typedef float4 Quad;
+  static __device__ __forceinline__ void unpack4(const Quad &t, float *x) {
+    x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+  }
   static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
     x[0] = __uint_as_float(v.x);
     x[1] = __uint_as_float(v.y);
@@ -977,17 +988,52 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   auto kept = [&](float x, int id) { return x >= xc && !(ties && x == xc && (uint32_t)id > idc); };
   float s0 = 0.f, s1 = 0.f;
   u64 best = 0;
-  if (plain) s0 = own_mx > -INFINITY ? sum_x * ex2((own_mx - m) * c) : 0.f;
-  else tokens.each([&](float x, int id) {
-    if (!kept(x, id)) return;
-    const float w = ex2((x - m) * c);
-    if (id & 1) s1 += w;
-    else s0 += w;
-    if (DRAW) {
-      const u64 k = argmax_key(w / noise[id], id);
-      best = k > best ? k : best;
-    }
-  });
+  if (plain) {
+    s0 = own_mx > -INFINITY ? sum_x * ex2((own_mx - m) * c) : 0.f;
+  } else if (!DRAW) {
+    tokens.each([&](float x, int id) {
+      const float w = kept(x, id) ? ex2((x - m) * c) : 0.f;
+      if (id & 1) s1 += w;
+      else s0 += w;
+    });
+  } else {
+    // the exact quotient only where an approximate one (2^-21) reaches the best so far; a thread's
+    // ids ascend, so the first of equal scores has the lowest
+    float top = -1.f;
+    int top_id = 0;
+    tokens.template each_vector<2>([&](int id, const float *x) {
+      float e[E];
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < E; ++i) any = any || kept(x[i], id + i);
+      if (!any) return;
+      if (((uintptr_t)(noise + id) & 15) == 0 && id >= start && id + E <= start + n) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const float4 t = __ldcs(reinterpret_cast<const float4 *>(noise + id + i));
+          e[i] = t.x, e[i + 1] = t.y, e[i + 2] = t.z, e[i + 3] = t.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) e[i] = kept(x[i], id + i) ? noise[id + i] : 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const bool k = kept(x[i], id + i);
+        const float w = k ? ex2((x[i] - m) * c) : 0.f;
+        if (i & 1) s1 += w;
+        else s0 += w;
+        if (k && __fdividef(w, e[i]) * 1.000001f >= top) {
+          const float score = __fdiv_rn(w, e[i]);
+          if (score > top) {
+            top = score;
+            top_id = id + i;
+          }
+        }
+      }
+    });
+    if (top >= 0.f) best = argmax_key(top, top_id);
+  }
   const float sum = warp_sum(s0 + s1);
   if (DRAW) best = warp_max_key(best);
   __syncthreads();
@@ -1028,26 +1074,28 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   auto prob_at = [&](int i) { return prob_of(tokens.at(i), start + i); };
   if (tid < head) out[tid] = prob_at(tid);
   if ((mis + head) % 4 == 0) {
-    for (int q = tid; q < quads; q += NT) {
-      const int i = head + 4 * q, id = start + i;
-      const T *at = RESIDENT ? slice + mis + i : tokens.src + i;
-      float x[4];
-      if constexpr (sizeof(T) == 2) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(at);
-        x[0] = __uint_as_float(t.x << 16);
-        x[1] = __uint_as_float(t.x & 0xffff0000u);
-        x[2] = __uint_as_float(t.y << 16);
-        x[3] = __uint_as_float(t.y & 0xffff0000u);
-      } else {
-        const float4 t = *reinterpret_cast<const float4 *>(at);
-        x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-      }
-      if (!RESIDENT && tokens.dirty) {
+    constexpr int U = 4;                   // four elements a load, U of them in flight
+    typedef typename Elem<T>::Quad Quad;
+    const T *from = RESIDENT ? slice + mis + head : tokens.src + head;
+    for (int q0 = tid; q0 < quads; q0 += U * NT) {
+      Quad t[U];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = tokens.clean(x[e]);
+      for (int u = 0; u < U; ++u)
+        if (q0 + u * NT < quads) t[u] = *reinterpret_cast<const Quad *>(from + 4 * (q0 + u * NT));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = head + 4 * (q0 + u * NT), id = start + i;
+        if (q0 + u * NT < quads) {
+          float x[4];
+          Elem<T>::unpack4(t[u], x);
+          if (!RESIDENT && tokens.dirty) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = tokens.clean(x[e]);
+          }
+          *reinterpret_cast<float4 *>(out + i) = make_float4(prob_of(x[0], id), prob_of(x[1], id + 1),
+                                                             prob_of(x[2], id + 2), prob_of(x[3], id + 3));
+        }
       }
-      *reinterpret_cast<float4 *>(out + i) =
-          make_float4(prob_of(x[0], id), prob_of(x[1], id + 1), prob_of(x[2], id + 2), prob_of(x[3], id + 3));
     }
   } else {
     for (int q = tid; q < quads; q += NT) {
