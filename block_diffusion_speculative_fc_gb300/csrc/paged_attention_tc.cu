@@ -16,9 +16,10 @@
 //
 // Two streams of 128 threads (a thread per row: TMEM lane = row, no exchange
 // between threads) alternate on the tensor cores: while one takes the softmax
-// of its tile, the other's products run.  With more than 128 rows the streams
-// hold 128 rows each and share every K/V tile (32 bytes of K/V per SM clock at
-// full tensor rate; 128 rows would need the 64 that L2 can just deliver).  With
+// of its tile, the other's products run.  A stream's row tile is 128 / group
+// whole tokens.  With more rows than that the streams
+// hold a row tile each and share every K/V tile (32 bytes of K/V per SM clock at
+// full tensor rate; one row tile would need the 64 that L2 can just deliver).  With
 // fewer, both hold the same rows and take even and odd tiles, which halves the
 // serial chain of a tile: those items are bound by the K/V bytes.  S and the
 // rounded weights w share their TMEM columns (w is the second product's A
@@ -40,7 +41,6 @@ namespace dflash {
 namespace {
 
 constexpr int KT = 128;                   // keys of a tile
-constexpr int ROWS = 256;                 // rows of an item, 128 a stream
 constexpr int THREADS = 384;
 // registers a thread: 168 at launch (384 threads), then 208 for the streams and 80 for the rest
 // (256 * 208 + 128 * 80 <= 384 * 168)
@@ -66,7 +66,7 @@ template <int D> struct Cfg {
 };
 
 struct Item {
-  int g, r0, nrows, req;                  // KV head, first row (token * G + head), rows, request (-1: prefix)
+  int g, tok0, ntok, req;                 // KV head, first token, tokens, request (-1: prefix)
   int page0, ntiles, keys_left, part;     // first page, tiles, keys from the first to the segment's end, partial rows (-1: final)
   int lim_base, lim_slope, pad0, pad1;    // keys that row's token sees: lim_base + lim_slope * token
 };
@@ -81,6 +81,7 @@ struct Head {
 
 struct Params {
   CUtensorMap tmK, tmV;                   // dims {D, KVH, n_pages * 64}, box {64, 1, 64}
+  CUtensorMap tmQ;                        // dims {D, H, total_rows}, box {64, G, 128 / G}
   PagedAttnParams a;
   Head *head;
   Item *items;
@@ -89,7 +90,7 @@ struct Params {
   float *part_o, *part_lse;               // [cap][D], [cap]
   int cap, max_items, sms;
   float scale_log2;                       // |scale| log2 e
-  uint32_t q_sign;                        // 0x80008000 when scale < 0
+  int negative;                           // scale < 0: S changes its sign
 };
 
 // ------------------------------------------------------------------ PTX
@@ -181,6 +182,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store32(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -203,20 +209,17 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 
-// Place of V(t) and K(t) in an item's load order: the first `ahead` K tiles,
-// then V(0), K(ahead), V(1), K(ahead + 1), ...
+// Place of V(t) in an item's load order: the first `ahead` K tiles, then V(0),
+// K(ahead), V(1), K(ahead + 1), ...
 __device__ __forceinline__ int order_v(int t, int n, int ahead) {
   return min(ahead, n) + t + min(t, max(0, n - ahead));
-}
-__device__ __forceinline__ int order_k(int t, int n, int ahead) {
-  return t < ahead ? t : order_v(t - ahead, n, ahead) + 1;
 }
 
 __device__ __forceinline__ Item load_item(const Item *p) {
   const int4 *s = reinterpret_cast<const int4 *>(p);
   const int4 a = __ldg(s), b = __ldg(s + 1), c = __ldg(s + 2);
   Item it;
-  it.g = a.x, it.r0 = a.y, it.nrows = a.z, it.req = a.w;
+  it.g = a.x, it.tok0 = a.y, it.ntok = a.z, it.req = a.w;
   it.page0 = b.x, it.ntiles = b.y, it.keys_left = b.z, it.part = b.w;
   it.lim_base = c.x, it.lim_slope = c.y;
   return it;
@@ -263,8 +266,8 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
 struct Split {
   int tiles, splits;
 };
-__device__ __forceinline__ Split split_keys(int nkt, int R, long long U) {
-  const int unit = R > 128 ? 2 : 1;
+__device__ __forceinline__ Split split_keys(int nkt, int n, int tpt, long long U) {
+  const int unit = n > tpt ? 2 : 1;       // row tiles of an item
   long long per = (U + unit - 1) / unit;
   per = per < 1 ? 1 : per;
   const int ns = nkt > 0 ? (int)((nkt + per - 1) / per) : 0;
@@ -273,7 +276,7 @@ __device__ __forceinline__ Split split_keys(int nkt, int R, long long U) {
   s.splits = (nkt + s.tiles - 1) / s.tiles;
   return s;
 }
-__device__ __forceinline__ int row_units(int R) { return R / ROWS * 2 + (R % ROWS > 128 ? 2 : R % ROWS > 0); }
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ Params p) {
   pdl_wait();
@@ -285,6 +288,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   __shared__ int s_lo, s_hi;
   const PagedRows &r = p.a.rows;
   const int b = threadIdx.x, G = p.a.H / p.a.KVH, KVH = p.a.KVH, prefix = r.prefix_len;
+  const int tpt = 128 / G;                      // tokens of a row tile
   if (b == 0) {
     s_lo = r.total_rows;
     s_hi = 0;
@@ -311,17 +315,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   const int lo = s_lo, rows = max(0, s_hi - s_lo);
   const int R = n * G, keys = ctx + n, nkt = n > 0 ? (keys + KT - 1) / KT : 0;
   const int Rp = prefix > 0 ? rows * G : 0, nktp = Rp > 0 ? prefix / KT + (prefix % KT != 0) : 0;
-  const long long W = block_sum((long long)KVH * nkt * row_units(R), s_sum) +
-                      (long long)KVH * nktp * row_units(Rp);
+  const long long W = block_sum((long long)KVH * nkt * ceil_div(n, tpt), s_sum) +
+                      (long long)KVH * nktp * ceil_div(rows, tpt);
   long long U = (W + (long long)ITEMS_PER_SM * p.sms - 1) / ((long long)ITEMS_PER_SM * p.sms);
   U = U < 2 ? 2 : U;
   Split sp, spp;
   int part = 0, items = 0, total_rows = 0, total_items = 0;
   bool joined = false;
-  const int nrt = (R + ROWS - 1) / ROWS, nrtp = (Rp + ROWS - 1) / ROWS;
+  const int nrt = ceil_div(n, 2 * tpt), nrtp = Rp > 0 ? ceil_div(rows, 2 * tpt) : 0;
   for (int pass = 0; pass < 2; ++pass) {
-    sp = split_keys(nkt, R, U);
-    spp = split_keys(nktp, Rp, U);
+    sp = split_keys(nkt, n, tpt, U);
+    spp = split_keys(nktp, rows, tpt, U);
     joined = n > 0 && (prefix > 0 || sp.splits > 1);
     part = block_scan(joined ? sp.splits * KVH * R : 0, s_scan, total_rows);
     items = block_scan(KVH * nrt * sp.splits, s_scan, total_items);
@@ -372,29 +376,29 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (s0 == 0) {
       const int per = KVH * spp.splits, rt = j / per, g = j % per / spp.splits, s = j % spp.splits;
       it.g = g;
-      it.r0 = lo * G + rt * ROWS;
-      it.nrows = min(ROWS, Rp - rt * ROWS);
+      it.tok0 = lo + rt * 2 * tpt;
+      it.ntok = min(2 * tpt, rows - rt * 2 * tpt);
       it.req = -1;
       it.page0 = s * spp.tiles * 2;
       it.ntiles = min(spp.tiles, nktp - s * spp.tiles);
       it.keys_left = prefix - s * spp.tiles * KT;
-      it.part = (g * spp.splits + s) * Rp + rt * ROWS;
+      it.part = (g * spp.splits + s) * Rp + rt * 2 * tpt * G;
       it.lim_base = it.keys_left;
       it.lim_slope = 0;
     } else {
       const int q = s0 - 1, ns = s_splits[q], tiles = s_tiles[q], nq = s_n[q], c = s_ctx[q], st = s_start[q];
-      const int Rq = nq * G, per = KVH * ns, nt = (Rq + ROWS - 1) / ROWS;
+      const int Rq = nq * G, per = KVH * ns, nt = ceil_div(nq, 2 * tpt);
       const int rt = nt - 1 - j / per, g = j % per / ns, s = j % ns;
-      const int last = (min(Rq, (rt + 1) * ROWS) - 1) / G;     // last token of the row tile
+      const int last = min(nq, (rt + 1) * 2 * tpt) - 1;        // last token of the row tiles
       const int seen = p.a.causal ? c + last + 1 : c + nq;
       it.g = g;
-      it.r0 = st * G + rt * ROWS;
-      it.nrows = min(ROWS, Rq - rt * ROWS);
+      it.tok0 = st + rt * 2 * tpt;
+      it.ntok = min(2 * tpt, nq - rt * 2 * tpt);
       it.req = q;
       it.page0 = s * tiles * 2;
       it.ntiles = max(0, min(tiles, (seen + KT - 1) / KT - s * tiles));
       it.keys_left = c + nq - s * tiles * KT;
-      it.part = s_part[q] >= 0 ? s_part[q] + (g * ns + s) * Rq + rt * ROWS : -1;
+      it.part = s_part[q] >= 0 ? s_part[q] + (g * ns + s) * Rq + rt * 2 * tpt * G : -1;
       it.lim_slope = p.a.causal;
       it.lim_base = (p.a.causal ? c + 1 - st : c + nq) - s * tiles * KT;
     }
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
-  constexpr int NS = C::NSLOT, NB = D / 64, CH = D / 8;
+  constexpr int NS = C::NSLOT, NB = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = smem + C::OFF_RING;
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   uint64_t *done = ml_free + 1;
   uint32_t *s_tmem = (uint32_t *)(done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.a.H / p.a.KVH;
+  const int G = p.a.H / p.a.KVH, tpt = 128 / G, rt_rows = tpt * G;   // tokens and rows of a row tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       mbar_init(&o_full[i], 1);
       mbar_init(&o_read[i], 128);
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, 1);
     mbar_init(q_free, 1);
     mbar_init(ml_full, 128);
     mbar_init(ml_free, 128);
@@ -452,6 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   if (warp == 8 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmK) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmV) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmQ) : "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -475,35 +480,40 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
     if (warp == 8) {
       // ------------------------------------------------------------ producer (one warp)
-      uint32_t u = 0;                       // tiles issued
+      uint32_t u = 0, k = 0;                // tiles issued, items begun
+      int slot = 0, phase = 1;              // place in the ring; parity of its empty barrier
       Item it;
       int prev0 = 0, prev1 = 0, cur0 = 0, cur1 = 0;   // pages of the last two K tiles
       while (ok && next_item(it)) {
-        const int n = it.ntiles, ahead = it.nrows > 128 ? 1 : 2;
+        const int n = it.ntiles, ahead = it.ntok > tpt ? 1 : 2;
         const int npages = (min(it.keys_left, n * KT) + kPageRows - 1) / kPageRows;
         const int *list = (it.req < 0 ? p.a.rows.prefix_pages
                                       : p.a.rows.page_table + (int64_t)it.req * p.a.rows.pages_per_req) + it.page0;
         int batch = 0;
         auto issue = [&](const CUtensorMap *tm, int t, int pg0, int pg1) {
-          const int slot = u % NS;
           bool good = true;
           if (lane == 0) {
-            good = mbar_wait(&empty[slot], ((u / NS) & 1) ^ 1);
+            good = mbar_wait(&empty[slot], phase);
             if (good) {
               const bool two = 2 * t + 1 < npages;
               asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[slot])),
                            "r"(two ? C::TILE : C::TILE / 2)
                            : "memory");
               uint8_t *dst = ring + slot * C::TILE;
-  #pragma unroll
-              for (int k = 0; k < NB; ++k) {
-                tma3(dst + k * (KT * 128), tm, &full[slot], 64 * k, it.g, pg0 * kPageRows);
-                if (two) tma3(dst + k * (KT * 128) + 8192, tm, &full[slot], 64 * k, it.g, pg1 * kPageRows);
+#pragma unroll
+              for (int c = 0; c < NB; ++c) {
+                tma3(dst + c * (KT * 128), tm, &full[slot], 64 * c, it.g, pg0 * kPageRows);
+                if (two) tma3(dst + c * (KT * 128) + 8192, tm, &full[slot], 64 * c, it.g, pg1 * kPageRows);
               }
             }
           }
           ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-          if (ok) ++u;
+          if (!ok) return;
+          ++u;
+          if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
+          }
         };
         auto issue_k = [&](int t) {
           const int j = 2 * t;
@@ -523,7 +533,28 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           cur1 = __shfl_sync(0xffffffffu, batch, j % 32 + 1);
           issue(&p.tmK, t, cur0, cur1);
         };
+        // the query rows, once the last S of the item before has read its own
+        auto issue_q = [&] {
+          bool good = true;
+          if (lane == 0) {
+            if (k > 0) good = mbar_wait(q_free, (k - 1) & 1);
+            if (good) {
+              const int tiles = it.ntok > tpt ? 2 : 1;
+              asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(q_full)),
+                           "r"(tiles * rt_rows * D * 2)
+                           : "memory");
+              for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                  tma3(smem + x * C::Q_TILE + c * (128 * 128), &p.tmQ, q_full, 64 * c, it.g * G, it.tok0 + x * tpt);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+          if (ok) ++k;
+        };
+        // the K tiles that go ahead find free slots before Q is free
         for (int t = 0; t < min(ahead, n) && ok; ++t) issue_k(t);
+        if (ok) issue_q();
         for (int t = 0; t < n && ok; ++t) {
           // K(t) is the last K tile issued, or the one before it
           const bool older = ahead == 2 && t + 1 < n;
@@ -535,75 +566,101 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (!ok) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
         // every copy has landed before the CTA exits
         for (uint32_t v = u > (uint32_t)NS ? u - NS : 0; v < u; ++v) mbar_wait(&full[v % NS], (v / NS) & 1);
+        if (k > 0) mbar_wait(q_full, (k - 1) & 1);
       }
     } else if (warp == 9) {
-      // ------------------------------------------------------------ MMA issuer (one thread)
-      if (lane == 0) {
-        constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
-        const uint32_t q_addr = su32(smem), ring_addr = su32(ring);
-        uint32_t u = 0, k = 0;              // ring tiles and number of the items before
-        uint32_t p_par = 0;                 // bit x: parity of p_full[x]
-        uint32_t o_used = 0, o_par = 3;     // bit x: stream x has had an item; parity of its o_read
-        auto wait = [&](uint64_t *b, uint32_t parity) {
-          if (ok && !mbar_wait(b, parity)) ok = false;
-        };
-        Item it;
-        while (ok && next_item(it)) {
-          // Steps (t, x): stream x takes tile t.  A pair takes every tile in both
-          // streams, a single row tile alternates.  A step is O_x += w V(t), then S_x
-          // of the stream's next tile t + ahead (the first S before the loop).
-          const int n = it.ntiles, pair = it.nrows > 128 ? 1 : 0, ahead = 2 - pair;
-          const int steps = n << pair;
-          auto slot_of = [&](int order) { return (int)((u + order) % NS); };
-          auto issue_s = [&](int x, int t) {
-            const int order = order_k(t, n, ahead), slot = slot_of(order);
-            wait(&full[slot], ((u + order) / NS) & 1);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t qd = desc_k(q_addr + (pair & x) * C::Q_TILE), kd = desc_k(ring_addr + slot * C::TILE);
-  #pragma unroll
+      // ------------------------------------------------------------ MMA issuer
+      // The warp stays together; one elected lane issues.
+      constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
+      const uint64_t q_desc = desc_k(su32(smem)), k_desc = desc_k(su32(ring)), v_desc = desc_mn(su32(ring), KT * 128);
+      uint32_t k = 0;                     // items before
+      int slot = 0, phase = 0;            // next ring tile to use
+      uint32_t p_par = 0;                 // bit x: parity of p_full[x]
+      uint32_t o_used = 0, o_par = 3;     // bit x: stream x has had an item; parity of its o_read
+      auto wait = [&](uint64_t *b, uint32_t parity) {
+        if (ok && !mbar_wait(b, parity)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      auto elected = [] {
+        uint32_t e;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+        return e != 0;
+      };
+      Item it;
+      while (ok && next_item(it)) {
+        // Steps (t, x): stream x takes tile t.  A pair takes every tile in both
+        // streams, a single row tile alternates.  A step is O_x += w V(t), then S_x
+        // of the stream's next tile t + ahead (the first S before the loop).  The ring
+        // is used in order: V(t), K(t + ahead), both steps of a pair from the same two.
+        const int n = it.ntiles, pair = it.ntok > tpt ? 1 : 0, ahead = 2 - pair;
+        const int steps = n << pair;
+        // S_x = Q K^T with the K tile at ring place (at, ph); `last`: its last use
+        auto issue_s = [&](int x, int at, int ph, bool last, bool last_of_item) {
+          wait(&full[at], ph);
+          if (!ok) return;
+          tc_fence_after();
+          if (elected()) {
+            const uint64_t qd = q_desc + (pair & x) * (C::Q_TILE >> 4), kd = k_desc + at * (C::TILE >> 4);
+#pragma unroll
             for (int i = 0; i < D / 16; ++i)
               umma_ss(tmem + x * KT, qd + (i >> 2) * ((128 * 128) >> 4) + 2 * (i & 3),
                       kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3), ID_S, i ? 1u : 0u);
             umma_commit(&s_full[x]);
-            if (x == 1 || !pair) {          // the tile's last use
-              umma_commit(&empty[slot]);
-              if (t == n - 1) umma_commit(q_free);
-            }
-          };
-          wait(q_full, k & 1);
-  #pragma unroll 1
-          for (int i = 0; i < min(2, steps) && ok; ++i) issue_s(i, pair ? 0 : i);
-  #pragma unroll 1
-          for (int i = 0; i < steps && ok; ++i) {
-            const int x = i & 1, t = i >> pair;
-            const int order = order_v(t, n, ahead), slot = slot_of(order);
-            wait(&p_full[x], (p_par >> x) & 1);
-            p_par ^= 1u << x;
-            if (t < ahead) {                // the item before has read this stream's O
-              if ((o_used >> x) & 1) wait(&o_read[x], (o_par >> x) & 1);
-              o_used |= 1u << x;
-              o_par ^= 1u << x;
-            }
-            wait(&full[slot], ((u + order) / NS) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = desc_mn(ring_addr + slot * C::TILE, KT * 128);
-  #pragma unroll
+            if (last) umma_commit(&empty[at]);
+            if (last && last_of_item) umma_commit(q_free);
+          }
+          __syncwarp();
+        };
+        auto advance = [&](int &at, int &ph) {
+          if (++at == NS) {
+            at = 0;
+            ph ^= 1;
+          }
+        };
+        wait(q_full, k & 1);
+        for (int i = 0; i < min(2, steps) && ok; ++i) {
+          const bool last = i == 1 || !pair;
+          issue_s(i, slot, phase, last, n <= ahead && i == min(2, steps) - 1);
+          if (last) advance(slot, phase);
+        }
+#pragma unroll 1
+        for (int i = 0; i < steps && ok; ++i) {
+          const int x = i & 1, t = i >> pair;
+          const bool last = x == 1 || !pair;
+          wait(&p_full[x], (p_par >> x) & 1);
+          p_par ^= 1u << x;
+          if (t < ahead) {                // the item before has read this stream's O
+            if ((o_used >> x) & 1) wait(&o_read[x], (o_par >> x) & 1);
+            o_used |= 1u << x;
+            o_par ^= 1u << x;
+          }
+          wait(&full[slot], phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (elected()) {
+            const uint64_t vd = v_desc + slot * (C::TILE >> 4);
+#pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
               umma_ts(tmem + 256 + x * 128, tmem + x * KT + kk * 8, vd + kk * (2048 >> 4), ID_O,
                       (t < ahead && kk == 0) ? 0u : 1u);
-            if (x == 1 || !pair) umma_commit(&empty[slot]);
-            if (t + ahead < n) issue_s(x, t + ahead);
-            else umma_commit(&o_full[x]);
+            if (last) umma_commit(&empty[slot]);
+            if (t + ahead >= n) umma_commit(&o_full[x]);
           }
-          u += 2 * n;
-          ++k;
+          __syncwarp();
+          int at = slot, ph = phase;
+          advance(at, ph);
+          if (t + ahead < n) {
+            issue_s(x, at, ph, last, t + ahead == n - 1);
+            if (last) advance(at, ph);
+          }
+          if (last) slot = at, phase = ph;
         }
-        umma_commit(done);
-        if (!mbar_wait(done, 0)) ok = false;   // every MMA has ended before TMEM is freed
-        if (!ok) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
+        ++k;
       }
+      if (elected()) umma_commit(done);
+      __syncwarp();
+      if (!mbar_wait(done, 0)) ok = false;   // every MMA has ended before TMEM is freed
+      if (!ok && lane == 0) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_STREAM));
@@ -612,56 +669,26 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + x * KT;
     const float sl = p.scale_log2;
+    const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
     // every wait is one for the warp, so that its lanes stay together
     auto wait = [&](uint64_t *b, uint32_t parity) {
       if (ok && !mbar_wait(b, parity)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
-    // the item's query rows: 128 of this stream, or half of the 128 of both
-    auto load_q = [&](const Item &it) {
-      const bool pair = it.nrows > 128;
-      constexpr int RP = 128 / CH;        // rows a pass of 128 threads
-      const int i0 = pair ? 0 : x * (CH / 2), i1 = pair ? CH : (x + 1) * (CH / 2);
-      const int first = pair ? x * 128 : 0, ch = row % CH;
-      uint8_t *dst = smem + (pair ? x : 0) * C::Q_TILE + (ch >> 3) * (128 * 128);
-      for (int i = i0; i < i1; i += 4) {
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rr = (i + j) * RP + row / CH, r = it.r0 + first + rr;
-          v[j] = make_uint4(0, 0, 0, 0);
-          if (first + rr < it.nrows) {
-            const int tok = r / G, h = it.g * G + r % G;
-            v[j] = __ldg(reinterpret_cast<const uint4 *>((const bf16 *)p.a.q + (int64_t)tok * p.a.q_stride +
-                                                         (int64_t)h * D) + ch);
-            v[j].x ^= p.q_sign;
-            v[j].y ^= p.q_sign;
-            v[j].z ^= p.q_sign;
-            v[j].w ^= p.q_sign;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rr = (i + j) * RP + row / CH;
-          *reinterpret_cast<uint4 *>(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[j];
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(q_full);
-    };
-
-    uint32_t c = 0, u = 0, k = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
+    uint32_t c = 0, u = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
+    const int row_tok = row / G, row_head = row % G;
     Item it, nit;
     bool have = next_item(it);
-    if (have) load_q(it);
     while (have) {
+      const bool more = next_item(nit);
       const int n = it.ntiles;
-      const bool pair = it.nrows > 128;
+      const bool pair = it.ntok > tpt;
       const int ahead = pair ? 1 : 2;
-      const int mine = pair ? x * 128 + row : row;             // this thread's row of the item
-      const bool live = (pair ? x * 128 : 0) + (warp & 3) * 32 < it.nrows;   // any row of the warp
-      const int tok = (it.r0 + mine) / G, h = it.g * G + (it.r0 + mine) % G;
-      const int lim = mine < it.nrows ? it.lim_base + it.lim_slope * tok : 0;
+      const int mine = (pair ? x * tpt : 0) + row_tok;         // this thread's token of the item
+      const bool own = row < rt_rows && mine < it.ntok;
+      const bool live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
+      const int tok = it.tok0 + mine, h = it.g * G + row_head;
+      const int lim = own ? it.lim_base + it.lim_slope * tok : 0;
       float m = -INFINITY, l = 0.f;
       for (int t = pair ? 0 : x; t < n && ok; t += pair ? 1 : 2) {
         wait(&s_full[x], c & 1);
@@ -673,6 +700,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < KT; i += 32) tmem_ld32(t_s + i, sv + i);
           tmem_ld_wait();
+          if (p.negative) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) sv[i] ^= 0x80000000u;
+          }
           const int vis = lim - t * KT;                        // visible keys of this tile
           const bool whole = __all_sync(0xffffffffu, vis >= KT);
           float mx;
@@ -751,12 +782,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         mbar_arrive(&p_full[x]);
       }
       u += 2 * n;
-      const bool more = next_item(nit);
-      if (more && ok) {                    // the last S of the item has read Q
-        wait(q_free, k & 1);
-        if (ok) load_q(nit);
-      }
-      ++k;
       if (!ok) break;
       // ---- the item's rows: o / l and log2 of their weight, or the result
       const bool both = !pair && n > 1;    // the other stream holds the odd tiles' share
@@ -787,10 +812,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           const float inv = l > 0.f ? 1.f / l : 0.f;
           a0 *= inv;
           a1 *= inv;
-          const bool store = mine < it.nrows;
           bf16 *out = (bf16 *)p.a.out + (int64_t)tok * p.a.out_stride + (int64_t)h * D;
-          float *po = p.part_o + (int64_t)(it.part + mine) * D;
-          if (store && it.part >= 0) p.part_lse[it.part + mine] = l > 0.f ? m + log2f(l) : -INFINITY;
+          const int at = it.part + mine * G + row_head;        // partial row
+          float *po = p.part_o + (int64_t)at * D;
+          if (own && it.part >= 0) p.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
@@ -806,22 +831,26 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               for (int j = 0; j < 32; ++j)
                 o[j] = __float_as_uint(__uint_as_float(o[j]) + (a1 != 0.f ? __uint_as_float(q[j]) * a1 : 0.f));
             }
-            if (!store) continue;
-            if (it.part >= 0) {
+            // 32 bytes a store: whole sectors, as a lane's rows are far apart
+            if (own && it.part >= 0) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4 *>(po + i + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-            } else {
+              for (int j = 0; j < 32; j += 8) store32(po + i + j, o + j);
+            } else if (own) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint32_t w[4];
+              for (int j = 0; j < 32; j += 16) {
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                   __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]),
                                                             __uint_as_float(o[j + 2 * e + 1]));
                   w[e] = *reinterpret_cast<uint32_t *>(&h2);
                 }
-                *reinterpret_cast<uint4 *>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (wide) {
+                  store32(out + i + j, w);
+                } else {
+                  *reinterpret_cast<uint4 *>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4 *>(out + i + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
               }
             }
           }
@@ -937,6 +966,18 @@ bool encode_pages(CUtensorMap *tm, const void *base, int n_pages, int kvh, int D
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows(CUtensorMap *tm, const void *q, int total_rows, int H, int D, int64_t stride, int G) {
+  EncodeTiledFn fn = encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)total_rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
   size_t head, items, req, row_req, part_o, part_lse, total;
   int64_t cap;
@@ -952,9 +993,10 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
     o += (bytes + 255) / 256 * 256;
     return at;
   };
-  const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows * (H / KVH) / ROWS + 1;
+  const int tpt = 128 / (H / KVH);
+  const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows / (2 * tpt) + 1;
   L.max_items = (int)(KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA);
-  L.cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * ROWS;
+  L.cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * 256;
   L.head = take(sizeof(Head));
   L.items = take(sizeof(Item) * L.max_items);
   L.req = take(sizeof(Request) * B);
@@ -971,7 +1013,8 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   Params p;
   memset(&p, 0, sizeof(p));
   if (!encode_pages(&p.tmK, a.k_pages, a.rows.n_pages, a.KVH, D) ||
-      !encode_pages(&p.tmV, a.v_pages, a.rows.n_pages, a.KVH, D))
+      !encode_pages(&p.tmV, a.v_pages, a.rows.n_pages, a.KVH, D) ||
+      !encode_rows(&p.tmQ, a.q, a.rows.total_rows, a.H, D, a.q_stride, a.H / a.KVH))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
@@ -987,7 +1030,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   p.max_items = L.max_items;
   p.sms = sms > 0 ? sms : 1;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
-  p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
+  p.negative = a.scale < 0.f;
   cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_attention_kernel<D>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
