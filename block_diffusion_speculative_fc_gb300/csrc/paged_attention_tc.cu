@@ -47,7 +47,9 @@ constexpr int THREADS = 384;
 constexpr int REGS_STREAM = 208, REGS_REST = 80;
 constexpr int PLAN_THREADS = 1024;
 constexpr int ITEMS_PER_SM = 3;           // what splits aim at
+constexpr int NQ = 4;                     // items known ahead in a CTA
 constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile)
+constexpr int BUCKETS = 128;              // sizes that the item list is ordered by
 constexpr float TAU = 8.f;
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
 
@@ -58,10 +60,10 @@ template <int D> struct Cfg {
   static constexpr int OFF_RING = 2 * Q_TILE;
   static constexpr int OFF_ML = OFF_RING + NSLOT * TILE;      // [128] float2
   static constexpr int OFF_BARS = OFF_ML + 128 * 8;
-  // full[NSLOT], empty[NSLOT], s_full[2], p_full[2], o_full[2], o_read[2], q_full, q_free,
-  // ml_full, ml_free, done
-  static constexpr int N_BARS = 2 * NSLOT + 13;
-  static constexpr int SMEM = 1024 + OFF_BARS + N_BARS * 8 + 16;
+  // full[NSLOT], empty[NSLOT], s_full[2], p_half[2], p_full[2], o_full[2], o_read[2], item_full[NQ],
+  // item_empty[NQ], q_full, q_free, ml_full, ml_free, done; then the queue entries and a word
+  static constexpr int N_BARS = 2 * NSLOT + 10 + 2 * NQ + 5;
+  static constexpr int SMEM = 1024 + OFF_BARS + N_BARS * 8 + NQ * 48 + 32;
   static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
 
@@ -76,7 +78,7 @@ struct Request {
 };
 struct Head {
   int items, merge, prefix_splits, prefix_tiles;
-  int first_row, rows, pad0, pad1;        // rows that meet the prefix
+  int first_row, rows, taken, pad;        // rows that meet the prefix; items handed out
 };
 
 struct Params {
@@ -182,6 +184,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<uint64_t *>(&d))
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+        "l"(*reinterpret_cast<uint64_t *>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<uint64_t *>(&d))
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return d;
+}
 __device__ __forceinline__ void store32(void *p, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -215,9 +232,9 @@ __device__ __forceinline__ int order_v(int t, int n, int ahead) {
   return min(ahead, n) + t + min(t, max(0, n - ahead));
 }
 
-__device__ __forceinline__ Item load_item(const Item *p) {
+__device__ __forceinline__ Item read_item(const int *p) {
   const int4 *s = reinterpret_cast<const int4 *>(p);
-  const int4 a = __ldg(s), b = __ldg(s + 1), c = __ldg(s + 2);
+  const int4 a = s[0], b = s[1], c = s[2];
   Item it;
   it.g = a.x, it.tok0 = a.y, it.ntok = a.z, it.req = a.w;
   it.page0 = b.x, it.ntiles = b.y, it.keys_left = b.z, it.part = b.w;
@@ -229,7 +246,7 @@ __device__ __forceinline__ Item load_item(const Item *p) {
 // One CTA: checks every request, chooses the key split of every segment (items
 // of at least U tile-units, U such that about ITEMS_PER_SM items an SM come
 // out; a unit is one 128-row tile), lays out partial rows and lists the items,
-// row tiles that see more keys first.
+// large ones first (the CTAs take them from the list one by one).
 __device__ __forceinline__ long long block_sum(long long v, long long *s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -286,6 +303,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   __shared__ int s_start[PLAN_THREADS], s_n[PLAN_THREADS], s_ctx[PLAN_THREADS], s_tiles[PLAN_THREADS];
   __shared__ int s_part[PLAN_THREADS], s_splits[PLAN_THREADS];
   __shared__ int s_lo, s_hi;
+  __shared__ int s_bucket[BUCKETS];             // items of a size, then the next place for one
   const PagedRows &r = p.a.rows;
   const int b = threadIdx.x, G = p.a.H / p.a.KVH, KVH = p.a.KVH, prefix = r.prefix_len;
   const int tpt = 128 / G;                      // tokens of a row tile
@@ -341,13 +359,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   if (b == 0) {
     s_first[0] = 0;
     Head h;
-    h.items = total_items;
+    h.items = 0;                                // set below
     h.prefix_splits = spp.splits;
     h.prefix_tiles = spp.tiles;
     h.first_row = lo;
     h.rows = rows;
     h.merge = total_rows > 0;
-    h.pad0 = h.pad1 = 0;
+    h.taken = h.pad = 0;
     *p.head = h;
   }
   s_start[b] = start;
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     p.req[b] = q;
   }
   __syncthreads();
-  for (int i = b; i < total_items; i += PLAN_THREADS) {
+  auto item_at = [&](int i) {
     // last segment whose first item is <= i (empty segments share a first item)
     int s0 = 0, s1 = r.B;
     while (s0 < s1) {
@@ -387,8 +405,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       it.lim_slope = 0;
     } else {
       const int q = s0 - 1, ns = s_splits[q], tiles = s_tiles[q], nq = s_n[q], c = s_ctx[q], st = s_start[q];
-      const int Rq = nq * G, per = KVH * ns, nt = ceil_div(nq, 2 * tpt);
-      const int rt = nt - 1 - j / per, g = j % per / ns, s = j % ns;
+      const int Rq = nq * G, per = KVH * ns;
+      const int rt = j / per, g = j % per / ns, s = j % ns;
       const int last = min(nq, (rt + 1) * 2 * tpt) - 1;        // last token of the row tiles
       const int seen = p.a.causal ? c + last + 1 : c + nq;
       it.g = g;
@@ -403,7 +421,33 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       it.lim_base = (p.a.causal ? c + 1 - st : c + nq) - s * tiles * KT;
     }
     it.pad0 = it.pad1 = 0;
-    p.items[i] = it;
+    return it;
+  };
+  // larger items first (in units of half a row tile, so that a lone row tile counts three: its
+  // products have half the rows but its K/V tiles are its own)
+  auto bucket_of = [&](const Item &it) {
+    const int size = it.ntiles * (it.ntok > tpt ? 4 : 3);
+    return BUCKETS - 1 - min(BUCKETS - 1, size <= 64 ? size : 64 + (size - 64) / 16);
+  };
+  for (int i = b; i < BUCKETS; i += PLAN_THREADS) s_bucket[i] = 0;
+  __syncthreads();
+  for (int i = b; i < total_items; i += PLAN_THREADS) {
+    const Item it = item_at(i);
+    if (it.ntiles > 0) atomicAdd(&s_bucket[bucket_of(it)], 1);
+  }
+  __syncthreads();
+  int listed = 0;
+  {
+    const int v = b < BUCKETS ? s_bucket[b] : 0;
+    const int at = block_scan(v, s_scan, listed);
+    __syncthreads();
+    if (b < BUCKETS) s_bucket[b] = at;
+  }
+  __syncthreads();
+  if (b == 0) p.head->items = listed;
+  for (int i = b; i < total_items; i += PLAN_THREADS) {
+    const Item it = item_at(i);
+    if (it.ntiles > 0) p.items[atomicAdd(&s_bucket[bucket_of(it)], 1)] = it;
   }
   if (total_rows > 0) {   // the owner of every row, for the join
     for (int t = b; t < r.total_rows; t += PLAN_THREADS) p.row_req[t] = -1;
@@ -423,10 +467,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   uint8_t *ring = smem + C::OFF_RING;
   float2 *s_ml = (float2 *)(smem + C::OFF_ML);
   uint64_t *full = (uint64_t *)(smem + C::OFF_BARS), *empty = full + NS;
-  uint64_t *s_full = empty + NS, *p_full = s_full + 2, *o_full = p_full + 2, *o_read = o_full + 2;
-  uint64_t *q_full = o_read + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *ml_free = ml_full + 1;
+  uint64_t *s_full = empty + NS, *p_half = s_full + 2, *p_full = p_half + 2, *o_full = p_full + 2;
+  uint64_t *o_read = o_full + 2, *item_full = o_read + 2, *item_empty = item_full + NQ;
+  uint64_t *q_full = item_empty + NQ, *q_free = q_full + 1, *ml_full = q_free + 1, *ml_free = ml_full + 1;
   uint64_t *done = ml_free + 1;
-  uint32_t *s_tmem = (uint32_t *)(done + 1);
+  int *s_items = (int *)(((uintptr_t)(done + 1) + 15) & ~(uintptr_t)15);   // [NQ][12]
+  uint32_t *s_tmem = (uint32_t *)(s_items + NQ * 12);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.a.H / p.a.KVH, tpt = 128 / G, rt_rows = tpt * G;   // tokens and rows of a row tile
 
@@ -437,9 +483,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 128);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_read[i], 128);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 9);       // a lane of the MMA warp and of each stream warp
     }
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -465,15 +516,18 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   pdl_wait();
   const int n_items = __ldg(&p.head->items);
   bool ok = true;
-  // the CTA's items in order, empty ones left out; false at the end
-  int next_index = blockIdx.x;
+  // consumers: the CTA's i-th item (a warp's wait); false at the end or after a timeout
+  uint32_t n_item = 0;
   auto next_item = [&](Item &it) {
-    while (next_index < n_items) {
-      it = load_item(p.items + next_index);
-      next_index += gridDim.x;
-      if (it.ntiles > 0) return true;
-    }
-    return false;
+    const int e = n_item % NQ;
+    if (ok && !mbar_wait(&item_full[e], (n_item / NQ) & 1)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = read_item(s_items + e * 12);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[e]);
+    ++n_item;
+    return it.ntiles > 0;
   };
 
   if (warp >= 8) {
@@ -484,7 +538,27 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       int slot = 0, phase = 1;              // place in the ring; parity of its empty barrier
       Item it;
       int prev0 = 0, prev1 = 0, cur0 = 0, cur1 = 0;   // pages of the last two K tiles
-      while (ok && next_item(it)) {
+      // the next item of the list, to the other warps as well (0 tiles: no more)
+      auto take_item = [&] {
+        const int e = n_item % NQ;
+        int idx = 0;
+        if (lane == 0) {
+          if (!mbar_wait(&item_empty[e], ((n_item / NQ) & 1) ^ 1)) idx = -1;
+          else idx = atomicAdd(&p.head->taken, 1);
+        }
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        if (idx < 0) {
+          ok = false;
+          return false;
+        }
+        if (lane < 12) s_items[e * 12 + lane] = idx < n_items ? __ldg((const int *)(p.items + idx) + lane) : 0;
+        __syncwarp();
+        it = read_item(s_items + e * 12);
+        if (lane == 0) mbar_arrive(&item_full[e]);
+        ++n_item;
+        return it.ntiles > 0;
+      };
+      while (ok && take_item()) {
         const int n = it.ntiles, ahead = it.ntok > tpt ? 1 : 2;
         const int npages = (min(it.keys_left, n * KT) + kPageRows - 1) / kPageRows;
         const int *list = (it.req < 0 ? p.a.rows.prefix_pages
@@ -627,8 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         for (int i = 0; i < steps && ok; ++i) {
           const int x = i & 1, t = i >> pair;
           const bool last = x == 1 || !pair;
-          wait(&p_full[x], (p_par >> x) & 1);
-          p_par ^= 1u << x;
+          wait(&p_half[x], (p_par >> x) & 1);
           if (t < ahead) {                // the item before has read this stream's O
             if ((o_used >> x) & 1) wait(&o_read[x], (o_par >> x) & 1);
             o_used |= 1u << x;
@@ -640,9 +713,20 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (elected()) {
             const uint64_t vd = v_desc + slot * (C::TILE >> 4);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
+            for (int kk = 0; kk < KT / 32; ++kk)
               umma_ts(tmem + 256 + x * 128, tmem + x * KT + kk * 8, vd + kk * (2048 >> 4), ID_O,
                       (t < ahead && kk == 0) ? 0u : 1u);
+          }
+          __syncwarp();
+          wait(&p_full[x], (p_par >> x) & 1);
+          p_par ^= 1u << x;
+          if (!ok) break;
+          tc_fence_after();
+          if (elected()) {
+            const uint64_t vd = v_desc + slot * (C::TILE >> 4);
+#pragma unroll
+            for (int kk = KT / 32; kk < KT / 16; ++kk)
+              umma_ts(tmem + 256 + x * 128, tmem + x * KT + kk * 8, vd + kk * (2048 >> 4), ID_O, 1u);
             if (last) umma_commit(&empty[slot]);
             if (t + ahead >= n) umma_commit(&o_full[x]);
           }
@@ -677,10 +761,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     };
     uint32_t c = 0, u = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
     const int row_tok = row / G, row_head = row % G;
-    Item it, nit;
-    bool have = next_item(it);
-    while (have) {
-      const bool more = next_item(nit);
+    Item it;
+    while (ok && next_item(it)) {
       const int n = it.ntiles;
       const bool pair = it.ntok > tpt;
       const int ahead = pair ? 1 : 2;
@@ -690,6 +772,19 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       const int tok = it.tok0 + mine, h = it.g * G + row_head;
       const int lim = own ? it.lim_base + it.lim_slope * tok : 0;
       float m = -INFINITY, l = 0.f;
+      // V rows past the segment's last key may hold anything: 0 times it has to be 0
+      auto clear_v = [&](int t) {
+        if (t != n - 1 || it.keys_left >= n * KT) return;
+        const int ov = u + order_v(t, n, ahead);
+        wait(&full[ov % NS], (ov / NS) & 1);
+        if (!ok) return;
+        uint8_t *vt = ring + (ov % NS) * C::TILE;
+        for (int i = (it.keys_left - t * KT) * 8 + row; i < KT * 8; i += 128)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+      };
       for (int t = pair ? 0 : x; t < n && ok; t += pair ? 1 : 2) {
         wait(&s_full[x], c & 1);
         if (!ok) break;
@@ -741,42 +836,39 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               tmem_st32(tmem + lanes + 256 + x * 128 + i, o);
             }
           }
+          clear_v(t);
           const float mm = m == -INFINITY ? 0.f : m;
-          float l0 = 0.f, l1 = 0.f;
+          const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int e = half * 64 + 2 * i;
-              float p0 = ex2(fmaf(__uint_as_float(sv[e]), sl, -mm));
-              float p1 = ex2(fmaf(__uint_as_float(sv[e + 1]), sl, -mm));
+              const float2 a = fma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2, mm2);
+              float2 q = make_float2(ex2(a.x), ex2(a.y));
               if (!whole) {
-                p0 = e < vis ? p0 : 0.f;
-                p1 = e + 1 < vis ? p1 : 0.f;
+                q.x = e < vis ? q.x : 0.f;
+                q.y = e + 1 < vis ? q.y : 0.f;
               }
-              l0 += p0;
-              l1 += p1;
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+              sum = add2(sum, q);
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
               w[i] = *reinterpret_cast<uint32_t *>(&h2);
             }
             tmem_st32(t_s + half * 32, w);
+            if (half == 0) {               // the first half of the keys may go
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&p_half[x]);
+            }
           }
-          l = fmaf(l, alpha, l0 + l1);
+          l = fmaf(l, alpha, sum.x + sum.y);
           tmem_st_wait();
-        }
-        if (t == n - 1 && it.keys_left < n * KT) {
-          // V rows past the segment's last key may hold anything: 0 times it has to be 0
-          const int ov = u + order_v(t, n, ahead);
-          wait(&full[ov % NS], (ov / NS) & 1);
-          if (!ok) break;
-          uint8_t *vt = ring + (ov % NS) * C::TILE;
-          const int v0 = it.keys_left - t * KT;
-          for (int i = v0 * 8 + row; i < KT * 8; i += 128)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
+        } else {
+          clear_v(t);
+          tc_fence_before();
+          mbar_arrive(&p_half[x]);
         }
         tc_fence_before();
         mbar_arrive(&p_full[x]);
@@ -862,8 +954,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // streams that took part in this item
       o_par ^= pair || n > 1 ? 3u : 1u;
       if (both) ++n_ml;
-      it = nit;
-      have = more;
     }
     if (!ok && lane == 0) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
   }
