@@ -5,7 +5,7 @@
 // keys; the rows of a batch fall into segments that share their keys: the
 // shared prefix (the rows of all requests) and each request's own rows (its
 // rows).  A work item is up to 256 rows of a segment times a range of 128-key
-// tiles.  Partial results (o / l, log2 of the weight) of a
+// tiles (two cache pages).  Partial results (o / l, log2 of the weight) of a
 // row that several items hold are joined by a last launch.
 //
 // The softmax is the running one: tile by tile S = Q K^T, w = 2^(S c - m), O +=
@@ -21,13 +21,9 @@
 // hold a row tile each and share every K/V tile (32 bytes of K/V per SM clock at
 // full tensor rate; one row tile would need the 64 that L2 can just deliver).  With
 // fewer, both hold the same rows and take even and odd tiles, which halves the
-// serial chain of a tile: those items are bound by the K/V bytes.  A tile is
-// one page of 64 keys and a stream has two S buffers, so that S of the next
-// tile is there when the softmax of one ends (with one buffer of 128 keys the
-// chain S - softmax - product set the pace: 4900 clocks for 256 rows x 128
-// keys, of which the products took 2060).  S and the rounded weights w share
-// their TMEM columns (w is the second product's A operand, read from TMEM; V
-// is read as staged, keys by dims).
+// serial chain of a tile: those items are bound by the K/V bytes.  S and the
+// rounded weights w share their TMEM columns (w is the second product's A
+// operand, read from TMEM; V is read as staged, keys by dims).
 //
 // Warps 0-3, 4-7: the streams; 8: TMA producer (a ring of K and V tiles, one
 // copy per page and 64 dims); 9, 10: issue the MMAs of a stream each; 11
@@ -44,30 +40,33 @@
 namespace dflash {
 namespace {
 
-constexpr int KT = kPageRows;             // keys of a tile: one page
+constexpr int KT = 128;                   // keys of a tile
 constexpr int THREADS = 384;
 // registers a thread: 168 at launch (384 threads), then 208 for the streams and 80 for the rest
 // (256 * 208 + 128 * 80 <= 384 * 168)
 constexpr int REGS_STREAM = 208, REGS_REST = 80;
 constexpr int PLAN_THREADS = 1024;
-constexpr int MIN_UNITS = 4;              // of an item (a unit: a row tile times a page)
 constexpr int ITEMS_PER_SM = 3;           // what splits aim at
 constexpr int NQ = 4;                     // items known ahead in a CTA
 constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile)
 constexpr int BUCKETS = 128;              // sizes that the item list is ordered by
+// The weights of a tile go to the upper half of its S columns, so that the lower half can be read
+// a second time.
+constexpr int P_COL = KT / 2;
 constexpr float TAU = 8.f;
-constexpr uint32_t WAIT_LIMIT = 1u << 22;
+constexpr uint32_t WAIT_NS = 20000;       // longest sleep of one try
+constexpr uint32_t WAIT_LIMIT = 1u << 16; // tries (about a second)
 
 template <int D> struct Cfg {
   static constexpr int TILE = KT * D * 2;             // K (or V) tile
-  static constexpr int NSLOT = D == 128 ? 10 : 20;
+  static constexpr int NSLOT = D == 128 ? 5 : 10;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int OFF_RING = 2 * Q_TILE;
   static constexpr int OFF_ML = OFF_RING + NSLOT * TILE;      // [128] float2
   static constexpr int OFF_BARS = OFF_ML + 128 * 8;
-  // full[NSLOT], empty[NSLOT], s_full[4], p_full[4], o_done[2], o_full[2], o_read[2], item_full[NQ],
+  // full[NSLOT], empty[NSLOT], s_full[2], turn[2], p_full[2], o_full[2], o_read[2], item_full[NQ],
   // item_empty[NQ], q_full, q_free, ml_full, ml_free, done; then the queue entries and a word
-  static constexpr int N_BARS = 2 * NSLOT + 14 + 2 * NQ + 5;
+  static constexpr int N_BARS = 2 * NSLOT + 10 + 2 * NQ + 5;
   static constexpr int SMEM = 1024 + OFF_BARS + N_BARS * 8 + NQ * 48 + 32;
   static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
@@ -108,23 +107,26 @@ __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t *b, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(count) : "memory");
+}
 __device__ __forceinline__ bool mbar_try(uint32_t b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(b), "r"(parity)
+      : "r"(b), "r"(parity), "r"(WAIT_NS)
       : "memory");
   return ok != 0;
 }
-// Bounded wait for the phase of parity `parity`; false = gave up.
+// Bounded wait for the phase of parity `parity`; false = gave up.  The thread
+// sleeps in the barrier: eight warps that polled took a quarter of the shared
+// memory bandwidth that the products need.
 __device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity) {
-  for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
+  for (uint32_t i = 0; i < WAIT_LIMIT; ++i)
     if (mbar_try(b, parity)) return true;
-    if (i > 64) __nanosleep(64);
-  }
   return false;
 }
 __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity) { return mbar_wait(su32(b), parity); }
@@ -237,10 +239,14 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 
-// Place of V(t) in an item's load order: the first `ahead` K tiles, then V(0),
-// K(ahead), V(1), K(ahead + 1), ...
+// Places of V(t) and K(t) in an item's load order: the first `ahead` K tiles,
+// then V(0), K(ahead), V(1), K(ahead + 1), ...
 __device__ __forceinline__ int order_v(int t, int n, int ahead) {
   return min(ahead, n) + t + min(t, max(0, n - ahead));
+}
+
+__device__ __forceinline__ int order_k(int t, int n, int ahead) {
+  return t < ahead ? t : order_v(t - ahead, n, ahead) + 1;
 }
 
 __device__ __forceinline__ Item read_item(const int *p) {
@@ -343,11 +349,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   __syncthreads();
   const int lo = s_lo, rows = max(0, s_hi - s_lo);
   const int R = n * G, keys = ctx + n, nkt = n > 0 ? (keys + KT - 1) / KT : 0;
-  const int Rp = prefix > 0 ? rows * G : 0, nktp = Rp > 0 ? prefix / KT : 0;
+  const int Rp = prefix > 0 ? rows * G : 0, nktp = Rp > 0 ? prefix / KT + (prefix % KT != 0) : 0;
   const long long W = block_sum((long long)KVH * nkt * ceil_div(n, tpt), s_sum) +
                       (long long)KVH * nktp * ceil_div(rows, tpt);
   long long U = (W + (long long)ITEMS_PER_SM * p.sms - 1) / ((long long)ITEMS_PER_SM * p.sms);
-  U = U < MIN_UNITS ? MIN_UNITS : U;
+  U = U < 2 ? 2 : U;
   Split sp, spp;
   int part = 0, items = 0, total_rows = 0, total_items = 0;
   bool joined = false;
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       it.tok0 = lo + rt * 2 * tpt;
       it.ntok = min(2 * tpt, rows - rt * 2 * tpt);
       it.req = -1;
-      it.page0 = s * spp.tiles;
+      it.page0 = s * spp.tiles * 2;
       it.ntiles = min(spp.tiles, nktp - s * spp.tiles);
       it.keys_left = prefix - s * spp.tiles * KT;
       it.part = (g * spp.splits + s) * Rp + rt * 2 * tpt * G;
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       it.tok0 = st + rt * 2 * tpt;
       it.ntok = min(2 * tpt, nq - rt * 2 * tpt);
       it.req = q;
-      it.page0 = s * tiles;
+      it.page0 = s * tiles * 2;
       it.ntiles = max(0, min(tiles, (seen + KT - 1) / KT - s * tiles));
       it.keys_left = c + nq - s * tiles * KT;
       it.part = s_part[q] >= 0 ? s_part[q] + (g * ns + s) * Rq + rt * 2 * tpt * G : -1;
@@ -478,8 +484,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   uint8_t *ring = smem + C::OFF_RING;
   float2 *s_ml = (float2 *)(smem + C::OFF_ML);
   uint64_t *full = (uint64_t *)(smem + C::OFF_BARS), *empty = full + NS;
-  uint64_t *s_full = empty + NS, *p_full = s_full + 4, *o_done = p_full + 4;   // [stream][buffer]
-  uint64_t *o_full = o_done + 2, *o_read = o_full + 2, *item_full = o_read + 2, *item_empty = item_full + NQ;
+  uint64_t *s_full = empty + NS, *turn = s_full + 2, *p_full = turn + 2, *o_full = p_full + 2;
+  uint64_t *o_read = o_full + 2, *item_full = o_read + 2, *item_empty = item_full + NQ;
   uint64_t *q_full = item_empty + NQ, *q_free = q_full + 1, *ml_full = q_free + 1, *ml_free = ml_full + 1;
   uint64_t *done = ml_free + 1;
   int *s_items = (int *)(((uintptr_t)(done + 1) + 15) & ~(uintptr_t)15);   // [NQ][12]
@@ -490,14 +496,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 2);            // two uses, see the MMA issuers
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&empty[i], 2);            // released by both streams, or twice by the one that used it
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&o_done[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_read[i], 128);
     }
@@ -550,6 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       uint32_t u = 0, k = 0;                // tiles issued, items begun
       int slot = 0, phase = 1;              // place in the ring; parity of its empty barrier
       Item it;
+      int prev0 = 0, prev1 = 0, cur0 = 0, cur1 = 0;   // pages of the last two K tiles
       // the next item of the list, to the other warps as well (0 tiles: no more)
       auto take_item = [&] {
         const int e = n_item % NQ;
@@ -571,21 +576,26 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         return it.ntiles > 0;
       };
       while (ok && take_item()) {
-        const int n = it.ntiles, ahead = it.ntok > tpt ? 2 : 4;
+        const int n = it.ntiles, ahead = it.ntok > tpt ? 1 : 2;
+        const int npages = (min(it.keys_left, n * KT) + kPageRows - 1) / kPageRows;
         const int *list = (it.req < 0 ? p.a.rows.prefix_pages
                                       : p.a.rows.page_table + (int64_t)it.req * p.a.rows.pages_per_req) + it.page0;
-        int batch = 0, before = 0;          // pages 32 i + lane of the K tiles' i and of the one before
-        auto issue = [&](const CUtensorMap *tm, int page) {
+        int batch = 0;
+        auto issue = [&](const CUtensorMap *tm, int t, int pg0, int pg1) {
           bool good = true;
           if (lane == 0) {
             good = mbar_wait(&empty[slot], phase);
             if (good) {
+              const bool two = 2 * t + 1 < npages;
               asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&full[slot])),
-                           "r"(C::TILE)
+                           "r"(two ? C::TILE : C::TILE / 2)
                            : "memory");
+              uint8_t *dst = ring + slot * C::TILE;
 #pragma unroll
-              for (int c = 0; c < NB; ++c)
-                tma3(ring + slot * C::TILE + c * (KT * 128), tm, &full[slot], 64 * c, it.g, page * kPageRows);
+              for (int c = 0; c < NB; ++c) {
+                tma3(dst + c * (KT * 128), tm, &full[slot], 64 * c, it.g, pg0 * kPageRows);
+                if (two) tma3(dst + c * (KT * 128) + 8192, tm, &full[slot], 64 * c, it.g, pg1 * kPageRows);
+              }
             }
           }
           ok = __shfl_sync(0xffffffffu, good, 0) != 0;
@@ -597,11 +607,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           }
         };
         auto issue_k = [&](int t) {
-          if (t % 32 == 0) {
-            before = batch;
+          const int j = 2 * t;
+          if (j % 32 == 0) {                // the next 32 pages, one a lane
             int pg = 0;
-            if (t + lane < n) {
-              pg = __ldg(list + t + lane);
+            if (j + lane < npages) {
+              pg = __ldg(list + j + lane);
               if (pg < 0 || pg >= p.a.rows.n_pages) {
                 raise_error(p.a.err, DFLASH_DERR_PAGE_RANGE);
                 pg = 0;
@@ -609,7 +619,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             }
             batch = pg;
           }
-          issue(&p.tmK, __shfl_sync(0xffffffffu, batch, t % 32));
+          prev0 = cur0, prev1 = cur1;
+          cur0 = __shfl_sync(0xffffffffu, batch, j % 32);
+          cur1 = __shfl_sync(0xffffffffu, batch, j % 32 + 1);
+          issue(&p.tmK, t, cur0, cur1);
         };
         // the query rows, once the last S of the item before has read its own
         auto issue_q = [&] {
@@ -634,10 +647,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         for (int t = 0; t < min(ahead, n) && ok; ++t) issue_k(t);
         if (ok) issue_q();
         for (int t = 0; t < n && ok; ++t) {
-          const int last_k = min(n, t + ahead) - 1;            // the last K tile issued
-          const int page_new = __shfl_sync(0xffffffffu, batch, t % 32);
-          const int page_old = __shfl_sync(0xffffffffu, before, t % 32);
-          issue(&p.tmV, t / 32 == last_k / 32 ? page_new : page_old);
+          // K(t) is the last K tile issued, or the one before it
+          const bool older = ahead == 2 && t + 1 < n;
+          issue(&p.tmV, t, older ? prev0 : cur0, older ? prev1 : cur1);
           if (ok && t + ahead < n) issue_k(t + ahead);
         }
       }
@@ -648,84 +660,89 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (k > 0) mbar_wait(q_full, (k - 1) & 1);
       }
     } else if (warp <= 10) {
-      // ------------------------------------------------------------ MMA issuers: a warp a stream
-      // One lane issues.  (One warp for both streams took 1750 clocks a step of 640 clocks of
-      // products: the waits and addresses of a step cost more than its products.)
-      const int x = warp - 9;
+      // ------------------------------------------------------------ MMA issuers: a lane a stream
+      // Groups of MMAs alternate between the streams (a token goes back and forth), which keeps
+      // them out of phase: one's softmax runs while the other's products do.  Without the token
+      // the two fall into step, both S ready at once, then both in the softmax and the tensor
+      // cores idle; one issuer for both needs 2300 clocks a step, half of them for waits and
+      // addresses.  Commits cost the tensor pipe 40 to 80 clocks each, so a step has one: S of the
+      // stream's next tile, after which the tiles that the step has read are released by the
+      // stream that waits for that S.
+      const uint32_t x = warp - 9;
       if (lane == 0) {
         constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
         const uint64_t k_desc = desc_k(su32(ring)), v_desc = desc_mn(su32(ring), KT * 128);
-        const uint32_t full_at = su32(full), t_s = tmem + x * 128, t_o = tmem + 256 + x * 128;
-        uint32_t u = 0, k = 0, c = 0;     // ring tiles, items, tiles of this stream before
-        uint32_t n_o = 0;                 // items of this stream before
+        const uint32_t full_at = su32(full), p_at = su32(&p_full[x]);
+        const uint32_t t_s = tmem + x * KT, t_o = tmem + 256 + x * 128;
+        uint32_t k = 0, u = 0, c = 0;     // items, ring tiles, tiles of this stream before
+        uint32_t n_o = 0, n_turn = 0;     // items of this stream, tokens received before
+        int owner = 0;                    // stream of the group before
         auto wait = [&](uint32_t bar, uint32_t parity) {
           if (mbar_try(bar, parity)) return;
           if (ok && !mbar_wait(bar, parity)) ok = false;
         };
-        uint32_t qn = 0;
+        auto take_turn = [&] { wait(su32(&turn[x]), n_turn++ & 1); };
         Item it;
         while (ok) {
-          const int e = qn % NQ;
-          wait(su32(&item_full[e]), (qn / NQ) & 1);
+          const int e = k % NQ;
+          wait(su32(&item_full[e]), (k / NQ) & 1);
           if (!ok) break;
           it = read_item(s_items + e * 12);
           mbar_arrive(&item_empty[e]);
-          ++qn;
           if (it.ntiles == 0) break;
           // The stream's tiles t0, t0 + dt, ...: all of a pair's, every other one of a single row
-          // tile's.  A step is O += w V(t), then S of tile t + ahead into the buffer that w leaves
-          // (the first S before).  Every ring tile counts two uses: one of each stream, or both
-          // of the one that takes it.
-          const int n = it.ntiles, pair = it.ntok > tpt ? 1 : 0, ahead = 4 >> pair;
-          const int t0 = pair ? 0 : x, dt = 2 - pair;
+          // tile's.  Groups: S of stream 0's first tile, of stream 1's, then step by step O += w V(t)
+          // and S of the stream's next tile; streams 0, 1, 0, ... in both kinds.
+          const int n = it.ntiles, pair = it.ntok > tpt ? 1 : 0, dt = 2 - pair, t0 = pair ? 0 : (int)x;
+          const bool two = (n << pair) > 1;                    // stream 1 has tiles
+          const int last_owner = ((n << pair) - 1) & 1;
           const uint64_t q_desc = desc_k(su32(smem) + (pair & x) * C::Q_TILE);
-          auto slot_of = [&](int order) { return (u + order) % NS; };
-          auto parity_of = [&](int order) { return ((u + order) / NS) & 1; };
-          auto used = [&](uint32_t slot) {
-            umma_commit(&empty[slot]);
-            if (!pair) umma_commit(&empty[slot]);
-          };
-          auto issue_s = [&](int t, int order, uint32_t buf) {
-            const uint32_t slot = slot_of(order);
-            wait(full_at + 8 * slot, parity_of(order));
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t kd = k_desc + slot * (C::TILE >> 4);
+          auto wait_tile = [&](int order) { wait(full_at + 8 * ((u + order) % NS), ((u + order) / NS) & 1); };
+          auto issue_s = [&](int order) {
+            const uint64_t kd = k_desc + ((u + order) % NS) * (C::TILE >> 4);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
-              umma_ss(t_s + buf * KT, q_desc + (i >> 2) * ((128 * 128) >> 4) + 2 * (i & 3),
+              umma_ss(t_s, q_desc + (i >> 2) * ((128 * 128) >> 4) + 2 * (i & 3),
                       kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3), ID_S, i ? 1u : 0u);
-            umma_commit(&s_full[2 * x + buf]);
-            used(slot);
-            if (t + dt >= n) umma_commit(q_free);
+            umma_commit(&s_full[x]);
           };
           wait(su32(q_full), k & 1);
           ++k;
-          if (t0 >= n) mbar_arrive(q_free);
-          for (int t = t0, b = c & 1; t < min(n, ahead) && ok; t += dt, b ^= 1) issue_s(t, t, b);
+          if (t0 < n) {
+            const int order = order_k(t0, n, dt);
+            wait_tile(order);
+            if (x == 1 || owner == 1) take_turn();
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(order);
+            if (two) mbar_arrive(&turn[x ^ 1]);
+          }
 #pragma unroll 1
-          for (int t = t0; t < n && ok; t += dt) {
-            const uint32_t b = c & 1;
-            const int order = order_v(t, n, ahead);
-            const uint32_t slot = slot_of(order);
-            wait(su32(&p_full[2 * x + b]), (c >> 1) & 1);
+          for (int t = t0; t < n; t += dt) {
+            const int order = order_v(t, n, dt);
+            const uint64_t vd = v_desc + ((u + order) % NS) * (C::TILE >> 4);
+            const bool more = t + dt < n;
             if (t == t0) {                // the item before has read this stream's O
               if (n_o > 0) wait(su32(&o_read[x]), (n_o - 1) & 1);
               ++n_o;
             }
-            wait(full_at + 8 * slot, parity_of(order));
-            if (!ok) break;
+            wait_tile(order);
+            if (more) wait_tile(order + 1);
+            wait(p_at, c & 1);
             ++c;
+            if (two) take_turn();
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = v_desc + slot * (C::TILE >> 4);
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-              umma_ts(t_o, t_s + b * KT + kk * 8, vd + kk * (2048 >> 4), ID_O, (t == t0 && kk == 0) ? 0u : 1u);
-            umma_commit(&o_done[x]);
-            used(slot);
-            if (t + dt >= n) umma_commit(&o_full[x]);
-            if (t + ahead < n) issue_s(t + ahead, order + 1, b);
+              umma_ts(t_o, t_s + P_COL + kk * 8, vd + kk * (2048 >> 4), ID_O, (t == t0 && kk == 0) ? 0u : 1u);
+            if (more) issue_s(order + 1);
+            else umma_commit(&o_full[x]);
+            // the other stream's step, or after the item's last the next item's first group, stream 0's
+            if (two && (x == 1 || more || !(last_owner == 0))) mbar_arrive(&turn[x ^ 1]);
           }
+          if (!ok) break;
+          owner = last_owner;
           u += 2 * n;
         }
         umma_commit(done);
@@ -738,7 +755,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     // ------------------------------------------------------------ softmax, a row a thread
     const int x = warp >> 2, row = threadIdx.x & 127;          // stream, row of its tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
+    const uint32_t t_s = tmem + lanes + x * KT;
     const float sl = p.scale_log2;
     const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
     // every wait is one for the warp, so that its lanes stay together
@@ -746,114 +763,129 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       if (ok && !mbar_wait(b, parity)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
-    uint32_t c = 0, u = 0, n_ml = 0;      // tiles of this stream, ring tiles, exchanges before
-    uint32_t o_par = 0;                   // bit x: parity of o_full[x]
+    uint32_t c = 0, u = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
     const int row_tok = row / G, row_head = row % G;
     Item it;
     while (ok && next_item(it)) {
       const int n = it.ntiles;
       const bool pair = it.ntok > tpt;
-      const int ahead = pair ? 2 : 4;
+      const int ahead = pair ? 1 : 2;
       const int mine = (pair ? x * tpt : 0) + row_tok;         // this thread's token of the item
       const bool own = row < rt_rows && mine < it.ntok;
       const bool live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
       const int tok = it.tok0 + mine, h = it.g * G + row_head;
       const int lim = own ? it.lim_base + it.lim_slope * tok : 0;
       float m = -INFINITY, l = 0.f;
+      const uint32_t uses = pair ? 1 : 2;   // of a tile by this stream, of the two that free it
+      auto release = [&](int order) { mbar_arrive(&empty[(u + order) % NS], uses); };
+      // V rows past the segment's last key may hold anything: 0 times it has to be 0
+      auto clear_v = [&](int t) {
+        if (t != n - 1 || it.keys_left >= n * KT) return;
+        const int ov = u + order_v(t, n, ahead);
+        wait(&full[ov % NS], (ov / NS) & 1);
+        if (!ok) return;
+        uint8_t *vt = ring + (ov % NS) * C::TILE;
+        for (int i = (it.keys_left - t * KT) * 8 + row; i < KT * 8; i += 128)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+      };
       for (int t = pair ? 0 : x; t < n && ok; t += pair ? 1 : 2) {
-        const int b = c & 1;
-        wait(&s_full[2 * x + b], (c >> 1) & 1);
+        wait(&s_full[x], c & 1);
         if (!ok) break;
+        ++c;
         tc_fence_after();
+        if (row == 0) {                    // S has read K(t), and the product before it its V
+          release(order_k(t, n, ahead));
+          if (t >= ahead) release(order_v(t - ahead, n, ahead));
+          if (t + ahead >= n) mbar_arrive(q_free, !pair && n == 1 ? 2 : 1);   // its last S
+        }
         if (live) {
-          uint32_t sv[KT];
+          // keys 0..63 for their maximum, then keys 64..127 and their weights, then keys 0..63 again: reading TMEM twice is cheaper than 128 live registers
+          uint32_t sv[KT / 2];
+          auto load = [&](int half) {
+            tmem_ld32(t_s + half * 64, sv);
+            tmem_ld32(t_s + half * 64 + 32, sv + 32);
+            tmem_ld_wait();
+            if (p.negative) {
 #pragma unroll
-          for (int i = 0; i < KT; i += 32) tmem_ld32(t_s + b * KT + i, sv + i);
-          tmem_ld_wait();
-          if (p.negative) {
-#pragma unroll
-            for (int i = 0; i < KT; ++i) sv[i] ^= 0x80000000u;
-          }
+              for (int i = 0; i < 64; ++i) sv[i] ^= 0x80000000u;
+            }
+          };
           const int vis = lim - t * KT;                        // visible keys of this tile
           const bool whole = __all_sync(0xffffffffu, vis >= KT);
-          float mx;
-          if (whole) {
-            float a0 = __uint_as_float(sv[0]), a1 = __uint_as_float(sv[1]);
-            float a2 = __uint_as_float(sv[2]), a3 = __uint_as_float(sv[3]);
+          auto maximum = [&](int half, float a0) {
+            if (whole) {
+              float a1 = __uint_as_float(sv[0]), a2 = __uint_as_float(sv[1]), a3 = __uint_as_float(sv[2]);
+              a0 = fmaxf(a0, __uint_as_float(sv[3]));
 #pragma unroll
-            for (int i = 4; i < KT - 4; i += 8) {
-              a0 = max3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-              a1 = max3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-              a2 = max3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
-              a3 = max3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+              for (int i = 4; i < 60; i += 8) {
+                a0 = max3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+                a1 = max3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+                a2 = max3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
+                a3 = max3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+              }
+              a0 = max3(a0, __uint_as_float(sv[60]), __uint_as_float(sv[61]));
+              a1 = max3(a1, __uint_as_float(sv[62]), __uint_as_float(sv[63]));
+              return max3(fmaxf(a0, a1), a2, a3);
             }
-            a0 = max3(a0, __uint_as_float(sv[KT - 4]), __uint_as_float(sv[KT - 3]));
-            a1 = max3(a1, __uint_as_float(sv[KT - 2]), __uint_as_float(sv[KT - 1]));
-            mx = max3(fmaxf(a0, a1), a2, a3) * sl;
-          } else {
-            mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < KT; ++i) mx = i < vis ? fmaxf(mx, __uint_as_float(sv[i])) : mx;
-            mx = vis > 0 ? mx * sl : -INFINITY;
-          }
+            for (int i = 0; i < 64; ++i) a0 = half * 64 + i < vis ? fmaxf(a0, __uint_as_float(sv[i])) : a0;
+            return a0;
+          };
+          load(0);
+          float mx = maximum(0, -INFINITY);
+          load(1);
+          mx = maximum(1, mx);
+          mx = vis > 0 ? mx * sl : -INFINITY;
           float alpha = 1.f;
           if (mx > m + TAU || m == -INFINITY) {
             if (m != -INFINITY) alpha = ex2(m - mx);
             m = mx;
           }
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-            // once the product of the tile before is in (S of this tile is, so the one before that is)
-            wait(&o_done[x], (c - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < D; i += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + i, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(t_o + i, o);
-            }
-          }
           const float mm = m == -INFINITY ? 0.f : m;
           const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
           float2 sum = make_float2(0.f, 0.f);
-          uint32_t w[32];
+          auto weights = [&](int half) {
+            uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 2 * i;
-            const float2 a = fma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2, mm2);
-            float2 q = make_float2(ex2(a.x), ex2(a.y));
-            if (!whole) {
-              q.x = e < vis ? q.x : 0.f;
-              q.y = e + 1 < vis ? q.y : 0.f;
+            for (int i = 0; i < 32; ++i) {
+              const int e = half * 64 + 2 * i;
+              const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
+              float2 q = make_float2(ex2(a.x), ex2(a.y));
+              if (!whole) {
+                q.x = e < vis ? q.x : 0.f;
+                q.y = e + 1 < vis ? q.y : 0.f;
+              }
+              sum = add2(sum, q);
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
+              w[i] = *reinterpret_cast<uint32_t *>(&h2);
             }
-            sum = add2(sum, q);
-            __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
-            w[i] = *reinterpret_cast<uint32_t *>(&h2);
+            tmem_st32(t_s + P_COL + half * 32, w);
+          };
+          weights(1);
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            // S of this tile was issued after the last O product of the stream: O is at rest
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(tmem + lanes + 256 + x * 128 + i, o);
+            }
           }
-          tmem_st32(t_s + b * KT, w);
+          load(0);
+          weights(0);
           l = fmaf(l, alpha, sum.x + sum.y);
           tmem_st_wait();
         }
-        if (t == n - 1 && it.keys_left < n * KT) {
-          // V rows past the segment's last key may hold anything: 0 times it has to be 0
-          const int ov = u + order_v(t, n, ahead);
-          wait(&full[ov % NS], (ov / NS) & 1);
-          if (!ok) break;
-          uint8_t *vt = ring + (ov % NS) * C::TILE;
-          for (int i = (it.keys_left - t * KT) * 8 + row; i < KT * 8; i += 128)
-#pragma unroll
-            for (int q = 0; q < NB; ++q)
-              *reinterpret_cast<uint4 *>(vt + q * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-        }
-        ++c;
+        clear_v(t);
         tc_fence_before();
-        mbar_arrive(&p_full[2 * x + b]);
+        mbar_arrive(&p_full[x]);
       }
-      u += 2 * n;
       if (!ok) break;
       // ---- the item's rows: o / l and log2 of their weight, or the result
       const bool both = !pair && n > 1;    // the other stream holds the odd tiles' share
@@ -880,6 +912,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         }
         if (!ok) break;
         tc_fence_after();
+        if (row == 0) {                    // the last V tiles
+          release(order_v(n - 1, n, ahead));
+          if (both) release(order_v(n - 2, n, ahead));
+        }
         if (live) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           a0 *= inv;
@@ -891,13 +927,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
-            tmem_ld32(t_o + i, o);
+            tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(a0 != 0.f ? __uint_as_float(o[j]) * a0 : 0.f);
             if (both) {
               uint32_t q[32];
-              tmem_ld32(t_o + 128 + i, q);
+              tmem_ld32(tmem + lanes + 256 + 128 + i, q);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -931,8 +967,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         mbar_arrive(&o_read[x]);
         if (both) mbar_arrive(&o_read[1]);
       }
-      o_par ^= pair || n > 1 ? 3u : 1u;    // the streams that took part
+      // streams that took part in this item
+      o_par ^= pair || n > 1 ? 3u : 1u;
       if (both) ++n_ml;
+      u += 2 * n;
     }
     if (!ok && lane == 0) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
   }
