@@ -46,7 +46,7 @@ constexpr int THREADS = 384;
 // (256 * 208 + 128 * 80 <= 384 * 168)
 constexpr int REGS_STREAM = 208, REGS_REST = 80;
 constexpr int PLAN_THREADS = 1024;
-constexpr int ITEMS_PER_SM = 3;           // what splits aim at
+constexpr int ITEMS_PER_SM = 2;           // what splits aim at
 constexpr int NQ = 4;                     // items known ahead in a CTA
 constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile)
 constexpr int BUCKETS = 128;              // sizes that the item list is ordered by
@@ -270,7 +270,7 @@ __device__ __forceinline__ long long block_sum(long long v, long long *s) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = s[threadIdx.x & 31];
+  v = (threadIdx.x & 31) < (blockDim.x >> 5) ? s[threadIdx.x & 31] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -287,7 +287,7 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
   __syncthreads();
   if (lane == 31) s[warp] = inc;
   __syncthreads();
-  int w = s[lane];
+  int w = lane < (blockDim.x >> 5) ? s[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, w, o);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   __shared__ int s_lo, s_hi;
   __shared__ int s_bucket[BUCKETS];             // items of a size, then the next place for one
   const PagedRows &r = p.a.rows;
-  const int b = threadIdx.x, G = p.a.H / p.a.KVH, KVH = p.a.KVH, prefix = r.prefix_len;
+  const int b = threadIdx.x, nt = blockDim.x, G = p.a.H / p.a.KVH, KVH = p.a.KVH, prefix = r.prefix_len;
   const int tpt = 128 / G;                      // tokens of a row tile
   if (b == 0) {
     s_lo = r.total_rows;
@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     const int size = it.ntiles * (it.ntok > tpt ? 4 : 3);
     return BUCKETS - 1 - min(BUCKETS - 1, size <= 64 ? size : 64 + (size - 64) / 16);
   };
-  for (int i = b; i < BUCKETS; i += PLAN_THREADS) s_bucket[i] = 0;
+  for (int i = b; i < BUCKETS; i += nt) s_bucket[i] = 0;
   __syncthreads();
-  for (int i = b; i < total_items; i += PLAN_THREADS) {
+  for (int i = b; i < total_items; i += nt) {
     const Item it = item_at(i);
     if (it.ntiles > 0) atomicAdd(&s_bucket[bucket_of(it)], 1);
   }
@@ -462,14 +462,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   }
   __syncthreads();
   if (b == 0) p.head->items = listed;
-  for (int i = b; i < total_items; i += PLAN_THREADS) {
+  for (int i = b; i < total_items; i += nt) {
     const Item it = item_at(i);
     if (it.ntiles > 0) p.items[atomicAdd(&s_bucket[bucket_of(it)], 1)] = it;
   }
   if (total_rows > 0) {   // the owner of every row, for the join
-    for (int t = b; t < r.total_rows; t += PLAN_THREADS) p.row_req[t] = -1;
+    for (int t = b; t < r.total_rows; t += nt) p.row_req[t] = -1;
     __syncthreads();
-    for (int q = b >> 5; q < r.B; q += PLAN_THREADS / 32)
+    for (int q = b >> 5; q < r.B; q += nt / 32)
       for (int t = b & 31; t < s_n[q]; t += 32) p.row_req[s_start[q] + t] = q;
   }
 }
@@ -774,7 +774,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       const bool own = row < rt_rows && mine < it.ntok;
       const bool live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
       const int tok = it.tok0 + mine, h = it.g * G + row_head;
-      const int lim = own ? it.lim_base + it.lim_slope * tok : 0;
+      // (rows that nobody owns see every key: the mask costs a warp its fast path)
+      const int lim = own ? it.lim_base + it.lim_slope * tok : 1 << 30;
       float m = -INFINITY, l = 0.f;
       const uint32_t uses = pair ? 1 : 2;   // of a tile by this stream, of the two that free it
       auto release = [&](int order) { mbar_arrive(&empty[(u + order) % NS], uses); };
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         if (!ok) break;
         ++c;
         tc_fence_after();
-        if (row == 0) {                    // S has read K(t), and the product before it its V
+        if (row == 96) {                   // S has read K(t), and the product before it its V
           release(order_k(t, n, ahead));
           if (t >= ahead) release(order_v(t - ahead, n, ahead));
           if (t + ahead >= n) mbar_arrive(q_free, !pair && n == 1 ? 2 : 1);   // its last S
@@ -986,14 +987,17 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 // ------------------------------------------------------------------ join
 // A warp a (row, head): out = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max)
 // over the prefix splits and the own splits whose first key the row sees.
+// Eight lanes read one partial row, so that a warp has four in flight.
 template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
-  if (!__ldg(&p.head->merge)) return;
-  constexpr int V = D / 32;                // floats a lane
-  const int lane = threadIdx.x & 31, H = p.a.H, KVH = p.a.KVH, G = H / KVH;
-  const int nsp = __ldg(&p.head->prefix_splits), first = __ldg(&p.head->first_row);
-  const int Rp = p.a.rows.prefix_len > 0 ? __ldg(&p.head->rows) * G : 0;
+  const Head *head = p.head;
+  const int4 h0 = __ldg(reinterpret_cast<const int4 *>(head)), h1 = __ldg(reinterpret_cast<const int4 *>(head) + 1);
+  if (!h0.y) return;
+  constexpr int C = D / 32;                // 16-byte chunks a lane
+  const int lane = threadIdx.x & 31, sub = lane & 7, quarter = lane >> 3;
+  const int H = p.a.H, KVH = p.a.KVH, G = H / KVH;
+  const int nsp = h0.z, first = h1.x, Rp = p.a.rows.prefix_len > 0 ? h1.y * G : 0;
   const int total = p.a.rows.total_rows * H, step = gridDim.x * (blockDim.x >> 5);
   for (int idx = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); idx < total; idx += step) {
     const int t = idx / H, h = idx % H, g = h / G;
@@ -1008,39 +1012,60 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int64_t at_o = r1.y + (int64_t)g * r0.w * R + (int64_t)(t - r0.x) * G + h % G;
     const int parts = (Rp > 0 ? nsp : 0) + own, np = parts - own;
     auto place = [&](int i) { return i < np ? at_p + (int64_t)i * Rp : at_o + (int64_t)(i - np) * R; };
-    float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + place(i)));
-    mx = warp_max(mx);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float acc[V], den = 0.f;
+    float mx = -INFINITY, den = 0.f;
+    float4 acc[C];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < parts; i0 += 32) {
-      const float wl = i0 + lane < parts ? ex2(__ldcg(p.part_lse + place(i0 + lane)) - base) : 0.f;
-      const int m = min(32, parts - i0);
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float w = __shfl_sync(0xffffffffu, wl, i);
-        den += w;
-        const float *o = p.part_o + place(i0 + i) * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4 *>(o));
-          acc[0] = fmaf(w, x.x, acc[0]);
-          acc[1] = fmaf(w, x.y, acc[1]);
-          acc[2] = fmaf(w, x.z, acc[2]);
-          acc[3] = fmaf(w, x.w, acc[3]);
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2 *>(o));
-          acc[0] = fmaf(w, x.x, acc[0]);
-          acc[1] = fmaf(w, x.y, acc[1]);
+      float w = i0 + lane < parts ? __ldcg(p.part_lse + place(i0 + lane)) : -INFINITY;
+      const float m = fmaxf(mx, warp_max(w)), base = m == -INFINITY ? 0.f : m, old = ex2(mx - base);
+      mx = m;
+      w = ex2(w - base);
+      den = den * old + w;
+      const int n = min(32, parts - i0);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        acc[c].x *= old;
+        acc[c].y *= old;
+        acc[c].z *= old;
+        acc[c].w *= old;
+      }
+#pragma unroll 2
+      for (int i = 0; i < n; i += 4) {
+        const float wi = __shfl_sync(0xffffffffu, w, i + quarter);
+        if (i + quarter < n) {
+          const float4 *o = reinterpret_cast<const float4 *>(p.part_o + place(i0 + i + quarter) * D) + sub;
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float4 x = __ldcg(o + 8 * c);
+            acc[c].x = fmaf(wi, x.x, acc[c].x);
+            acc[c].y = fmaf(wi, x.y, acc[c].y);
+            acc[c].z = fmaf(wi, x.z, acc[c].z);
+            acc[c].w = fmaf(wi, x.w, acc[c].w);
+          }
         }
       }
     }
-    const float inv = 1.f / den;
-    __nv_bfloat162 *out = reinterpret_cast<__nv_bfloat162 *>((bf16 *)p.a.out + (int64_t)t * p.a.out_stride +
-                                                             (int64_t)h * D + lane * V);
+    const float inv = 1.f / warp_sum(den);
 #pragma unroll
-    for (int v = 0; v < V / 2; ++v) out[v] = __floats2bfloat162_rn(acc[2 * v] * inv, acc[2 * v + 1] * inv);
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int o = 8; o < 32; o <<= 1) {
+        acc[c].x += __shfl_xor_sync(0xffffffffu, acc[c].x, o);
+        acc[c].y += __shfl_xor_sync(0xffffffffu, acc[c].y, o);
+        acc[c].z += __shfl_xor_sync(0xffffffffu, acc[c].z, o);
+        acc[c].w += __shfl_xor_sync(0xffffffffu, acc[c].w, o);
+      }
+    }
+    // quarter q writes chunk q
+    bf16 *out = (bf16 *)p.a.out + (int64_t)t * p.a.out_stride + (int64_t)h * D;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (c == quarter) {
+        __nv_bfloat162 w2[2] = {__floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv),
+                                __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv)};
+        *reinterpret_cast<uint2 *>(out + (8 * c + sub) * 4) = *reinterpret_cast<uint2 *>(w2);
+      }
   }
 }
 
@@ -1138,12 +1163,13 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   p.sms = sms > 0 ? sms : 1;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
   p.negative = a.scale < 0.f;
-  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, p);
+  // a thread a request; barriers of 256 threads are cheaper than those of 1024
+  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(a.rows.B <= 256 ? 256 : PLAN_THREADS), 0, s, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_attention_kernel<D>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.rows.total_rows * a.H;
-  const int grid = (int)std::min<int64_t>((warps + 7) / 8, 8LL * p.sms);
+  const int grid = (int)std::min<int64_t>((warps + 7) / 8, 16LL * p.sms);
   return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(256), 0, s, p);
 }
 template <int D> cudaError_t prepare() {
