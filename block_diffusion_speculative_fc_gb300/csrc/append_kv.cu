@@ -12,12 +12,16 @@
 // floating-point reduction.  sin and cos are formed once per token and pair
 // (rd/2 calls of sincospif) and shared by its heads through shared memory.
 //
-// One CTA per token; 16 bytes per thread and chunk, the 16-byte chunks of a
-// head in consecutive lanes: the mean square is a shuffle reduction over those
-// lanes, and the rotation partner rd/2 dims away sits in the same slot of
-// another lane (through shared memory where rd/2 is not a multiple of the
-// chunk).  A thread's first kU chunks are in flight before the CTA looks up
-// its request, position and page (three dependent loads).
+// One CTA per token.  A thread holds two 16-byte chunks of a head D/2 dims
+// apart, the chunks of a head's half in consecutive lanes: the mean square is a
+// shuffle reduction over those lanes, and where the rotation covers the whole
+// head both sides of a pair are in one thread (partial rotations of halves go
+// through shared memory).  A thread's sines and cosines serve all its heads and
+// stay in registers.  With a chunk a thread and the pair's other side in another
+// lane, shared-memory accesses and shuffles bound it instead of HBM: 2048 tokens
+// of 32 + 8 + 8 heads of 128 took 24.0 us.  A thread's first kU units (pairs of
+// chunks) are in flight before the CTA looks up its request, position and page
+// (two dependent loads).
 #include "common.cuh"
 #include "paged_rows.cuh"
 #include "target_ops.h"
@@ -25,7 +29,7 @@
 namespace dflash {
 namespace {
 
-constexpr int kU = 4;
+constexpr int kU = 2;   // units of a thread and pass
 
 template <typename T> struct Chunk;
 template <> struct Chunk<bf16> {
@@ -62,46 +66,52 @@ template <> struct Chunk<float> {
   }
 };
 
-// LPR lanes per head row; D = LPR * E.
-template <typename T, int LPR>
+enum Rotation { kInterleaved, kWholeHalves, kPartHalves };
+
+// L lanes per head; D = 2 L E.
+template <typename T, int L, int ROT>
 __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int E = Chunk<T>::E, D = LPR * E;
+  constexpr int E = Chunk<T>::E, D = 2 * L * E;
   __shared__ float2 s_cs[64];
-  __shared__ int s_b;
-  extern __shared__ float s_x[];   // [threads][E], rotations across chunk borders only
+  __shared__ RowOwner s_owner;
+  __shared__ uint4 s_gain[2][2 * L];   // of queries, of keys
+  extern __shared__ float s_x[];       // [2 E][threads]: kPartHalves only
   pdl_wait();
   const int t = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
-  const int lane = tid & (LPR - 1);
-  const int chunks = (p.H + 2 * p.KVH) * LPR;
-  // chunk c: head c / LPR of [q heads | k heads | v heads]
+  const int lane = tid & (L - 1);
+  const int units = (p.H + 2 * p.KVH) * L;
+  // unit c: chunks `lane` and L + `lane` of head c / L of [q heads | k heads | v heads]
   auto source = [&](int c) -> const uint4 * {
-    const int head = c / LPR;
+    const int head = c / L;
     const T *row;
     if (head < p.H) row = (const T *)p.q + (int64_t)t * p.q_stride + head * D;
     else if (head < p.H + p.KVH) row = (const T *)p.k + (int64_t)t * p.k_stride + (head - p.H) * D;
     else row = (const T *)p.v + (int64_t)t * p.v_stride + (head - p.H - p.KVH) * D;
     return reinterpret_cast<const uint4 *>(row) + lane;
   };
-  uint4 raw[kU];
+  uint4 raw[kU][2];
 #pragma unroll
   for (int u = 0; u < kU; ++u)
-    if (tid + u * nt < chunks) raw[u] = *source(tid + u * nt);
+    if (tid + u * nt < units) {
+      const uint4 *src = source(tid + u * nt);
+      raw[u][0] = src[0];
+      raw[u][1] = src[L];
+    }
 
   const PagedRows &r = p.rows;
-  const int b = owner_of_row(r, t, p.err, &s_b);
-  if (b < 0) return;
-  const int kv = r.kv_len[b];
-  const int64_t pos64 = (int64_t)kv + (t - r.row_start[b]);
+  for (int i = tid; i < 4 * L; i += nt) {
+    const uint4 *gain = (const uint4 *)(i < 2 * L ? p.q_gain : p.k_gain);
+    if (gain) s_gain[i / (2 * L)][i % (2 * L)] = gain[i % (2 * L)];
+  }
+  if (!owner_of_row(r, t, p.err, &s_owner)) return;
+  const int b = s_owner.b, kv = s_owner.kv;
+  const int64_t pos64 = (int64_t)kv + (t - s_owner.start);
   if (kv < r.prefix_len || pos64 - r.prefix_len >= (int64_t)r.pages_per_req * kPageRows) {
     if (tid == 0) raise_error(p.err, DFLASH_DERR_KV_CAPACITY);
     return;
   }
   const int pos = (int)pos64, own = pos - r.prefix_len;
   const int page = r.page_table[(int64_t)b * r.pages_per_req + own / kPageRows];
-  if (page < 0 || page >= r.n_pages) {
-    if (tid == 0) raise_error(p.err, DFLASH_DERR_PAGE_RANGE);
-    return;
-  }
   const int half = p.rot >> 1;
   for (int i = tid; i < half; i += nt) {
     const unsigned long long turn = (unsigned long long)pos * p.turns[i];
@@ -109,111 +119,128 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
     s_cs[i] = make_float2(cs * p.amp, sn * p.amp);
   }
+  if (page < 0 || page >= r.n_pages) {
+    if (tid == 0) raise_error(p.err, DFLASH_DERR_PAGE_RANGE);
+    return;
+  }
   __syncthreads();
 
+  // the pairs whose both sides this thread holds
+  float2 cs[E];
+  if (ROT != kPartHalves) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = ROT == kWholeHalves ? lane * E + e : (e / (E / 2)) * (D / 4) + lane * (E / 2) + e % (E / 2);
+      cs[e] = s_cs[i < half ? i : 0];
+    }
+  }
   const int64_t slot = (int64_t)page * kPageRows + own % kPageRows;
-  const bool shuffled = !p.inter && half % E == 0;
-  for (int c0 = 0; c0 < chunks; c0 += kU * nt) {
+  for (int c0 = 0; c0 < units; c0 += kU * nt) {
     if (c0 > 0) {
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        if (c0 + tid + u * nt < chunks) raw[u] = *source(c0 + tid + u * nt);
+        if (c0 + tid + u * nt < units) {
+          const uint4 *src = source(c0 + tid + u * nt);
+          raw[u][0] = src[0];
+          raw[u][1] = src[L];
+        }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int c = c0 + tid + u * nt;
-      if (c0 + u * nt >= chunks) break;          // the whole CTA is past the end
-      const int head = c / LPR;
-      const bool live = c < chunks;
+      if (c0 + u * nt >= units) break;           // the whole CTA is past the end
+      const int head = c / L;
+      const bool live = c < units;
       const bool is_q = head < p.H, is_v = head >= p.H + p.KVH;
-      uint4 res = raw[u];
       // heads differ within a warp: every lane takes part in the exchanges
-      float x[E];
-      Chunk<T>::unpack(live ? raw[u] : make_uint4(0, 0, 0, 0), x);
-      const T *gain = (const T *)(is_q ? p.q_gain : p.k_gain);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      float x[2 * E];
+      Chunk<T>::unpack(live ? raw[u][0] : zero, x);
+      Chunk<T>::unpack(live ? raw[u][1] : zero, x + E);
       if (p.q_gain || p.k_gain) {
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 2 * E; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
-        if (gain && !is_v) {
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, L);
+        if ((is_q ? p.q_gain : p.k_gain) && !is_v) {
           const float rs = rsqrtf(ss * (1.0f / D) + p.eps);
-          float g[E];
-          Chunk<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(gain) + lane), g);
+          float g[2 * E];
+          Chunk<T>::unpack(s_gain[is_q ? 0 : 1][lane], g);
+          Chunk<T>::unpack(s_gain[is_q ? 0 : 1][L + lane], g + E);
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = x[e] * rs * g[e];
+          for (int e = 0; e < 2 * E; ++e) x[e] = x[e] * rs * g[e];
         }
       }
-      if (p.inter) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const int i = (lane * E + e) >> 1;
-          if (i < half) {
-            const float2 cs = s_cs[i];
-            const float a = x[e], bb = x[e + 1];
-            x[e] = a * cs.x - bb * cs.y;
-            x[e + 1] = bb * cs.x + a * cs.y;
-          }
-        }
-      } else if (shuffled) {
-        const int hl = half / E;                 // lanes of half the rotated dims
-        const bool lo = lane < hl, rotated = lane < 2 * hl;
-        const int from = rotated ? (lo ? lane + hl : lane - hl) : lane;
+      if (ROT == kInterleaved) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float y = __shfl_sync(0xffffffffu, x[e], from, LPR);
-          if (rotated) {
-            const float2 cs = s_cs[(lo ? lane : lane - hl) * E + e];
-            x[e] = lo ? x[e] * cs.x - y * cs.y : x[e] * cs.x + y * cs.y;
+          const int k = (e / (E / 2)) * E + 2 * (e % (E / 2));   // first side, in x
+          const int i = (e / (E / 2)) * (D / 4) + lane * (E / 2) + e % (E / 2);
+          if (i < half) {
+            const float a = x[k], bb = x[k + 1];
+            x[k] = a * cs[e].x - bb * cs[e].y;
+            x[k + 1] = bb * cs[e].x + a * cs[e].y;
           }
+        }
+      } else if (ROT == kWholeHalves) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float a = x[e], bb = x[E + e];
+          x[e] = a * cs[e].x - bb * cs[e].y;
+          x[E + e] = bb * cs[e].x + a * cs[e].y;
         }
       } else {
-        float *row = s_x + (tid - lane) * E;     // this head's D values
+        // dim d of this head: side d / (D / 2), lane d / E % L, value d % E
+        float *at = s_x + (tid - lane);
 #pragma unroll
-        for (int e = 0; e < E; ++e) row[lane * E + e] = x[e];
+        for (int e = 0; e < 2 * E; ++e) at[e * nt + lane] = x[e];
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int d = lane * E + e;
+        for (int e = 0; e < 2 * E; ++e) {
+          const int d = (e / E) * (D / 2) + lane * E + e % E;
           if (d < p.rot) {
             const bool lo = d < half;
-            const float y = row[lo ? d + half : d - half];
-            const float2 cs = s_cs[lo ? d : d - half];
-            x[e] = lo ? x[e] * cs.x - y * cs.y : x[e] * cs.x + y * cs.y;
+            const int o = lo ? d + half : d - half;
+            const float y = at[((o / (D / 2)) * E + o % E) * nt + o / E % L];
+            const float2 w = s_cs[lo ? d : d - half];
+            x[e] = lo ? x[e] * w.x - y * w.y : x[e] * w.x + y * w.y;
           }
         }
         __syncwarp();
       }
       if (!live) continue;
-      if (!is_v) res = Chunk<T>::pack(x);
       T *dst;
       if (is_q) dst = (T *)p.q_out + (int64_t)t * p.q_out_stride + head * D;
       else if (!is_v) dst = (T *)p.k_pages + (slot * p.KVH + (head - p.H)) * D;
       else dst = (T *)p.v_pages + (slot * p.KVH + (head - p.H - p.KVH)) * D;
-      *(reinterpret_cast<uint4 *>(dst) + lane) = res;
+      uint4 *to = reinterpret_cast<uint4 *>(dst) + lane;
+      to[0] = is_v ? raw[u][0] : Chunk<T>::pack(x);
+      to[L] = is_v ? raw[u][1] : Chunk<T>::pack(x + E);
     }
   }
 }
 
-template <typename T, int LPR>
+template <typename T, int L>
 cudaError_t launch(const AppendParams &p, cudaStream_t s) {
-  const int chunks = (p.H + 2 * p.KVH) * LPR;
-  // kU chunks a thread and pass, in as few passes as 256 threads allow
-  const int passes = (chunks + 256 * kU - 1) / (256 * kU);
-  int nt = (chunks + passes * kU - 1) / (passes * kU);
+  constexpr int E = Chunk<T>::E, D = 2 * L * E;
+  const int units = (p.H + 2 * p.KVH) * L;
+  // kU units a thread and pass, in as few passes as 256 threads allow
+  const int passes = (units + 256 * kU - 1) / (256 * kU);
+  int nt = (units + passes * kU - 1) / (passes * kU);
   nt = (nt + 31) / 32 * 32;
-  const bool across = !p.inter && (p.rot / 2) % Chunk<T>::E != 0;
-  const size_t smem = across ? sizeof(float) * Chunk<T>::E * nt : 0;
-  return launch_pdl(append_kv_kernel<T, LPR>, dim3(p.rows.total_rows), dim3(nt), smem, s, p);
+  const dim3 grid(p.rows.total_rows), block(nt);
+  if (p.inter || p.rot == 0) return launch_pdl(append_kv_kernel<T, L, kInterleaved>, grid, block, 0, s, p);
+  if (p.rot == D) return launch_pdl(append_kv_kernel<T, L, kWholeHalves>, grid, block, 0, s, p);
+  return launch_pdl(append_kv_kernel<T, L, kPartHalves>, grid, block, sizeof(float) * 2 * E * nt, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_append_kv(int dtype, int head_dim, const AppendParams &p, cudaStream_t s) {
   if (dtype == DFLASH_BF16)
-    return head_dim == 64 ? launch<bf16, 8>(p, s) : launch<bf16, 16>(p, s);
-  return head_dim == 64 ? launch<float, 16>(p, s) : launch<float, 32>(p, s);
+    return head_dim == 64 ? launch<bf16, 4>(p, s) : launch<bf16, 8>(p, s);
+  return head_dim == 64 ? launch<float, 8>(p, s) : launch<float, 16>(p, s);
 }
 
 }  // namespace dflash

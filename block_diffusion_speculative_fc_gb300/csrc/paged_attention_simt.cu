@@ -26,10 +26,9 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
   float *Qs = Vs + KT * D;           // [G][D]
   float *Os = Qs + G * D;            // [G][D]
   float *ms = Os + G * D, *ls = ms + G;
-  __shared__ int s_b;
-  const int b = owner_of_row(r, t, p.err, &s_b);
-  if (b < 0) return;
-  const int kv = r.kv_len[b], a = r.row_start[b], n = r.row_start[b + 1] - a;
+  __shared__ RowOwner s_owner;
+  if (!owner_of_row(r, t, p.err, &s_owner)) return;
+  const int b = s_owner.b, kv = s_owner.kv, a = s_owner.start, n = r.row_start[b + 1] - a;
   if (kv < r.prefix_len ||
       (int64_t)kv + n - r.prefix_len > (int64_t)r.pages_per_req * kPageRows) {
     if (tid == 0) raise_error(p.err, DFLASH_DERR_KV_CAPACITY);
