@@ -313,6 +313,7 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ Params p) {
   pdl_wait();
+  pdl_trigger();   // the attention CTAs set up their barriers and TMEM meanwhile, then wait for the plan
   __shared__ long long s_sum[32];
   __shared__ int s_scan[32];
   __shared__ int s_first[PLAN_THREADS + 2];     // first item of every segment (prefix, requests)
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   pdl_wait();
-  const int n_items = __ldg(&p.head->items);
+  const int n_items = __ldcg(&p.head->items);
   bool ok = true;
   // consumers: the CTA's i-th item (a warp's wait); false at the end or after a timeout
   uint32_t n_item = 0;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           ok = false;
           return false;
         }
-        if (lane < 12) s_items[e * 12 + lane] = idx < n_items ? __ldg((const int *)(p.items + idx) + lane) : 0;
+        if (lane < 12) s_items[e * 12 + lane] = idx < n_items ? __ldcg((const int *)(p.items + idx) + lane) : 0;
         __syncwarp();
         it = read_item(s_items + e * 12);
         if (lane == 0) mbar_arrive(&item_full[e]);
@@ -994,7 +995,7 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const Head *head = p.head;
-  const int4 h0 = __ldg(reinterpret_cast<const int4 *>(head)), h1 = __ldg(reinterpret_cast<const int4 *>(head) + 1);
+  const int4 h0 = __ldcg(reinterpret_cast<const int4 *>(head)), h1 = __ldcg(reinterpret_cast<const int4 *>(head) + 1);
   if (!h0.y) return;
   constexpr int C = D / 32;                // 16-byte chunks a lane
   const int lane = threadIdx.x & 31, sub = lane & 7, quarter = lane >> 3;
@@ -1003,10 +1004,10 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const int total = p.a.rows.total_rows * H, step = gridDim.x * (blockDim.x >> 5);
   for (int idx = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); idx < total; idx += step) {
     const int t = idx / H, h = idx % H, g = h / G;
-    const int b = __ldg(p.row_req + t);
+    const int b = __ldcg(p.row_req + t);
     if (b < 0) continue;
-    const int4 r0 = __ldg(reinterpret_cast<const int4 *>(p.req + b));
-    const int4 r1 = __ldg(reinterpret_cast<const int4 *>(p.req + b) + 1);
+    const int4 r0 = __ldcg(reinterpret_cast<const int4 *>(p.req + b));
+    const int4 r1 = __ldcg(reinterpret_cast<const int4 *>(p.req + b) + 1);
     if (r1.y < 0) continue;                // written by its one item
     const int R = r0.y * G, seen = p.a.causal ? r0.z + (t - r0.x) + 1 : r0.z + r0.y;
     const int span = r1.x * KT, own = min(r0.w, (seen + span - 1) / span);
