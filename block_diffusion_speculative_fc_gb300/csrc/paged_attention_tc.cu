@@ -478,6 +478,45 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ attention
+// A row's part of an item from its visible keys alone, one thread: for rows whose products met a
+// value that is not finite behind their last key (0 times it is not 0 in the matrix product).
+// Writes o * inv to po or out; nothing when the keys from lim to end hold finite values only.
+template <int D>
+__device__ __noinline__ void redo_row(const Params &p, int req, int g, int page0, int lim, int end, const bf16 *q,
+                                      float m, float inv, float *po, bf16 *out) {
+  const int *list = p.a.rows.page_table + (int64_t)req * p.a.rows.pages_per_req + page0;
+  const int KVH = p.a.KVH;
+  auto at = [&](const void *pages, int key) {
+    const int pg = list[key / kPageRows];
+    const int64_t slot = (int64_t)(pg >= 0 && pg < p.a.rows.n_pages ? pg : 0) * kPageRows + key % kPageRows;
+    return (const bf16 *)pages + (slot * KVH + g) * D;
+  };
+  bool finite = true;
+  for (int key = lim; key < end; ++key) {
+    const bf16 *v = at(p.a.v_pages, key);
+    for (int d = 0; d < D; ++d) finite = finite && isfinite(__bfloat162float(v[d]));
+  }
+  if (finite) return;
+  for (int d0 = 0; d0 < D; d0 += 16) {
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+    for (int key = 0; key < lim; ++key) {
+      const bf16 *k = at(p.a.k_pages, key), *v = at(p.a.v_pages, key) + d0;
+      float sc = 0.f;
+      for (int d = 0; d < D; ++d) sc = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), sc);
+      const float w = ex2((p.negative ? -sc : sc) * p.scale_log2 - m);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = fmaf(w, __bfloat162float(v[i]), o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (po) po[d0 + i] = o[i] * inv;
+      else out[d0 + i] = __float2bfloat16_rn(o[i] * inv);
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
@@ -921,13 +960,18 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (both) release(order_v(n - 2, n, ahead));
         }
         if (live) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          // a split may hold no key that the row sees; a whole row of -infinities has no result (NaN)
+          const float inv = l == 0.f && it.part >= 0 ? 0.f : 1.f / l;
+          // keys of these tiles that the row does not see
+          const int end = min(n * KT, it.keys_left);
+          const bool hides = own && lim < end && l != 0.f;
+          bool odd = false;
           a0 *= inv;
           a1 *= inv;
           bf16 *out = (bf16 *)p.a.out + (int64_t)tok * p.a.out_stride + (int64_t)h * D;
           const int at = it.part + mine * G + row_head;        // partial row
           float *po = p.part_o + (int64_t)at * D;
-          if (own && it.part >= 0) p.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+          if (own && it.part >= 0) p.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
@@ -942,6 +986,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 o[j] = __float_as_uint(__uint_as_float(o[j]) + (a1 != 0.f ? __uint_as_float(q[j]) * a1 : 0.f));
+            }
+            if (hides) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) odd = odd || !isfinite(__uint_as_float(o[j]));
             }
             // 32 bytes a store: whole sectors, as a lane's rows are far apart
             if (own && it.part >= 0) {
@@ -966,6 +1014,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               }
             }
           }
+          if (odd)
+            redo_row<D>(p, it.req, it.g, it.page0, lim, end,
+                        (const bf16 *)p.a.q + (int64_t)tok * p.a.q_stride + (int64_t)h * D, m, inv,
+                        it.part >= 0 ? po : nullptr, out);
         }
         tc_fence_before();
         mbar_arrive(&o_read[x]);

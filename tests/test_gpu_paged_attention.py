@@ -126,6 +126,39 @@ def test_scores_far_below_zero(sess, dtype, dim):
         close(pb, q, 2, out, dim ** -0.5, True)
 
 
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("lens,ctx,j", [([16], [20], 5), ([16], [115], 12), ([300], [0], 140), ([9], [3000], 3)])
+@pytest.mark.parametrize("prefix", [0, 128])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(sess, dtype, dim, lens, ctx, j, prefix):
+    """Row j's value has a NaN and infinities: rows before j are as without it, from j on those
+    dims and no others are not finite.  The same with a NaN key: every dim from j on."""
+    for what in ("v", "k"):
+        pb = Paged(lens, ctx, prefix=prefix, kvh=1, dim=dim, dtype=dtype, seed=8)
+        q = pb.normal(pb.rows, 5, dim)
+        want = attend64(pb, q, 5, dim ** -0.5, True)
+        pages, rows = pb.slots(0, prefix + ctx[0] + j, prefix + ctx[0] + j + 1)
+        if what == "v":
+            pb.v[pages, rows, 0, 3] = float("nan")
+            pb.v[pages, rows, 0, dim - 2] = float("inf")
+            pb.v[pages, rows, 0, dim // 2] = float("-inf")
+        else:
+            pb.k[pages, rows, 0, 9] = float("nan")
+        hit = torch.zeros(dim, dtype=torch.bool, device="cuda")
+        hit[[3, dim - 2, dim // 2] if what == "v" else slice(None)] = True
+        out = torch.full((pb.rows, 5, dim), FILL, dtype=dtype, device="cuda")
+        lay = pb.layer(5)
+        sess.paged_attention(lay, q, pb.row_start, pb.kv_len, out, sess.attention_workspace(lay, 1, pb.rows))
+        assert sess.error() == 0
+        for t, (exact, spread, mag) in want.items():
+            if t < j:
+                half = torch.finfo(dtype).eps / 2
+                ds = ((dim + 8) * 2.0 ** -24 * mag)[:, None]
+                tol = half * exact.abs() + (half * (dtype == BF) + 2 * ds + 2.0 ** -18) * spread * (1 + half)
+                assert float(((out[t].double() - exact).abs() - tol).max()) <= 0, t
+            else:
+                assert torch.equal(~torch.isfinite(out[t]), hit.expand(5, dim)), t
+
+
 def test_batch_limits(sess):
     lens = [1 if i % 3 else 0 for i in range(1024)]
     run(sess, lens, [i % 70 for i in range(1024)], 2, 1, 64, BF, seed=1)
