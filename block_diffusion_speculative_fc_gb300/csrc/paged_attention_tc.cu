@@ -47,7 +47,8 @@ constexpr int THREADS = 384;
 constexpr int REGS_STREAM = 208, REGS_REST = 80;
 constexpr int PLAN_THREADS = 1024;
 constexpr int NQ = 4;                     // items known ahead in a CTA
-constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile)
+constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile pair)
+constexpr int MAX_SMS = EXTRA * 3 / 4;    // CTAs at most
 constexpr int BUCKETS = 128;              // sizes that the item list is ordered by
 // The weights of a tile go to the upper half of its S columns, so that the lower half can be read
 // a second time.
@@ -92,8 +93,8 @@ struct Params {
   Item *items;
   Request *req;
   int *row_req;                           // [total_rows]
-  float *part_o, *part_lse;               // [cap][D], [cap]
-  int cap, max_items, sms;
+  float *part_o, *part_lse;               // [partial rows][D], [partial rows]
+  int sms;
   float scale_log2;                       // |scale| log2 e
   int negative;                           // scale < 0: S changes its sign
 };
@@ -347,7 +348,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     }
   }
   __syncthreads();
-  const int lo = s_lo, rows = max(0, s_hi - s_lo);
+  // more rows than there are: ranges overlap (a decreasing pair among them is flagged already), and
+  // the workspace has no room for them
+  const bool fits = block_sum(n, s_sum) <= r.total_rows;
+  if (!fits) {
+    n = 0;
+    if (b == 0) raise_error(p.a.err, DFLASH_DERR_ROW_RANGE);
+  }
+  const int lo = s_lo, rows = fits ? max(0, s_hi - s_lo) : 0;
   const int R = n * G, keys = ctx + n, nkt = n > 0 ? (keys + KT - 1) / KT : 0;
   const int Rp = prefix > 0 ? rows * G : 0, nktp = Rp > 0 ? prefix / KT + (prefix % KT != 0) : 0;
   const long long W = block_sum((long long)KVH * nkt * ceil_div(n, tpt), s_sum) +
@@ -357,24 +365,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   // prompts (whose requests' items are smaller than either) 216 both ways.
   long long U = (W + p.sms - 1) / p.sms;
   U = U < 2 ? 2 : U;
-  Split sp, spp;
-  int part = 0, items = 0, total_rows = 0, total_items = 0;
-  bool joined = false;
+  // Items beyond one per (segment, KV head, pair of row tiles) are fewer than 4/3 W / U <= 4/3 SMs <=
+  // EXTRA (a pair costs two units of its U in split_keys; segments of c row tiles have (c + 1) / 2
+  // pairs and count c in W), each with at most 256 partial rows: the workspace has room for them.
+  const Split sp = split_keys(nkt, n, tpt, U), spp = split_keys(nktp, rows, tpt, U);
+  const bool joined = n > 0 && (prefix > 0 || sp.splits > 1);
   const int nrt = ceil_div(n, 2 * tpt), nrtp = Rp > 0 ? ceil_div(rows, 2 * tpt) : 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    sp = split_keys(nkt, n, tpt, U);
-    spp = split_keys(nktp, rows, tpt, U);
-    joined = n > 0 && (prefix > 0 || sp.splits > 1);
-    part = block_scan(joined ? sp.splits * KVH * R : 0, s_scan, total_rows);
-    items = block_scan(KVH * nrt * sp.splits, s_scan, total_items);
-    const int prefix_rows = spp.splits * KVH * Rp, prefix_items = KVH * nrtp * spp.splits;
-    part += prefix_rows;
-    items += prefix_items;
-    total_rows += prefix_rows;
-    total_items += prefix_items;
-    if (total_rows <= p.cap && total_items <= p.max_items) break;
-    U = 1LL << 40;   // one split each always fits (the bound on splits makes this unreachable)
-  }
+  const int prefix_rows = spp.splits * KVH * Rp, prefix_items = KVH * nrtp * spp.splits;
+  int total_rows = 0, total_items = 0;
+  const int part = block_scan(joined ? sp.splits * KVH * R : 0, s_scan, total_rows) + prefix_rows;
+  const int items = block_scan(KVH * nrt * sp.splits, s_scan, total_items) + prefix_items;
+  total_rows += prefix_rows;
+  total_items += prefix_items;
   s_first[b + 1] = items;
   if (b == 0) {
     s_first[0] = 0;
@@ -1167,8 +1169,6 @@ bool encode_rows(CUtensorMap *tm, const void *q, int total_rows, int H, int D, i
 
 struct Layout {
   size_t head, items, req, row_req, part_o, part_lse, total;
-  int64_t cap;
-  int max_items;
 };
 // Partial rows: at most one per row and segment plus 256 for every item beyond
 // one per (segment, head, row tile).
@@ -1182,14 +1182,14 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   };
   const int tpt = 128 / (H / KVH);
   const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows / (2 * tpt) + 1;
-  L.max_items = (int)(KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA);
-  L.cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * 256;
+  const int64_t max_items = KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA;
+  const int64_t cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * 256;
   L.head = take(sizeof(Head));
-  L.items = take(sizeof(Item) * L.max_items);
+  L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);
   L.row_req = take(4 * (size_t)total_rows);
-  L.part_lse = take(4 * L.cap);
-  L.part_o = take(4 * L.cap * D);
+  L.part_lse = take(4 * cap);
+  L.part_o = take(4 * cap * D);
   L.total = o;
   return L;
 }
@@ -1213,9 +1213,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   p.row_req = (int *)(ws + L.row_req);
   p.part_o = (float *)(ws + L.part_o);
   p.part_lse = (float *)(ws + L.part_lse);
-  p.cap = (int)L.cap;
-  p.max_items = L.max_items;
-  p.sms = sms > 0 ? sms : 1;
+  p.sms = std::max(1, std::min(sms, MAX_SMS));
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
   p.negative = a.scale < 0.f;
   // a thread a request; barriers of 256 threads are cheaper than those of 1024

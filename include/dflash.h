@@ -459,8 +459,11 @@ int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hid
  * row_start[batch] on belong to nobody and are never written.  A row_start
  * pair that decreases or leaves [0, total_rows] sets DFLASH_DERR_ROW_RANGE
  * and its request is skipped.  No row may belong to two requests:
- * dflash_append_kv flags such rows and skips them, the outputs that
- * dflash_paged_attention writes for them are unspecified.
+ * dflash_append_kv flags such rows and skips them; the outputs that
+ * dflash_paged_attention writes for them are unspecified, and where the
+ * ranges hold more than total_rows rows in all it flags that
+ * (DFLASH_DERR_ROW_RANGE) and writes nothing.  Arrays of 32-bit values are
+ * 4-byte aligned.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -540,6 +543,7 @@ int dflash_rope_init(int32_t rotary_dim, int32_t interleaved, double theta,
  *   q_gain, k_gain  [head_dim], NULL for no norm; eps >= 0
  *   rope      host, read during the call
  *   q_out     [total_rows, n_heads, head_dim], its own row stride; may be q
+ *             (with q's stride), else it shares no memory with q, k or v
  * Pointers 16-byte aligned (gains too), strides multiples of 16 bytes.
  * Rows whose cache row does not exist are flagged (DFLASH_DERR_KV_CAPACITY,
  * DFLASH_DERR_PAGE_RANGE) and skipped whole.  Two rows of one call must not
@@ -561,7 +565,8 @@ int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
  * rows of all requests as one matrix, and the partial softmax results of the
  * prefix and of the requests' own rows are joined at the end.
  *   q, out    [total_rows, n_heads, head_dim], row strides in elements
- *             (multiples of 16 bytes, pointers 16-byte aligned); out is not q
+ *             (multiples of 16 bytes, pointers 16-byte aligned); out shares
+ *             no memory with q
  *   workspace device memory, 256-byte aligned, of at least
  *             dflash_paged_attention_workspace_size bytes; written by the
  *             call, nothing is kept in it between calls.  Calls that may

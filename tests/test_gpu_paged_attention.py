@@ -203,6 +203,19 @@ def test_requests_without_a_place_are_flagged_and_skipped(sess, dtype, dim):
     bad_case(sess, 0x40, [0, 1], dtype, dim, row_start=put(3, 12))
 
 
+@pytest.mark.parametrize("dim,prefix", [(128, 0), (64, 0), (128, 128)])
+def test_ranges_that_repeat_every_row_are_flagged_and_nothing_is_written(sess, dim, prefix):
+    """40 ranges, 20 of them all rows and 20 decreasing: more rows than the workspace was sized for."""
+    pb = Paged([6] + [0] * 39, [10] * 40, prefix=prefix, kvh=1, dim=dim, dtype=BF, seed=4)
+    q, lay = pb.normal(pb.rows, 64, dim), pb.layer(64)
+    pb.row_start = i32([0, 6] * 20 + [0])
+    out = torch.full((pb.rows, 64, dim), FILL, dtype=BF, device="cuda")
+    sess.paged_attention(lay, q, pb.row_start, pb.kv_len, out, sess.attention_workspace(lay, 40, pb.rows))
+    assert sess.error() == 0x40
+    assert bool((out == FILL).all())
+    run(sess, [3], [4], 4, 1, dim, BF, prefix=prefix)
+
+
 @pytest.mark.parametrize("dtype,dim", KINDS)
 def test_bad_pages_are_flagged(sess, dtype, dim):
     """An id outside the pool is never followed; the other requests are right."""
