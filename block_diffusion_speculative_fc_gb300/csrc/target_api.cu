@@ -22,6 +22,9 @@ bool aligned16(const void *p, int64_t stride, size_t es) {
   return (uintptr_t)p % 16 == 0 && (stride * (int64_t)es) % 16 == 0;
 }
 
+// 32-bit arrays of the device
+template <typename... P> bool aligned4(const P *...p) { return (((uintptr_t)p % 4 == 0) && ...); }
+
 int check_layer(const dflash_layer_kv *kv, int32_t batch, int32_t total_rows) {
   if (!kv) return fail(DFLASH_EINVAL, "kv is NULL");
   if (kv->dtype != DFLASH_F32 && kv->dtype != DFLASH_BF16) return fail(DFLASH_EUNSUPPORTED, "dtype");
@@ -42,6 +45,8 @@ int check_layer(const dflash_layer_kv *kv, int32_t batch, int32_t total_rows) {
   if (kv->prefix_len < 0 || kv->prefix_len % kPageRows || kv->prefix_len > INT32_MAX / 2)
     return fail(DFLASH_EINVAL, "prefix_len must be a multiple of 64");
   if (kv->prefix_len > 0 && !kv->prefix_pages) return fail(DFLASH_EINVAL, "prefix_pages is NULL");
+  if (!aligned4(kv->page_table, kv->prefix_pages))
+    return fail(DFLASH_EINVAL, "page_table and prefix_pages must be 4-byte aligned");
   if (batch < 0 || total_rows < 0) return fail(DFLASH_EINVAL, "negative batch or total_rows");
   if (batch > 1024) return fail(DFLASH_ECAPACITY, "batch > 1024");
   if ((int64_t)total_rows * kv->n_heads > (1 << 28))
@@ -80,6 +85,8 @@ int sampling_params(dflash_handle *h, int32_t rows, int32_t vocab, const void *l
   if (rows > 0 && !logits) return fail(DFLASH_EINVAL, "logits is NULL");
   if (row_stride < vocab) return fail(DFLASH_EINVAL, "row_stride < vocab");
   if ((uintptr_t)logits % elem(dtype)) return fail(DFLASH_EINVAL, "logits misaligned");
+  if (!aligned4(sp->temperature, sp->top_k, sp->top_p, sp->min_p))
+    return fail(DFLASH_EINVAL, "sampling parameters must be 4-byte aligned");
   std::memset(p, 0, sizeof(*p));
   p->logits = logits;
   p->ld = row_stride;
@@ -167,6 +174,7 @@ int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
   const bool empty = batch == 0 || total_rows == 0;
   if (!empty && (!row_start || !kv_len || !k || !v))
     return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
   const size_t es = elem(kv->dtype);
   const int64_t qw = (int64_t)kv->n_heads * kv->head_dim, kw = (int64_t)kv->n_kv_heads * kv->head_dim;
   if (!empty && ((q && (q_stride < qw || q_out_stride < qw)) || k_stride < kw || v_stride < kw))
@@ -175,6 +183,8 @@ int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
       !aligned16(k, k_stride, es) || !aligned16(v, v_stride, es) || (uintptr_t)q_gain % 16 ||
       (uintptr_t)k_gain % 16)
     return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
+  if (q && q == q_out && q_stride != q_out_stride && total_rows > 1)
+    return fail(DFLASH_EINVAL, "q_out is q with another row stride");
   if (int st = handle_ready(h, &p.err)) return st;
   if (empty) return DFLASH_OK;
   p.rows = paged_rows(kv, batch, total_rows, row_start, kv_len);
@@ -228,6 +238,7 @@ int dflash_paged_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t 
   if (batch == 0 || total_rows == 0) return handle_ready(h, &p.err);
   if (!row_start || !kv_len || !q || !out) return fail(DFLASH_EINVAL, "a required pointer is NULL");
   if (q == out) return fail(DFLASH_EINVAL, "out must not be q");
+  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
   const size_t es = elem(kv->dtype);
   const int64_t qw = (int64_t)kv->n_heads * kv->head_dim;
   if (q_stride < qw || out_stride < qw) return fail(DFLASH_EINVAL, "a row stride is below the row's width");
@@ -282,6 +293,7 @@ int dflash_sample_tokens(dflash_handle *h, int32_t rows, int32_t vocab, const vo
   if (int st = sampling_params(h, rows, vocab, logits, dtype, row_stride, params, &p)) return st;
   if (rows == 0) return handle_ready(h, &p.err);
   if (!exp_noise || !ids) return fail(DFLASH_EINVAL, "exp_noise or ids is NULL");
+  if (!aligned4(exp_noise, ids, prob)) return fail(DFLASH_EINVAL, "exp_noise, ids and prob must be 4-byte aligned");
   if (int st = handle_ready(h, &p.err)) return st;
   p.noise = exp_noise;
   p.ids = ids;

@@ -186,3 +186,20 @@ def test_sampling_refusals(handle):
     refused(-6, call_probs, handle, probs=FAKE - 1600)     # ends where the logits begin
     refused(-1, call_sample, handle, noise=None)
     refused(-1, call_sample, handle, ids=None)
+
+
+def test_misaligned_arrays_and_overlapping_outputs_are_refused(handle):
+    for bad in [dict(row_start=FAKE + 2), dict(kv_len=FAKE + 1), dict(os_=1032),
+                dict(kv=layer(page_table=FAKE + 2)),
+                dict(kv=layer(prefix_len=64, prefix_pages=FAKE + 1))]:
+        refused(-1, call_append, handle, **bad)
+    refused(-6, call_append, handle, os_=1032, rows=1)      # one row: the stride is not used
+    for bad in [dict(row_start=FAKE + 2), dict(kv_len=FAKE + 1), dict(kv=layer(page_table=FAKE + 2)),
+                dict(kv=layer(prefix_len=64, prefix_pages=FAKE + 1))]:
+        refused(-1, call_attend, handle, **bad)
+    for call in (call_probs, call_sample):
+        for i in range(4):
+            sp = pkg.DflashSampling(*[FAKE + 2 * (i == j) for j in range(4)], 2)
+            refused(-1, call, handle, sp=sp)
+    refused(-1, call_sample, handle, noise=FAKE + 2)
+    refused(-1, call_sample, handle, ids=FAKE + 1)
