@@ -15,8 +15,8 @@
 // One CTA per token.  A thread holds two 16-byte chunks of a head D/2 dims
 // apart, the chunks of a head's half in consecutive lanes: the mean square is a
 // shuffle reduction over those lanes, and where the rotation covers the whole
-// head both sides of a pair are in one thread (partial rotations of halves go
-// through shared memory).  A thread's sines and cosines serve all its heads and
+// head both sides of a pair are in one thread (in another lane where it covers
+// at most half of the head; other halves go through shared memory).  A thread's sines and cosines serve all its heads and
 // stay in registers.  With a chunk a thread and the pair's other side in another
 // lane, shared-memory accesses and shuffles bound it instead of HBM: 2048 tokens
 // of 32 + 8 + 8 heads of 128 took 24.0 us.  A thread's first kU units (pairs of
@@ -66,7 +66,9 @@ template <> struct Chunk<float> {
   }
 };
 
-enum Rotation { kInterleaved, kWholeHalves, kPartHalves };
+// pairs (2i, 2i+1); halves of the whole head; halves within a head's first half, of whole chunks;
+// any other halves
+enum Rotation { kInterleaved, kWholeHalves, kLowHalves, kPartHalves };
 
 // L lanes per head; D = 2 L E.
 template <typename T, int L, int ROT>
@@ -125,12 +127,16 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  // the pairs whose both sides this thread holds
+  // the pairs of this thread's values
+  const int hl = half / E;             // lanes of half the rotated dims (kLowHalves)
+  const bool lo = lane < hl, rotated = lane < 2 * hl;
   float2 cs[E];
   if (ROT != kPartHalves) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int i = ROT == kWholeHalves ? lane * E + e : (e / (E / 2)) * (D / 4) + lane * (E / 2) + e % (E / 2);
+      const int i = ROT == kWholeHalves ? lane * E + e
+                    : ROT == kLowHalves ? (lo ? lane : lane - hl) * E + e
+                                        : (e / (E / 2)) * (D / 4) + lane * (E / 2) + e % (E / 2);
       cs[e] = s_cs[i < half ? i : 0];
     }
   }
@@ -190,6 +196,13 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
           x[e] = a * cs[e].x - bb * cs[e].y;
           x[E + e] = bb * cs[e].x + a * cs[e].y;
         }
+      } else if (ROT == kLowHalves) {
+        const int from = rotated ? (lo ? lane + hl : lane - hl) : lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float y = __shfl_sync(0xffffffffu, x[e], from, L);
+          if (rotated) x[e] = lo ? x[e] * cs[e].x - y * cs[e].y : x[e] * cs[e].x + y * cs[e].y;
+        }
       } else {
         // dim d of this head: side d / (D / 2), lane d / E % L, value d % E
         float *at = s_x + (tid - lane);
@@ -232,6 +245,8 @@ cudaError_t launch(const AppendParams &p, cudaStream_t s) {
   const dim3 grid(p.rows.total_rows), block(nt);
   if (p.inter || p.rot == 0) return launch_pdl(append_kv_kernel<T, L, kInterleaved>, grid, block, 0, s, p);
   if (p.rot == D) return launch_pdl(append_kv_kernel<T, L, kWholeHalves>, grid, block, 0, s, p);
+  if (p.rot <= D / 2 && p.rot / 2 % E == 0)
+    return launch_pdl(append_kv_kernel<T, L, kLowHalves>, grid, block, 0, s, p);
   return launch_pdl(append_kv_kernel<T, L, kPartHalves>, grid, block, sizeof(float) * 2 * E * nt, s, p);
 }
 
