@@ -27,9 +27,9 @@
 //
 // Measured (32 query heads on 8 KV heads of 128, graph replays): two prompts of
 // 2500 and 4096 tokens 215 us, 880 TFLOP/s of visible products; 32 requests x 16
-// rows over a shared prefix of 8192 and 256..4096 rows of their own 149 us
+// rows over a shared prefix of 8192 and 256..4096 rows of their own 148 us
 // (kernel 130, plan and join 19); 64 single tokens of 64 heads over a prefix of
-// 16384 120 us; one token over 1001 keys 19 us.  A 128-key step takes a stream
+// 16384 118 us; one token over 1001 keys 19 us.  A 128-key step takes a stream
 // about 5000 clocks: 2350 in the softmax (TMEM reads, the maximum, exponentials
 // and the rounding of 128 scores a thread), 1400 in its two products, the rest
 // waiting for its turn at the tensor pipe and for barriers: the tensor pipe is
@@ -92,7 +92,7 @@ struct Request {
 };
 struct Head {
   int items, merge, prefix_splits, prefix_tiles;
-  int first_row, rows, taken, pad;        // rows that meet the prefix; items handed out
+  int first_row, rows, taken, pad;        // rows that meet the prefix; items handed out past one a CTA
 };
 
 struct Params {
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
         int idx = 0;
         if (lane == 0) {
           if (!mbar_wait(&item_empty[e], ((n_item / NQ) & 1) ^ 1)) idx = -1;
-          else idx = atomicAdd(&p.head->taken, 1);
+          else idx = n_item == 0 ? blockIdx.x : gridDim.x + atomicAdd(&p.head->taken, 1);
         }
         idx = __shfl_sync(0xffffffffu, idx, 0);
         if (idx < 0) {
