@@ -88,7 +88,7 @@ struct Fixed {
   u64 warp_m[NT / 32];
   int warp_c[NT / 32];
   float group[GROUPS];           // maxima of groups of four threads
-  int own_n;                     // tokens that this CTA lists
+  int own_n, own_at;             // tokens that this CTA lists, their place in the leader's list
   u64 own_rest;                  // weight outside the histogram
   u64 w_rest[NT / 32], w_listed[NT / 32];
   float fred[NT / 32];
@@ -807,18 +807,12 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     Fixed &lead = *cl.map_shared_rank(&f, 0);
     const bool weights = top_k == 0 && !by_min_p;
     u64 listed = 0, rest = 0;
-    int count = 0;
     float part0 = 0.f, part1 = 0.f;
+    // to this CTA's list first (weighed and sent together below): what a token costs here, all lanes
+    // of its warp wait for
     auto list_token = [&](float x, int id) {
-      ++count;
-      if (weights) {
-        int b;
-        uint32_t u;
-        weigh(x, tab, b, u);
-        listed += units(u, b);
-      }
-      const int at = atomicAdd(&lead.n_list, 1);
-      if (at < CAP) lead.list[at] = key_of(x, id);
+      const int at = atomicAdd(&f.own_n, 1);
+      if (at < CAP) f.sorted[at] = key_of(x, id);
     };
     // most vectors hold no token of the list
     auto list_some = [&](int id, const float *x) {
@@ -844,8 +838,16 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     } else {
       tokens.template each_vector<4>(list_some);
     }
-    if (count) atomicAdd(&f.own_n, count);
+    __syncthreads();
+    const int own_n = min(f.own_n, CAP);
+    if (tid == 0) f.own_at = own_n > 0 ? atomicAdd(&lead.n_list, own_n) : 0;
     if (weights) {
+      for (int i = tid; i < own_n; i += NT) {
+        int b;
+        uint32_t u;
+        weigh(order_value((uint32_t)(f.sorted[i] >> 32)), tab, b, u);
+        listed += units(u, b);
+      }
       rest = (u64)((part0 + part1) * 0x1p44f);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -858,6 +860,8 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       }
     }
     __syncthreads();
+    for (int i = tid; i < own_n; i += NT)
+      if (f.own_at + i < CAP) lead.list[f.own_at + i] = f.sorted[i];
     if (tid < C) {
       Fixed &o = *cl.map_shared_rank(&f, tid);
       u64 r = 0, l = 0;
