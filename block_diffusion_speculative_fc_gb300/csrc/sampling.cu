@@ -16,10 +16,10 @@
 //
 // Measured: 16 rows of 151936 bf16 logits with top-k and top-p 13.1 us (clusters
 // of 8, latency: loads, five cluster barriers, the list's sort); 2048 rows of
-// mixed kinds 530 us, 3.5 TB/s of the floor's bytes (two CTAs of 16 warps an SM
+// mixed kinds 519 us, 3.6 TB/s of the floor's bytes (two CTAs of 16 warps an SM
 // take turns loading, scanning and storing; 417 us with top-k and top-p in every
-// row, 675 us with top-p alone, where 8% of the rows need the histogram); one
-// draw 8.8 us, 128 draws of 163840 logits 63 us (the rows with the histogram
+// row, 645 us with top-p alone, where 8% of the rows need the histogram); one
+// draw 8.8 us, 128 draws of 163840 logits 61 us (the rows with the histogram
 // take 40 us each, the others 10).
 //
 // Most rows keep few tokens, and those are found without a histogram or a
@@ -317,6 +317,10 @@ template <typename T, bool RESIDENT> struct Slice {
   }
   // fn(first id, E values) of every vector, U of them in flight
   template <int U, typename F> __device__ __forceinline__ void each_vector(F fn) const {
+    each_vector<U>([](int, int, const float *) {}, [&](int, int id, const float *x) { fn(id, x); });
+  }
+  // ahead(u, first id, values) of U vectors, then fn(u, first id, values) of them
+  template <int U, typename A, typename F> __device__ __forceinline__ void each_vector(A ahead, F fn) const {
     const uint4 *at = vectors();
     for (int v0 = threadIdx.x; v0 < nv; v0 += U * NT) {
       uint4 t[U];
@@ -326,17 +330,29 @@ template <typename T, bool RESIDENT> struct Slice {
         t[u] = make_uint4(0, 0, 0, 0);
         if (RESIDENT ? v < nv : v < nv && whole(v)) t[u] = at[v];
       }
+      auto values = [&](int u, int v, float *x) {
+        Elem<T>::unpack(t[u], x);
+        if (!RESIDENT && (dirty || !whole(v))) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = slow(v, e);
+        }
+      };
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int v = v0 + u * NT;
+        float x[E];
         if (v < nv) {
-          float x[E];
-          Elem<T>::unpack(t[u], x);
-          if (!RESIDENT && (dirty || !whole(v))) {
+          values(u, v, x);
+          ahead(u, start + v * E - mis, x);
+        }
+      }
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = slow(v, e);
-          }
-          fn(start + v * E - mis, x);
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT;
+        float x[E];
+        if (v < nv) {
+          values(u, v, x);
+          fn(u, start + v * E - mis, x);
         }
       }
     }
@@ -1014,30 +1030,34 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     // ids ascend, so the first of equal scores has the lowest
     float top = -1.f;
     int top_id = 0;
-    tokens.template each_vector<2>([&](int id, const float *x) {
-      float e[E];
-      bool any = false;
+    float e[2][E];                       // the noise of two vectors is in flight
+    bool any[2];
+    auto fetch = [&](int u, int id, const float *x) {
+      any[u] = false;
 #pragma unroll
-      for (int i = 0; i < E; ++i) any = any || kept(x[i], id + i);
-      if (!any) return;
+      for (int i = 0; i < E; ++i) any[u] = any[u] || kept(x[i], id + i);
+      if (!any[u]) return;
       if (((uintptr_t)(noise + id) & 15) == 0 && id >= start && id + E <= start + n) {
 #pragma unroll
         for (int i = 0; i < E; i += 4) {
           const float4 t = __ldcs(reinterpret_cast<const float4 *>(noise + id + i));
-          e[i] = t.x, e[i + 1] = t.y, e[i + 2] = t.z, e[i + 3] = t.w;
+          e[u][i] = t.x, e[u][i + 1] = t.y, e[u][i + 2] = t.z, e[u][i + 3] = t.w;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) e[i] = kept(x[i], id + i) ? noise[id + i] : 1.f;
+        for (int i = 0; i < E; ++i) e[u][i] = kept(x[i], id + i) ? noise[id + i] : 1.f;
       }
+    };
+    tokens.template each_vector<2>(fetch, [&](int u, int id, const float *x) {
+      if (!any[u]) return;
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const bool k = kept(x[i], id + i);
         const float w = k ? ex2((x[i] - m) * c) : 0.f;
         if (i & 1) s1 += w;
         else s0 += w;
-        if (k && __fdividef(w, e[i]) * 1.000001f >= top) {
-          const float score = __fdiv_rn(w, e[i]);
+        if (k && __fdividef(w, e[u][i]) * 1.000001f >= top) {
+          const float score = __fdiv_rn(w, e[u][i]);
           if (score > top) {
             top = score;
             top_id = id + i;
