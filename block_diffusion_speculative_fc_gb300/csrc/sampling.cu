@@ -60,7 +60,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int NT = 512;          // threads of a CTA
-constexpr int NB = 1024;         // histogram bins: a = 0 .. 31.97 and one for the rest
+constexpr int NB = 1024;         // histogram bins: a = 0 .. 31.95 and one for the rest
+constexpr float TAIL = 31.95f;   // a of the last bin's first token (inside the bin before it)
 constexpr int PB = NB / NT;      // bins of a thread in a scan
 constexpr int CAP = 1024;        // gathered tokens (two a thread)
 constexpr int MAX_K = 512;       // top-k of the short way
@@ -142,7 +143,7 @@ struct Weigher {
   __device__ __forceinline__ void operator()(float x, const Tables &t, int &bin, uint32_t &u) const {
     float a, al;
     distance(x, a, al);
-    if (!(a < 31.95f)) {                // far tail (a may be infinite, al then NaN)
+    if (!(a < TAIL)) {                  // far tail (a may be infinite, al then NaN)
       bin = NB - 1;
       u = (uint32_t)(ex2(31.f - a) * 0x1p26f);
       return;
@@ -488,19 +489,28 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       o.cut = cut;
     }
   };
+  // A cut that no bin or token holds (bins and key ranges that disagree): flagged, and the row ends
+  // with the cut of the stage before.
+  auto no_cut = [&] {
+    if (tid == 0) raise_error(err, DFLASH_DERR_TIMEOUT);
+    tell(CMD_DONE, 0);
+  };
   auto tell_range = [&](int count) {
     int sh = 0;
     while (((hi - lo - 1) >> sh) >= NB) ++sh;
     if (tid == 0) f.n_list = 0;
     tell(count <= CAP ? CMD_GATHER : CMD_SPLIT, sh);
   };
-  // start of a stage: the first histogram's bin, and its range of keys (somewhat wider than it)
+  // start of a stage: the first histogram's bin, and its range of keys, somewhat wider than it (the
+  // last bin begins at TAIL, not half a bin before its number)
   auto begin = [&] {
     bin = select(n0, above0, above_m0, 0, 0);
+    if (bin < 0) return no_cut();
     float x_hi = FLT_MAX, x_lo = -FLT_MAX;
     if (tid < C) {
       const double inv = (double)temp * 0.6931471805599453 / 32.0;
-      x_hi = __double2float_ru(fmax((double)m - fmax(0.0, (bin - 0.51) * inv), -(double)FLT_MAX));
+      const double first = bin < NB - 1 ? bin - 0.51 : 32.0 * TAIL - 0.01;
+      x_hi = __double2float_ru(fmax((double)m - fmax(0.0, first * inv), -(double)FLT_MAX));
       if (bin < NB - 1) x_lo = __double2float_rd(fmax((double)m - (bin + 0.51) * inv, -(double)FLT_MAX));
     }
     x_hi = __shfl_sync(0xffffffffu, x_hi, 0);
@@ -538,13 +548,17 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         totals(nn, mm, bin);
         scan(nn, mm, ab, abm, tc, tm);
         const int s = select(nn, ab, abm, above, above_m);
-        const int sh = f.sh;
-        const u64 v = (u64)(NB - 1 - s);
-        const u64 l = lo + (v << sh), h = l + (1ull << sh);
-        lo = l;
-        hi = h < hi ? h : hi;
-        __syncthreads();   // sh has been read
-        tell_range(f.sel_n);
+        if (s < 0) {
+          no_cut();
+        } else {
+          const int sh = f.sh;
+          const u64 v = (u64)(NB - 1 - s);
+          const u64 l = lo + (v << sh), h = l + (1ull << sh);
+          lo = l;
+          hi = h < hi ? h : hi;
+          __syncthreads();   // sh has been read
+          tell_range(f.sel_n);
+        }
       } else if (f.n_list > CAP) {
         const int over = f.n_list;
         __syncthreads();
@@ -569,8 +583,10 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         }
         scan(nn, mm, ab, abm, tc, tm);
         const int s = select(nn, ab, abm, above, above_m);   // the cut's place in the list
-        cut = f.sorted[s];
-        if (stage == 0 && top_p < 1.f) {
+        if (s >= 0) cut = f.sorted[s];
+        if (s < 0) {
+          no_cut();
+        } else if (stage == 0 && top_p < 1.f) {
           if (s / 2 == tid) f.range_lo = above_m + mm[s % 2];   // weight through the cut
           __syncthreads();
           const u64 through = f.range_lo;

@@ -1,0 +1,130 @@
+"""Rows whose cut falls where the sampling kernels change their way of finding it.
+
+Kept sets are checked in every row: a cut may lie on either side of a token only where that token's
+cumulative share is within 2^-26 of top_p (the kernel's border sums are good to about 2^-28), and
+nowhere among equal weights, whose whole-number sums are exact.  Probabilities: as in
+test_gpu_sampling.py, p (3 a 2^-24 + 2^-21 + 100 * 2^-24).
+"""
+import math
+from fractions import Fraction
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from tests.target_reference import make_session  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+INF = math.inf
+TOL = 2.0 ** -21 + 100 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def sess():
+    s = make_session()
+    yield s
+    s.close()
+
+
+def order64(x):
+    """Finite logits in the kernel's order: values in float64, ids.  -0 and +0 are equal."""
+    big = torch.finfo(x.dtype).max
+    x = x.double() + 0.0
+    x = torch.where(x.isnan(), -INF, x).clamp(max=big)
+    v, at = x.sort(descending=True, stable=True)
+    n = int((v > -INF).sum())
+    return v[:n], at[:n]
+
+
+def cut_range(w, k, p):
+    """Fewest and most tokens that top-k and top-p may keep of weights in descending order."""
+    n = min(k, w.numel()) if k > 0 else w.numel()
+    if p >= 1:
+        return n, n
+    w = w[:n]
+    if bool((w == w[0]).all()):
+        exact = max(1, math.ceil(Fraction(p) * n)) if p > 0 else 1
+        return exact, exact
+    share = (w.cumsum(0) - w) / w.sum()
+    return (max(1, int((share < p - 2.0 ** -26).sum())), max(1, int((share < p + 2.0 ** -26).sum())))
+
+
+def check_row(x, T, k, p, probs, noise, token, prob):
+    T, p = (float(torch.tensor(t, dtype=F32)) for t in (T, p))
+    v, at = order64(x)
+    if T < 2.0 ** -126:
+        a, k, p = torch.zeros_like(v), 1, 1.0
+    else:
+        a = (v[0] - v) / T
+    w = torch.exp(-a)
+    lo, hi = cut_range(w, k, p)
+    got = probs.double()
+    n = int((got > 0).sum())
+    assert lo <= n <= hi, (T, k, p, lo, hi, n)
+    kept = torch.zeros(x.numel(), dtype=torch.bool, device=x.device)
+    kept[at[:n]] = True
+    assert torch.equal(kept, got > 0), (T, k, p)
+    want = w[:n] / w[:n].sum()
+    tol = want * (3 * a[:n] * 2.0 ** -24 + TOL)
+    assert bool(((got[at[:n]] - want).abs() <= tol).all()), (T, k, p)
+    score = w[:n] / noise[at[:n]].double()
+    best = int((at[:n] == token).nonzero())
+    assert float(score[best]) >= float(score.max()) * (1 - 2.0 ** -14)
+    assert abs(prob - float(want[best])) <= float(tol[best])
+
+
+def check(sess, x, entries, seed=0, many=False):
+    """Rows of x with (T, top-k, top-p) each; many: the rows repeated until they are a large batch,
+    which takes a CTA a row."""
+    R, V = x.shape
+    times = -(-320 // R) if many else 1
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    noise = torch.empty((R, V), device="cuda").exponential_(generator=g).clamp_(min=1e-30)
+    xs, ns = x.repeat(times, 1), noise.repeat(times, 1)
+    T, k, p = zip(*(entries * times))
+    ps = dict(temperature=torch.tensor(T, device="cuda"), top_p=torch.tensor(p, device="cuda"),
+              top_k=torch.tensor(k, dtype=torch.int32, device="cuda"))
+    probs = torch.full(xs.shape, -1.0, device="cuda")
+    ids = torch.full((R * times,), -9, dtype=torch.int32, device="cuda")
+    prob = torch.full((R * times,), -1.0, device="cuda")
+    sess.target_probs(xs, probs, **ps)
+    assert sess.error() == 0
+    sess.sample_tokens(xs, ns, ids, prob=prob, **ps)
+    assert sess.error() == 0
+    for t in (probs, ids, prob):
+        assert torch.equal(t, t[:R].repeat(times, *[1] * (t.dim() - 1)))
+    for r in range(R):
+        check_row(x[r], *entries[r], probs[r], noise[r], int(ids[r]), float(prob[r]))
+
+
+def levels(V, dtype, seed, *groups):
+    """A row of (count, value) groups at random places, -infinity elsewhere."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    at = torch.randperm(V, generator=g, device="cuda").split([n for n, _ in groups] +
+                                                             [V - sum(n for n, _ in groups)])
+    x = torch.full((V,), -INF, device="cuda")
+    for i, (_, value) in zip(at, groups):
+        x[i] = value
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_cuts_at_the_first_tokens_of_the_tail(sess, dtype, many):
+    """32 (m - x) log2(e) / T between 1022.40 and 1022.49: the last bin of the histogram holds these
+    tokens though their number rounds to the bin before."""
+    low = -22.125                                # in both types
+    T = 22.125 * math.log2(math.e) / 31.9514     # a = 31.9514
+    rows, entries = [], []
+    for groups, ks in [([(500, 0.0), (500, low)], (600, 999)),                       # all of the tail
+                       ([(500, 0.0), (300, low), (300, -25.0)], (700, 800, 900)),
+                       ([(100, 0.0), (2000, low)], (400, 700)),
+                       ([(600, 0.0), (1, low), (1500, -30.0)], (601, 602)),
+                       ([(1, 0.0), (3000, low)], (2, 513, 3000))]:
+        for k in ks:
+            rows.append(levels(4099, dtype, k, *groups))
+            entries.append((T, k, 1.0))
+    check(sess, torch.stack(rows), entries, many=many)
