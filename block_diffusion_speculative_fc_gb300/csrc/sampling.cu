@@ -456,7 +456,8 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       w += mm[i];
     }
   };
-  // the bin that holds the cut, given what lies above every bin
+  // the bin that holds the cut, given what lies above every bin; there is one unless bins and key
+  // ranges disagree, which is flagged
   auto select = [&](const int *nn, const int *ab, const u64 *abm, int base, u64 base_m) {
     if (tid == 0) f.sel_bin = -1;
     __syncthreads();
@@ -465,8 +466,9 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       if (nn[i] > 0 && (stage == 0 ? base + ab[i] < top_k : base_m + abm[i] < target)) mine = tid * PB + i;
     if (mine >= 0) atomicMax(&f.sel_bin, mine);
     __syncthreads();
-    const int s = f.sel_bin;
-    if (s >= 0 && s / PB == tid) {
+    const int s = max(f.sel_bin, 0);
+    if (tid == 0 && f.sel_bin < 0) raise_error(err, DFLASH_DERR_TIMEOUT);
+    if (s / PB == tid) {
       const int i = s % PB;
       f.sel_n = nn[i];
       f.sel_above = base + ab[i];
@@ -489,12 +491,6 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       o.cut = cut;
     }
   };
-  // A cut that no bin or token holds (bins and key ranges that disagree): flagged, and the row ends
-  // with the cut of the stage before.
-  auto no_cut = [&] {
-    if (tid == 0) raise_error(err, DFLASH_DERR_TIMEOUT);
-    tell(CMD_DONE, 0);
-  };
   auto tell_range = [&](int count) {
     int sh = 0;
     while (((hi - lo - 1) >> sh) >= NB) ++sh;
@@ -505,7 +501,6 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
   // last bin begins at TAIL, not half a bin before its number)
   auto begin = [&] {
     bin = select(n0, above0, above_m0, 0, 0);
-    if (bin < 0) return no_cut();
     float x_hi = FLT_MAX, x_lo = -FLT_MAX;
     if (tid < C) {
       const double inv = (double)temp * 0.6931471805599453 / 32.0;
@@ -548,17 +543,13 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         totals(nn, mm, bin);
         scan(nn, mm, ab, abm, tc, tm);
         const int s = select(nn, ab, abm, above, above_m);
-        if (s < 0) {
-          no_cut();
-        } else {
-          const int sh = f.sh;
-          const u64 v = (u64)(NB - 1 - s);
-          const u64 l = lo + (v << sh), h = l + (1ull << sh);
-          lo = l;
-          hi = h < hi ? h : hi;
-          __syncthreads();   // sh has been read
-          tell_range(f.sel_n);
-        }
+        const int sh = f.sh;
+        const u64 v = (u64)(NB - 1 - s);
+        const u64 l = lo + (v << sh), h = l + (1ull << sh);
+        lo = l;
+        hi = h < hi ? h : hi;
+        __syncthreads();   // sh has been read
+        tell_range(f.sel_n);
       } else if (f.n_list > CAP) {
         const int over = f.n_list;
         __syncthreads();
@@ -583,10 +574,8 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         }
         scan(nn, mm, ab, abm, tc, tm);
         const int s = select(nn, ab, abm, above, above_m);   // the cut's place in the list
-        if (s >= 0) cut = f.sorted[s];
-        if (s < 0) {
-          no_cut();
-        } else if (stage == 0 && top_p < 1.f) {
+        cut = f.sorted[s];
+        if (stage == 0 && top_p < 1.f) {
           if (s / 2 == tid) f.range_lo = above_m + mm[s % 2];   // weight through the cut
           __syncthreads();
           const u64 through = f.range_lo;
