@@ -111,8 +111,9 @@ struct Fixed {
 
 enum { CMD_GATHER = 0, CMD_SPLIT = 1, CMD_DONE = 2 };
 
+// -0 and +0 have one image (-0 + 0 = +0): equal logits go by id.
 __device__ __forceinline__ uint32_t order_image(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float order_value(uint32_t k) {

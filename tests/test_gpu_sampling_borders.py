@@ -128,3 +128,23 @@ def test_cuts_at_the_first_tokens_of_the_tail(sess, dtype, many):
             rows.append(levels(4099, dtype, k, *groups))
             entries.append((T, k, 1.0))
     check(sess, torch.stack(rows), entries, many=many)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_zeros_of_either_sign_are_equal(sess, dtype, many):
+    """-0 and +0 are one logit: the lower id comes first, greedy, in the list and in the histogram."""
+    V = 4099
+    x = torch.full((10, V), -3.0, device="cuda")
+    x[0, 7], x[0, 8] = -0.0, 0.0
+    x[1, 0], x[1, V - 1] = -0.0, 0.0
+    x[2, :40:2], x[2, 1:40:2] = -0.0, 0.0            # a short list, cut among them
+    x[3] = x[2]
+    x[4, :2000:2], x[4, 1:2000:2] = -0.0, 0.0        # more than a list holds
+    x[5] = x[4]
+    x[6], x[7], x[8], x[9] = x[4], x[4], 0.0, -0.0
+    x[6, 5], x[7, 5] = 1e-38, -1e-38                 # the smallest neighbours keep their order
+    x[8, ::3] = -0.0
+    entries = [(0.0, 0, 1.0), (1.0, 1, 1.0), (1.0, 9, 1.0), (1.0, 30, 0.5), (1.0, 600, 1.0), (1.0, 0, 0.3),
+               (1.0, 601, 1.0), (1.0, 1500, 0.4), (1.0, 700, 0.9), (1.0, 1000, 1.0)]
+    check(sess, x.to(dtype), entries, many=many)
