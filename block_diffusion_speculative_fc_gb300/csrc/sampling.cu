@@ -664,6 +664,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
       min_p = 0.f;
     }
   }
+  if (top_p < 0.f) top_p = 0.f;   // the first token alone, as 0 (NaN stays for the check below)
   if (top_k <= 0 || top_k >= V) top_k = 0;
   const bool filtered = top_k > 0 || top_p < 1.f;
   // nothing is dropped: the sum of the weights goes along with the first pass, relative to the

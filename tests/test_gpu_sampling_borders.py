@@ -148,3 +148,13 @@ def test_zeros_of_either_sign_are_equal(sess, dtype, many):
     entries = [(0.0, 0, 1.0), (1.0, 1, 1.0), (1.0, 9, 1.0), (1.0, 30, 0.5), (1.0, 600, 1.0), (1.0, 0, 0.3),
                (1.0, 601, 1.0), (1.0, 1500, 0.4), (1.0, 700, 0.9), (1.0, 1000, 1.0)]
     check(sess, x.to(dtype), entries, many=many)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_top_p_below_zero_keeps_the_first_token(sess, dtype, many):
+    V = 4099
+    flat = torch.ones((2, V), device="cuda")
+    flat[1] = torch.linspace(0, 1e-3, V, device="cuda")
+    x = torch.cat([flat, flat, flat]).to(dtype)
+    check(sess, x, [(1.0, 0, 0.0)] * 2 + [(1.0, 0, -1.0)] * 2 + [(1.0, 0, -3e38), (2.0, 700, -1e10)], many=many)
