@@ -70,6 +70,9 @@ constexpr int MAXC = 8;          // CTAs of a cluster
 constexpr int GROUPS = NT / 4;
 constexpr int STREAM_VOCAB = 1 << 18;   // tokens of a CTA at most (sums of the histogram)
 constexpr int MAX_SMEM = 220 * 1024;
+// Up to here two logits whose difference passes the largest float differ by a weight of 0; above it
+// they need not, and an infinite difference says nothing of the place of the lower one.
+constexpr float MAX_T = 0x1p100f;
 
 struct Tables {
   uint32_t u[32];                // round(2^26 2^(-i/32))
@@ -721,7 +724,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     }
     if (!RESIDENT) tokens.dirty = __syncthreads_or(dirty) != 0;
   }
-  if (!(temp >= 0.f) || isinf(temp) || isnan(top_p) || !(min_p <= 1.f)) {
+  if (!(temp >= 0.f && temp <= MAX_T) || isnan(top_p) || !(min_p <= 1.f)) {
     if (rank == 0 && tid == 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
     return;   // the whole cluster, before any of its barriers
   }

@@ -588,7 +588,7 @@ int dflash_paged_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t 
  * Sampling parameters: device arrays of rows / rows_per_entry entries (row r
  * uses entry r / rows_per_entry; block_size rows an entry for a verify
  * block), NULL for the value that does nothing.
- *   temperature  (1) >= 0, finite; weights w_v = exp((x_v - max x) / T).
+ *   temperature  (1) 0 to 2^100; weights w_v = exp((x_v - max x) / T).
  *                0 (or below 2^-126): the largest logit alone, lowest id on ties
  *   top_k        (0) the k largest logits, lower ids first among equal ones; <=
  *                0 or >= vocab: all

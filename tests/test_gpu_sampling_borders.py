@@ -158,3 +158,25 @@ def test_a_top_p_below_zero_keeps_the_first_token(sess, dtype, many):
     flat[1] = torch.linspace(0, 1e-3, V, device="cuda")
     x = torch.cat([flat, flat, flat]).to(dtype)
     check(sess, x, [(1.0, 0, 0.0)] * 2 + [(1.0, 0, -1.0)] * 2 + [(1.0, 0, -3e38), (2.0, 700, -1e10)], many=many)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_largest_temperature_and_the_largest_differences(sess, dtype):
+    """At T = 2^100 logits that differ by more than the largest float weigh nothing beside the
+    maximum, and keep their place in the order; a temperature above is refused."""
+    V, top = 4099, 2.0 ** 100
+    x = torch.stack([levels(V, dtype, i, (2000, 3e38), (2000, -3e38)) for i in range(4)])
+    check(sess, x[:3], [(top, 0, 0.5), (top, 1500, 1.0), (top, 1200, 0.25)])
+    k = torch.tensor([3000, 0, 2000, 1], dtype=torch.int32, device="cuda")
+    T = torch.tensor([top, 2 * top, 3e38, top], device="cuda")
+    probs = torch.full((4, V), -1.0, device="cuda")
+    ids = torch.full((4,), -5, dtype=torch.int32, device="cuda")
+    sess.target_probs(x, probs, temperature=T, top_k=k)
+    assert sess.error() == 0x80
+    sess.sample_tokens(x, torch.ones((4, V), device="cuda"), ids, temperature=T, top_k=k)
+    assert sess.error() == 0x80
+    assert bool((probs[1:3] == -1).all()) and ids.tolist()[1:3] == [-5, -5]
+    high = x > 0
+    assert torch.equal(probs[0] > 0, high[0]) and bool(((probs[0][high[0]] * 2000 - 1).abs() < TOL).all())
+    first = int(high[3].nonzero()[0])
+    assert int(ids[0]) == int(high[0].nonzero()[0]) and int(ids[3]) == first and float(probs[3, first]) == 1
