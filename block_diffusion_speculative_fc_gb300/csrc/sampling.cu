@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
           sum_f += e[i];
           ids[i] = keep[i] ? (int)~(uint32_t)f.sorted[at] : 0;
           if (DRAW && keep[i]) {
-            const u64 k = argmax_key(e[i] / noise[ids[i]], ids[i]);
+            const float variate = noise[ids[i]], score = e[i] / variate;
+            const u64 k = variate >= 0.f && score >= 0.f ? argmax_key(score, ids[i]) : 0;
             best = k > best ? k : best;
           }
         }
@@ -980,9 +981,11 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
           if (warp == 0) {
             best = warp_max_key(f.kred[lane & (NT / 32 - 1)]);
             if (lane == 0) {
-              const int id = argmax_key_index(best);
+              const int id = best ? argmax_key_index(best) : -1;
               p.ids[row] = id;
-              if (p.prob) {
+              if (id < 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
+              if (p.prob && id < 0) p.prob[row] = 0.f;
+              else if (p.prob) {
                 const float xd = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
                 p.prob[row] = ex2((fminf(xd, Elem<T>::largest()) - m) * c) * inv;
               }
@@ -1068,7 +1071,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
         else s0 += w;
         if (k && __fdividef(w, e[u][i]) * 1.000001f >= top) {
           const float score = __fdiv_rn(w, e[u][i]);
-          if (score > top) {
+          if (score > top && e[u][i] >= 0.f) {
             top = score;
             top_id = id + i;
           }
@@ -1102,9 +1105,12 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     if (rank == 0 && tid == 0) {
       best = 0;
       for (int r = 0; r < C; ++r) best = f.x_race[r] > best ? f.x_race[r] : best;
-      const int id = argmax_key_index(best);
+      // no score: every kept token's variate is negative or NaN
+      const int id = best ? argmax_key_index(best) : -1;
       p.ids[row] = id;
-      if (p.prob) {
+      if (id < 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
+      if (p.prob && id < 0) p.prob[row] = 0.f;
+      else if (p.prob) {
         float x = to_f32(((const T *)p.logits)[(int64_t)row * p.ld + id]);
         x = fminf(x, Elem<T>::largest());
         p.prob[row] = ex2((x - m) * c) * inv;

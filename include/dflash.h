@@ -627,7 +627,9 @@ int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const voi
  * the kept v of w_v / exp_noise[r][v] (the exponential race of
  * dflash_accept_commit_sampled: an exact draw, lowest id on ties, float32
  * IEEE division), read only where v is kept.
- *   exp_noise  device float32 [rows, vocab] Exp(1) variates (> 0)
+ *   exp_noise  device float32 [rows, vocab] Exp(1) variates (> 0).  Tokens whose
+ *              variate is negative or NaN are not drawn; where no kept token is
+ *              left the row sets DFLASH_DERR_SAMPLING and gets id -1, prob 0
  *   ids        device int32 [rows]
  *   prob       optional device float32 [rows]: the drawn token's probability
  */

@@ -180,3 +180,29 @@ def test_the_largest_temperature_and_the_largest_differences(sess, dtype):
     assert torch.equal(probs[0] > 0, high[0]) and bool(((probs[0][high[0]] * 2000 - 1).abs() < TOL).all())
     first = int(high[3].nonzero()[0])
     assert int(ids[0]) == int(high[0].nonzero()[0]) and int(ids[3]) == first and float(probs[3, first]) == 1
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_variates_that_are_none(sess, dtype, many):
+    """Negative and NaN variates draw nothing; a row with no other among its kept tokens has no id."""
+    V, spot = 4099, 77
+    x = torch.linspace(3, 0, V, device="cuda").to(dtype).expand(9, V).contiguous()
+    noise = torch.full((9, V), math.nan, device="cuda")
+    noise[3:6] = -1.0
+    noise[6:, spot] = 2.0
+    times = 40 if many else 1
+    n = 9 * times
+    ps = dict(temperature=torch.tensor([1.0, 1.0, 1e-3] * 3 * times, device="cuda"),
+              top_k=torch.tensor([0, 100, 1000] * 3 * times, dtype=torch.int32, device="cuda"))
+    ids = torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    prob = torch.full((n,), -9.0, device="cuda")
+    sess.sample_tokens(x.repeat(times, 1), noise.repeat(times, 1), ids, prob=prob, **ps)
+    assert sess.error() == 0x80
+    assert ids.tolist() == ([-1] * 6 + [spot] * 3) * times
+    prob = prob.view(times, 9)
+    assert bool((prob[:, :6] == 0).all()) and bool((prob[:, 6:8] > 0).all())
+    noise[:6, 5] = 1.0
+    sess.sample_tokens(x.repeat(times, 1), noise.repeat(times, 1), ids, prob=prob.view(-1), **ps)
+    assert sess.error() == 0
+    assert ids.tolist() == ([5] * 6 + [spot] * 3) * times
