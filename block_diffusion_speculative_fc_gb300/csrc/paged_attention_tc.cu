@@ -92,7 +92,7 @@ struct Request {
 };
 struct Head {
   int items, merge, prefix_splits, prefix_tiles;
-  int first_row, rows, taken, pad;        // rows that meet the prefix; items handed out past one a CTA
+  int first_row, rows, taken, redo;       // rows that meet the prefix; items handed out past one a CTA; rows to do again
 };
 
 struct Params {
@@ -103,6 +103,7 @@ struct Params {
   Item *items;
   Request *req;
   int *row_req;                           // [total_rows]
+  int2 *redo;                             // rows to do again: (token * H + head, request)
   float *part_o, *part_lse;               // [partial rows][D], [partial rows]
   int sms;
   float scale_log2;                       // |scale| log2 e
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     h.first_row = lo;
     h.rows = rows;
     h.merge = total_rows > 0;
-    h.taken = h.pad = 0;
+    h.taken = h.redo = 0;
     *p.head = h;
   }
   s_start[b] = start;
@@ -490,43 +491,25 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ attention
-// A row's part of an item from its visible keys alone, one thread: for rows whose products met a
-// value that is not finite behind their last key (0 times it is not 0 in the matrix product).
-// Writes o * inv to po or out; nothing when the keys from lim to end hold finite values only.
+// The matrix product multiplies the values of keys that a row does not see by 0, which is not 0 for
+// a value that is not finite.  Such keys are in the tiles that hold a row tile's own tokens, where
+// the result gives them away; the warp then looks for them here (the last one from `from` to `end`, -1:
+// none; fewer than 2 * 128 + 128 keys), and rows that it spoils are done again by the join launch.
 template <int D>
-__device__ __noinline__ void redo_row(const Params &p, int req, int g, int page0, int lim, int end, const bf16 *q,
-                                      float m, float inv, float *po, bf16 *out) {
+__device__ __noinline__ int last_not_finite(const Params &p, int req, int g, int page0, int from, int end) {
   const int *list = p.a.rows.page_table + (int64_t)req * p.a.rows.pages_per_req + page0;
-  const int KVH = p.a.KVH;
-  auto at = [&](const void *pages, int key) {
-    const int pg = list[key / kPageRows];
+  constexpr int C = D / 8;                 // 16-byte chunks of a key's values
+  int last = -1;
+  for (int i = (int)(threadIdx.x & 31); i < (end - from) * C; i += 32) {
+    const int key = from + i / C, pg = list[key / kPageRows];
     const int64_t slot = (int64_t)(pg >= 0 && pg < p.a.rows.n_pages ? pg : 0) * kPageRows + key % kPageRows;
-    return (const bf16 *)pages + (slot * KVH + g) * D;
-  };
-  bool finite = true;
-  for (int key = lim; key < end; ++key) {
-    const bf16 *v = at(p.a.v_pages, key);
-    for (int d = 0; d < D; ++d) finite = finite && isfinite(__bfloat162float(v[d]));
+    const uint4 v = *(reinterpret_cast<const uint4 *>((const bf16 *)p.a.v_pages + (slot * p.a.KVH + g) * D) + i % C);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)            // exponents of all ones
+      if ((w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u) last = key;
   }
-  if (finite) return;
-  for (int d0 = 0; d0 < D; d0 += 16) {
-    float o[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-    for (int key = 0; key < lim; ++key) {
-      const bf16 *k = at(p.a.k_pages, key), *v = at(p.a.v_pages, key) + d0;
-      float sc = 0.f;
-      for (int d = 0; d < D; ++d) sc = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), sc);
-      const float w = ex2((p.negative ? -sc : sc) * p.scale_log2 - m);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = fmaf(w, __bfloat162float(v[i]), o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (po) po[d0 + i] = o[i] * inv;
-      else out[d0 + i] = __float2bfloat16_rn(o[i] * inv);
-    }
-  }
+  return __reduce_max_sync(0xffffffffu, last);
 }
 
 template <int D>
@@ -1026,10 +1009,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               }
             }
           }
-          if (odd)
-            redo_row<D>(p, it.req, it.g, it.page0, lim, end,
-                        (const bf16 *)p.a.q + (int64_t)tok * p.a.q_stride + (int64_t)h * D, m, inv,
-                        it.part >= 0 ? po : nullptr, out);
+          if (__any_sync(0xffffffffu, odd)) {
+            const int first = __reduce_min_sync(0xffffffffu, odd ? lim : end);
+            const int last = last_not_finite<D>(p, it.req, it.g, it.page0, first, end);
+            if (odd && lim <= last) {      // (a row has such keys in one split at most)
+              p.redo[atomicAdd(&p.head->redo, 1)] = make_int2(tok * p.a.H + h, it.req);
+              if (it.part >= 0) p.part_lse[at] = INFINITY;   // the join leaves the row alone
+            }
+          }
         }
         tc_fence_before();
         mbar_arrive(&o_read[x]);
@@ -1055,17 +1042,99 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 // A warp a (row, head): out = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max)
 // over the prefix splits and the own splits whose first key the row sees.
 // Eight lanes read one partial row, so that a warp has four in flight.
+//
+// Rows whose products met a value that is not finite behind their last key are attended to again
+// here, a CTA a row, over their visible keys alone.  Nothing waits for it, however long the row
+// (in the attention kernel the other warps' waits would run out): a warp takes 32 keys at a time,
+// a key a lane for the scores, D / 32 dims a lane for the values.
+constexpr int JOIN_THREADS = 256;
+template <int D> __device__ __noinline__ void attend_row(const Params &p, int2 which) {
+  constexpr int W = JOIN_THREADS / 32, V = D / 32;
+  __shared__ float s_q[D], s_m[W], s_l[W], s_o[W][D];
+  const int H = p.a.H, KVH = p.a.KVH, t = which.x / H, h = which.x % H, g = h / (H / KVH);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedRows &r = p.a.rows;
+  const int4 req = __ldcg(reinterpret_cast<const int4 *>(p.req + which.y));
+  const int keys = r.prefix_len + req.z + (t - req.x) + 1;      // (only causal rows have keys behind their last)
+  __syncthreads();                         // the row before has been read
+  for (int d = threadIdx.x; d < D; d += JOIN_THREADS)
+    s_q[d] = to_f32(((const bf16 *)p.a.q)[(int64_t)t * p.a.q_stride + (int64_t)h * D + d]);
+  __syncthreads();
+  const float scale = p.negative ? -p.scale_log2 : p.scale_log2;
+  float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) o[c] = 0.f;
+  for (int k0 = 32 * warp; k0 < keys; k0 += JOIN_THREADS) {
+    const int key = k0 + lane, n = min(32, keys - k0);
+    int64_t slot = 0;
+    float x = -INFINITY;
+    if (lane < n) {
+      const int pg = key < r.prefix_len
+                         ? r.prefix_pages[key / kPageRows]
+                         : r.page_table[(int64_t)which.y * r.pages_per_req + (key - r.prefix_len) / kPageRows];
+      slot = (((int64_t)(pg >= 0 && pg < r.n_pages ? pg : 0) * kPageRows + key % kPageRows) * KVH + g) * D;
+      const uint4 *k = reinterpret_cast<const uint4 *>((const bf16 *)p.a.k_pages + slot);
+      float dot = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 u = k[c];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dot = fmaf(s_q[8 * c + 2 * e], __uint_as_float(w[e] << 16), dot);
+          dot = fmaf(s_q[8 * c + 2 * e + 1], __uint_as_float(w[e] & 0xffff0000u), dot);
+        }
+      }
+      x = dot * scale;
+    }
+    const float mx = fmaxf(m, warp_max(x)), base = mx == -INFINITY ? 0.f : mx;
+    const float w = ex2(x - base), alpha = ex2(m - base);
+    m = mx;
+    l = l * alpha + warp_sum(w);
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] *= alpha;
+    for (int j = 0; j < n; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j) + lane * V;
+#pragma unroll
+      for (int c = 0; c < V; c += 2) {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(v + c);
+        o[c] = fmaf(wj, __uint_as_float(u << 16), o[c]);
+        o[c + 1] = fmaf(wj, __uint_as_float(u & 0xffff0000u), o[c + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < V; ++c) s_o[warp][lane * V + c] = o[c];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += JOIN_THREADS) {
+    float mx = -INFINITY, den = 0.f, num = 0.f;
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    for (int w = 0; w < W; ++w) {
+      if (s_l[w] == 0.f) continue;         // a warp without keys
+      const float f = ex2(s_m[w] - base);
+      den = fmaf(f, s_l[w], den);
+      num = fmaf(f, s_o[w][d], num);
+    }
+    ((bf16 *)p.a.out)[(int64_t)t * p.a.out_stride + (int64_t)h * D + d] = __float2bfloat16_rn(num / den);
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const Head *head = p.head;
   const int4 h0 = __ldcg(reinterpret_cast<const int4 *>(head)), h1 = __ldcg(reinterpret_cast<const int4 *>(head) + 1);
-  if (!h0.y) return;
   constexpr int C = D / 32;                // 16-byte chunks a lane
   const int lane = threadIdx.x & 31, sub = lane & 7, quarter = lane >> 3;
   const int H = p.a.H, KVH = p.a.KVH, G = H / KVH;
   const int nsp = h0.z, first = h1.x, Rp = p.a.rows.prefix_len > 0 ? h1.y * G : 0;
-  const int total = p.a.rows.total_rows * H, step = gridDim.x * (blockDim.x >> 5);
+  const int total = h0.y ? p.a.rows.total_rows * H : 0, step = gridDim.x * (blockDim.x >> 5);
   for (int idx = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); idx < total; idx += step) {
     const int t = idx / H, h = idx % H, g = h / G;
     const int b = __ldcg(p.row_req + t);
@@ -1113,6 +1182,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         }
       }
     }
+    if (mx == INFINITY) continue;          // a part to do again (no other has that weight)
     const float inv = 1.f / warp_sum(den);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -1134,6 +1204,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         *reinterpret_cast<uint2 *>(out + (8 * c + sub) * 4) = *reinterpret_cast<uint2 *>(w2);
       }
   }
+  const int redo = __ldcg(&p.head->redo);
+  for (int i = blockIdx.x; i < redo; i += gridDim.x) attend_row<D>(p, __ldcg(p.redo + i));
 }
 
 // ------------------------------------------------------------------ host
@@ -1178,7 +1250,7 @@ bool encode_rows(CUtensorMap *tm, const void *q, int total_rows, int H, int D, i
 }
 
 struct Layout {
-  size_t head, items, req, row_req, part_o, part_lse, total;
+  size_t head, items, req, row_req, redo, part_o, part_lse, total;
 };
 // Partial rows: at most one per row and segment plus 256 for every item beyond
 // one per (segment, head, row tile).
@@ -1198,6 +1270,7 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);
   L.row_req = take(4 * (size_t)total_rows);
+  L.redo = take(sizeof(int2) * (size_t)rows);
   L.part_lse = take(4 * cap);
   L.part_o = take(4 * cap * D);
   L.total = o;
@@ -1221,6 +1294,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   p.items = (Item *)(ws + L.items);
   p.req = (Request *)(ws + L.req);
   p.row_req = (int *)(ws + L.row_req);
+  p.redo = (int2 *)(ws + L.redo);
   p.part_o = (float *)(ws + L.part_o);
   p.part_lse = (float *)(ws + L.part_lse);
   p.sms = std::max(1, std::min(sms, MAX_SMS));
@@ -1233,7 +1307,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.rows.total_rows * a.H;
   const int grid = (int)std::min<int64_t>((warps + 7) / 8, 16LL * p.sms);
-  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(256), 0, s, p);
+  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(JOIN_THREADS), 0, s, p);
 }
 template <int D> cudaError_t prepare() {
   return cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
