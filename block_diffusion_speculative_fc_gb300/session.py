@@ -95,6 +95,7 @@ class DraftSession:
         self.h = dflash_create(self.c, self.w)
         self.ws_bytes = dflash_workspace_size(self.h)
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device="cuda")
+        self.device = self.ws.device
         base = self.ws.data_ptr()
         self.ws_ptr = (base + 255) // 256 * 256
         dflash_bind_workspace(self.h, self.ws_ptr, self.ws_bytes, _stream())
@@ -176,7 +177,13 @@ class DraftSession:
                                     cand_ids, q_rows, _stream())
 
     # ---- the target's side of a cycle (include/dflash.h)
+    def _on_device(self, device, name):
+        # the calls' other tensors are compared with this one
+        if device != self.device:
+            raise ValueError(f"{name}: on {device}, but the session is on {self.device}")
+
     def _ragged(self, layer, row_start, kv_len):
+        self._on_device(layer.device, "layer")
         batch = kv_len.shape[0]
         if batch > layer.batch:
             raise ValueError(f"kv_len: at most the page table's {layer.batch} requests")
@@ -206,6 +213,7 @@ class DraftSession:
 
     def attention_workspace(self, layer, batch, total_rows):
         """Device workspace for paged_attention calls of at most this size."""
+        self._on_device(layer.device, "layer")
         n = dflash_paged_attention_workspace_size(layer.struct, batch, total_rows)
         return torch.empty(n, dtype=torch.uint8, device=layer.device)
 
@@ -222,6 +230,7 @@ class DraftSession:
                                workspace, workspace.numel(), _stream())
 
     def _sampling(self, logits, temperature, top_k, top_p, min_p):
+        self._on_device(logits.device, "logits")
         if logits.dim() < 2 or logits.stride(-1) != 1:
             raise ValueError("logits: rows of contiguous values are needed")
         flat = logits.flatten(0, -2) if logits.dim() > 2 else logits

@@ -58,6 +58,8 @@ class LayerKV:
         if k_pages.dim() != 4 or k_pages.shape[1] != 64:
             raise ValueError(f"k_pages: shape [n_pages, 64, KVH, D] is needed, not {tuple(k_pages.shape)}")
         self.device, self.dtype = k_pages.device, k_pages.dtype
+        if self.device.type != "cuda":
+            raise ValueError(f"k_pages: a CUDA tensor is needed, not one on {self.device}")
         code = dtype_code(k_pages, "k_pages")
         check(k_pages, "k_pages", self.dtype, self.device)
         check(v_pages, "v_pages", self.dtype, self.device, k_pages.shape)
