@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
   float *Ps = Qs + QR * D;           // [QR][PS]
   __shared__ int s_owner[MAX_TOKENS], s_owners[MAX_TOKENS];
   __shared__ float s_m[QR], s_l[QR];
+  __shared__ unsigned long long s_claimed;   // rows of all ranges
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -54,20 +55,30 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
   const PagedRows &r = p.rows;
   pdl_wait();
   if (tid < MAX_TOKENS) s_owners[tid] = 0;
+  if (tid == 0) s_claimed = 0;
   __syncthreads();
+  unsigned long long claimed = 0;
   for (int i = tid; i < r.B; i += THREADS) {
     const int a = r.row_start[i], e = r.row_start[i + 1];
     if (a < 0 || a > e || e > r.total_rows) {
       if (t0 == 0) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
       continue;
     }
+    claimed += (unsigned long long)(e - a);
     for (int t = max(a, t0); t < min(e, t0 + split.tokens); ++t) {
       s_owner[t - t0] = i;
       atomicAdd(&s_owners[t - t0], 1);
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) claimed += __shfl_xor_sync(0xffffffffu, claimed, o);
+  if (lane == 0 && claimed) atomicAdd(&s_claimed, claimed);
   __syncthreads();
   if (tid < split.tokens && s_owners[tid] > 1) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
+  if (s_claimed > (unsigned long long)r.total_rows) {   // every CTA finds the same, and none writes
+    if (tid == 0) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
+    return;
+  }
 
   for (int first = 0, next; first < split.tokens; first = next) {
     next = first + 1;

@@ -341,12 +341,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     s_hi = 0;
   }
   __syncthreads();
-  int start = 0, n = 0, ctx = 0;
+  int start = 0, n = 0, ctx = 0, claimed = 0;
   if (b < r.B) {
     const int a = r.row_start[b], e = r.row_start[b + 1], kv = r.kv_len[b];
     if (a < 0 || a > e || e > r.total_rows) {
       raise_error(p.a.err, DFLASH_DERR_ROW_RANGE);
     } else if (e > a) {
+      claimed = e - a;
       if (kv < prefix || (int64_t)kv + (e - a) - prefix > (int64_t)r.pages_per_req * kPageRows) {
         raise_error(p.a.err, DFLASH_DERR_KV_CAPACITY);
       } else {
@@ -360,8 +361,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   }
   __syncthreads();
   // more rows than there are: ranges overlap (a decreasing pair among them is flagged already), and
-  // the workspace has no room for them
-  const bool fits = block_sum(n, s_sum) <= r.total_rows;
+  // the workspace has no room for them; rows of requests that are skipped count too
+  const bool fits = block_sum(claimed, s_sum) <= r.total_rows;
   if (!fits) {
     n = 0;
     if (b == 0) raise_error(p.a.err, DFLASH_DERR_ROW_RANGE);
