@@ -379,7 +379,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   U = U < 2 ? 2 : U;
   // Items beyond one per (segment, KV head, pair of row tiles) are fewer than 4/3 W / U <= 4/3 SMs <=
   // EXTRA (a pair costs two units of its U in split_keys; segments of c row tiles have (c + 1) / 2
-  // pairs and count c in W), each with at most 256 partial rows: the workspace has room for them.
+  // pairs and count c in W), each with the rows of at most 2 tpt tokens and of no more than there
+  // are: the workspace has room for them.
   const Split sp = split_keys(nkt, n, tpt, U), spp = split_keys(nktp, rows, tpt, U);
   const bool joined = n > 0 && (prefix > 0 || sp.splits > 1);
   const int nrt = ceil_div(n, 2 * tpt), nrtp = Rp > 0 ? ceil_div(rows, 2 * tpt) : 0;
@@ -1253,8 +1254,8 @@ bool encode_rows(CUtensorMap *tm, const void *q, int total_rows, int H, int D, i
 struct Layout {
   size_t head, items, req, row_req, redo, part_o, part_lse, total;
 };
-// Partial rows: at most one per row and segment plus 256 for every item beyond
-// one per (segment, head, row tile).
+// Partial rows: at most one per row and segment plus those of every item beyond
+// one per (segment, head, row tile pair), which has no more tokens than the call.
 Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   Layout L;
   size_t o = 0;
@@ -1266,7 +1267,8 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   const int tpt = 128 / (H / KVH);
   const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows / (2 * tpt) + 1;
   const int64_t max_items = KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA;
-  const int64_t cap = rows * (prefix > 0 ? 2 : 1) + (int64_t)EXTRA * 256;
+  const int64_t cap = rows * (prefix > 0 ? 2 : 1) +
+                      (int64_t)EXTRA * std::min(2 * tpt, total_rows) * (H / KVH);
   L.head = take(sizeof(Head));
   L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);

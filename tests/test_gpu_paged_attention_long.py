@@ -63,3 +63,20 @@ def test_hidden_values_behind_long_contexts(sess, dim, prefix):
             assert torch.equal(~torch.isfinite(got), seen.expand(heads, dim)), (b, i)
             over = ((got - want).abs() - tol)[:, ~seen]
             assert float(over.max()) <= 0, (b, i, float(over.max()))
+
+
+@pytest.mark.parametrize("lens,ctx,heads,kvh,dim,prefix", [
+    ([1], [20000], 32, 8, 128, 0), ([1], [20000], 128, 1, 128, 1024), ([2], [9000], 5, 1, 64, 0),
+    ([1] * 64, [70 * i for i in range(64)], 64, 8, 128, 16384), ([16] * 30, [100 * i for i in range(30)], 32, 8, 128, 0),
+    ([700, 257, 64], [0, 1000, 31], 21, 3, 64, 640), ([33, 1, 0, 47], [5000, 6000, 0, 130], 2, 2, 64, 128)])
+def test_nothing_is_written_behind_the_workspace(sess, lens, ctx, heads, kvh, dim, prefix):
+    from tests.target_reference import Paged
+    pb = Paged(lens, ctx, prefix=prefix, kvh=kvh, dim=dim, seed=3)
+    lay, q = pb.layer(heads), pb.normal(pb.rows, heads, dim)
+    n = sess.attention_workspace(lay, len(lens), pb.rows).numel()
+    ws = torch.full((n + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.full((pb.rows, heads, dim), FILL, dtype=BF, device="cuda")
+    sess.paged_attention(lay, q, pb.row_start, pb.kv_len, out, ws[:n])
+    assert sess.error() == 0
+    assert bool((ws[n:] == 0x5a).all())
+    assert bool(torch.isfinite(out).all())
