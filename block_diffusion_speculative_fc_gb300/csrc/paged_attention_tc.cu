@@ -95,6 +95,12 @@ struct Head {
   int first_row, rows, taken, redo;       // rows that meet the prefix; items handed out past one a CTA; rows to do again
 };
 
+// A row of an item to do again.
+struct Redo {
+  int at, req, page0, lim;                // token * H + head, request, first page, keys that the row sees
+  int part, next, pad0, pad1;             // partial row (-1: final), next of the CTA's list (-1: none)
+};
+
 struct Params {
   CUtensorMap tmK, tmV;                   // dims {D, KVH, n_pages * 64}, box {64, 1, 64}
   CUtensorMap tmQ;                        // dims {D, H, total_rows}, box {64, G, 128 / G}
@@ -103,7 +109,7 @@ struct Params {
   Item *items;
   Request *req;
   int *row_req;                           // [total_rows]
-  int2 *redo;                             // rows to do again: (token * H + head, request)
+  Redo *redo;                             // [total_rows * H]
   float *part_o, *part_lse;               // [partial rows][D], [partial rows]
   int sms;
   float scale_log2;                       // |scale| log2 e
@@ -495,10 +501,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 // ------------------------------------------------------------------ attention
 // The matrix product multiplies the values of keys that a row does not see by 0, which is not 0 for
 // a value that is not finite.  Such keys are in the tiles that hold a row tile's own tokens, where
-// the result gives them away; the warp then looks for them here (the last one from `from` to `end`, -1:
-// none; fewer than 2 * 128 + 128 keys), and rows that it spoils are done again by the join launch.
+// the result gives them away (`odd`); the warp then looks for the last of them here (fewer than 2 * 128 +
+// 128 keys lie between `lim`, the keys that a row sees, and `end`) and lists the rows before it, which
+// the CTA does again once it has no more items: nothing waits for it then, however many keys they see.
 template <int D>
-__device__ __noinline__ int last_not_finite(const Params &p, int req, int g, int page0, int from, int end) {
+__device__ __noinline__ void list_spoiled(const Params &p, int *s_redo, int req, int g, int page0, int at, int part,
+                                          int lim, int end, bool odd) {
+  const int from = __reduce_min_sync(0xffffffffu, odd ? lim : end);
   const int *list = p.a.rows.page_table + (int64_t)req * p.a.rows.pages_per_req + page0;
   constexpr int C = D / 8;                 // 16-byte chunks of a key's values
   int last = -1;
@@ -511,7 +520,98 @@ __device__ __noinline__ int last_not_finite(const Params &p, int req, int g, int
     for (int e = 0; e < 4; ++e)            // exponents of all ones
       if ((w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u) last = key;
   }
-  return __reduce_max_sync(0xffffffffu, last);
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (odd && lim <= last) {                // (a row has such keys in one split at most)
+    const int i = atomicAdd(&p.head->redo, 1);
+    Redo e;
+    e.at = at, e.req = req, e.page0 = page0, e.lim = lim;
+    e.part = part, e.next = atomicExch(s_redo, i), e.pad0 = e.pad1 = 0;
+    p.redo[i] = e;
+  }
+}
+
+// The rows of the CTA's list over their visible keys alone, by its first 256 threads.  A warp takes 32
+// keys at a time, a key a lane for the scores, D / 32 dims a lane for the values; the row's weight (lse)
+// stands already, as no score of a hidden key enters it.
+template <int D> __device__ __noinline__ void redo_rows(const Params &p, int first, float *sm) {
+  constexpr int W = 8, V = D / 32;
+  float *s_q = sm, *s_m = s_q + D, *s_l = s_m + W, *s_o = s_l + W;      // [D], [W], [W], [W][D]
+  const int H = p.a.H, KVH = p.a.KVH, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedRows &r = p.a.rows;
+  const float scale = p.negative ? -p.scale_log2 : p.scale_log2;
+  auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+  for (int next; first >= 0; first = next) {
+    const Redo e = p.redo[first];
+    next = e.next;
+    const int t = e.at / H, h = e.at % H, g = h / (H / KVH);
+    const int *list = r.page_table + (int64_t)e.req * r.pages_per_req + e.page0;
+    sync();                                // the row before has been read
+    for (int d = threadIdx.x; d < D; d += 256)
+      s_q[d] = to_f32(((const bf16 *)p.a.q)[(int64_t)t * p.a.q_stride + (int64_t)h * D + d]);
+    sync();
+    float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) o[c] = 0.f;
+    for (int k0 = 32 * warp; k0 < e.lim; k0 += 32 * W) {
+      const int key = k0 + lane, n = min(32, e.lim - k0);
+      int64_t slot = 0;
+      float x = -INFINITY;
+      if (lane < n) {
+        const int pg = list[key / kPageRows];
+        slot = (((int64_t)(pg >= 0 && pg < r.n_pages ? pg : 0) * kPageRows + key % kPageRows) * KVH + g) * D;
+        const uint4 *k = reinterpret_cast<const uint4 *>((const bf16 *)p.a.k_pages + slot);
+        float dot = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u = k[c];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dot = fmaf(s_q[8 * c + 2 * i], __uint_as_float(w[i] << 16), dot);
+            dot = fmaf(s_q[8 * c + 2 * i + 1], __uint_as_float(w[i] & 0xffff0000u), dot);
+          }
+        }
+        x = dot * scale;
+      }
+      const float mx = fmaxf(m, warp_max(x)), base = mx == -INFINITY ? 0.f : mx;
+      const float w = ex2(x - base), alpha = ex2(m - base);
+      m = mx;
+      l = l * alpha + warp_sum(w);
+#pragma unroll
+      for (int c = 0; c < V; ++c) o[c] *= alpha;
+      for (int j = 0; j < n; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j) + lane * V;
+#pragma unroll
+        for (int c = 0; c < V; c += 2) {
+          const uint32_t u = *reinterpret_cast<const uint32_t *>(v + c);
+          o[c] = fmaf(wj, __uint_as_float(u << 16), o[c]);
+          o[c + 1] = fmaf(wj, __uint_as_float(u & 0xffff0000u), o[c + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) s_o[warp * D + lane * V + c] = o[c];
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    sync();
+    for (int d = threadIdx.x; d < D; d += 256) {
+      float mx = -INFINITY, den = 0.f, num = 0.f;
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      for (int w = 0; w < W; ++w) {
+        if (s_l[w] == 0.f) continue;       // a warp without keys
+        const float f = ex2(s_m[w] - base);
+        den = fmaf(f, s_l[w], den);
+        num = fmaf(f, s_o[w * D + d], num);
+      }
+      const float x = num / den;
+      if (e.part >= 0) p.part_o[(int64_t)e.part * D + d] = x;
+      else ((bf16 *)p.a.out)[(int64_t)t * p.a.out_stride + (int64_t)h * D + d] = __float2bfloat16_rn(x);
+    }
+  }
 }
 
 template <int D>
@@ -529,10 +629,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   uint64_t *done = ml_free + 1;
   int *s_items = (int *)(((uintptr_t)(done + 1) + 15) & ~(uintptr_t)15);   // [NQ][12]
   uint32_t *s_tmem = (uint32_t *)(s_items + NQ * 12);
+  int *s_redo = s_items + NQ * 12 + 1;   // last of the CTA's rows to do again (-1: none)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.a.H / p.a.KVH, tpt = 128 / G, rt_rows = tpt * G;   // tokens and rows of a row tile
 
   if (threadIdx.x == 0) {
+    *s_redo = -1;
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 2);            // released by both streams, or twice by the one that used it
@@ -1011,14 +1113,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               }
             }
           }
-          if (__any_sync(0xffffffffu, odd)) {
-            const int first = __reduce_min_sync(0xffffffffu, odd ? lim : end);
-            const int last = last_not_finite<D>(p, it.req, it.g, it.page0, first, end);
-            if (odd && lim <= last) {      // (a row has such keys in one split at most)
-              p.redo[atomicAdd(&p.head->redo, 1)] = make_int2(tok * p.a.H + h, it.req);
-              if (it.part >= 0) p.part_lse[at] = INFINITY;   // the join leaves the row alone
-            }
-          }
+          if (__builtin_expect(__any_sync(0xffffffffu, odd), 0))
+            list_spoiled<D>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
         }
         tc_fence_before();
         mbar_arrive(&o_read[x]);
@@ -1033,6 +1129,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   }
   tc_fence_before();
   __syncthreads();
+  // (every copy has landed and every product ended: the ring is free)
+  if (__builtin_expect(*s_redo >= 0, 0)) {
+    if (threadIdx.x < 256) redo_rows<D>(p, *s_redo, reinterpret_cast<float *>(ring));
+    __syncthreads();
+  }
   pdl_trigger();   // every global write of this CTA is done
   if (warp == 9) {
     tc_fence_after();
@@ -1044,99 +1145,17 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 // A warp a (row, head): out = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max)
 // over the prefix splits and the own splits whose first key the row sees.
 // Eight lanes read one partial row, so that a warp has four in flight.
-//
-// Rows whose products met a value that is not finite behind their last key are attended to again
-// here, a CTA a row, over their visible keys alone.  Nothing waits for it, however long the row
-// (in the attention kernel the other warps' waits would run out): a warp takes 32 keys at a time,
-// a key a lane for the scores, D / 32 dims a lane for the values.
-constexpr int JOIN_THREADS = 256;
-template <int D> __device__ __noinline__ void attend_row(const Params &p, int2 which) {
-  constexpr int W = JOIN_THREADS / 32, V = D / 32;
-  __shared__ float s_q[D], s_m[W], s_l[W], s_o[W][D];
-  const int H = p.a.H, KVH = p.a.KVH, t = which.x / H, h = which.x % H, g = h / (H / KVH);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PagedRows &r = p.a.rows;
-  const int4 req = __ldcg(reinterpret_cast<const int4 *>(p.req + which.y));
-  const int keys = r.prefix_len + req.z + (t - req.x) + 1;      // (only causal rows have keys behind their last)
-  __syncthreads();                         // the row before has been read
-  for (int d = threadIdx.x; d < D; d += JOIN_THREADS)
-    s_q[d] = to_f32(((const bf16 *)p.a.q)[(int64_t)t * p.a.q_stride + (int64_t)h * D + d]);
-  __syncthreads();
-  const float scale = p.negative ? -p.scale_log2 : p.scale_log2;
-  float m = -INFINITY, l = 0.f, o[V];
-#pragma unroll
-  for (int c = 0; c < V; ++c) o[c] = 0.f;
-  for (int k0 = 32 * warp; k0 < keys; k0 += JOIN_THREADS) {
-    const int key = k0 + lane, n = min(32, keys - k0);
-    int64_t slot = 0;
-    float x = -INFINITY;
-    if (lane < n) {
-      const int pg = key < r.prefix_len
-                         ? r.prefix_pages[key / kPageRows]
-                         : r.page_table[(int64_t)which.y * r.pages_per_req + (key - r.prefix_len) / kPageRows];
-      slot = (((int64_t)(pg >= 0 && pg < r.n_pages ? pg : 0) * kPageRows + key % kPageRows) * KVH + g) * D;
-      const uint4 *k = reinterpret_cast<const uint4 *>((const bf16 *)p.a.k_pages + slot);
-      float dot = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 u = k[c];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dot = fmaf(s_q[8 * c + 2 * e], __uint_as_float(w[e] << 16), dot);
-          dot = fmaf(s_q[8 * c + 2 * e + 1], __uint_as_float(w[e] & 0xffff0000u), dot);
-        }
-      }
-      x = dot * scale;
-    }
-    const float mx = fmaxf(m, warp_max(x)), base = mx == -INFINITY ? 0.f : mx;
-    const float w = ex2(x - base), alpha = ex2(m - base);
-    m = mx;
-    l = l * alpha + warp_sum(w);
-#pragma unroll
-    for (int c = 0; c < V; ++c) o[c] *= alpha;
-    for (int j = 0; j < n; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j) + lane * V;
-#pragma unroll
-      for (int c = 0; c < V; c += 2) {
-        const uint32_t u = *reinterpret_cast<const uint32_t *>(v + c);
-        o[c] = fmaf(wj, __uint_as_float(u << 16), o[c]);
-        o[c + 1] = fmaf(wj, __uint_as_float(u & 0xffff0000u), o[c + 1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < V; ++c) s_o[warp][lane * V + c] = o[c];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  for (int d = threadIdx.x; d < D; d += JOIN_THREADS) {
-    float mx = -INFINITY, den = 0.f, num = 0.f;
-    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    for (int w = 0; w < W; ++w) {
-      if (s_l[w] == 0.f) continue;         // a warp without keys
-      const float f = ex2(s_m[w] - base);
-      den = fmaf(f, s_l[w], den);
-      num = fmaf(f, s_o[w][d], num);
-    }
-    ((bf16 *)p.a.out)[(int64_t)t * p.a.out_stride + (int64_t)h * D + d] = __float2bfloat16_rn(num / den);
-  }
-}
-
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const Head *head = p.head;
   const int4 h0 = __ldcg(reinterpret_cast<const int4 *>(head)), h1 = __ldcg(reinterpret_cast<const int4 *>(head) + 1);
+  if (!h0.y) return;
   constexpr int C = D / 32;                // 16-byte chunks a lane
   const int lane = threadIdx.x & 31, sub = lane & 7, quarter = lane >> 3;
   const int H = p.a.H, KVH = p.a.KVH, G = H / KVH;
   const int nsp = h0.z, first = h1.x, Rp = p.a.rows.prefix_len > 0 ? h1.y * G : 0;
-  const int total = h0.y ? p.a.rows.total_rows * H : 0, step = gridDim.x * (blockDim.x >> 5);
+  const int total = p.a.rows.total_rows * H, step = gridDim.x * (blockDim.x >> 5);
   for (int idx = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); idx < total; idx += step) {
     const int t = idx / H, h = idx % H, g = h / G;
     const int b = __ldcg(p.row_req + t);
@@ -1184,7 +1203,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
         }
       }
     }
-    if (mx == INFINITY) continue;          // a part to do again (no other has that weight)
     const float inv = 1.f / warp_sum(den);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -1206,8 +1224,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
         *reinterpret_cast<uint2 *>(out + (8 * c + sub) * 4) = *reinterpret_cast<uint2 *>(w2);
       }
   }
-  const int redo = __ldcg(&p.head->redo);
-  for (int i = blockIdx.x; i < redo; i += gridDim.x) attend_row<D>(p, __ldcg(p.redo + i));
 }
 
 // ------------------------------------------------------------------ host
@@ -1273,7 +1289,7 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);
   L.row_req = take(4 * (size_t)total_rows);
-  L.redo = take(sizeof(int2) * (size_t)rows);
+  L.redo = take(sizeof(Redo) * (size_t)rows);
   L.part_lse = take(4 * cap);
   L.part_o = take(4 * cap * D);
   L.total = o;
@@ -1297,7 +1313,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   p.items = (Item *)(ws + L.items);
   p.req = (Request *)(ws + L.req);
   p.row_req = (int *)(ws + L.row_req);
-  p.redo = (int2 *)(ws + L.redo);
+  p.redo = (Redo *)(ws + L.redo);
   p.part_o = (float *)(ws + L.part_o);
   p.part_lse = (float *)(ws + L.part_lse);
   p.sms = std::max(1, std::min(sms, MAX_SMS));
@@ -1310,7 +1326,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.rows.total_rows * a.H;
   const int grid = (int)std::min<int64_t>((warps + 7) / 8, 16LL * p.sms);
-  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(JOIN_THREADS), 0, s, p);
+  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(256), 0, s, p);
 }
 template <int D> cudaError_t prepare() {
   return cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
