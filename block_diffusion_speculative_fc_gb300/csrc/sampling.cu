@@ -64,10 +64,19 @@ constexpr int NB = 1024;         // histogram bins: a = 0 .. 31.95 and one for t
 constexpr float TAIL = 31.95f;   // a of the last bin's first token (inside the bin before it)
 constexpr int PB = NB / NT;      // bins of a thread in a scan
 constexpr int CAP = 1024;        // gathered tokens (two a thread)
-constexpr int MAX_K = 512;       // top-k of the short way
-constexpr int TOP_P_LIST = 128;  // tokens that its list holds at least for top-p alone
+// Top-k of the short way at most.  k = 512 by the list and by the histogram: 16 rows of 151936 50 us and
+// 65, 128 fp32 rows of 50257 69 and 112; k = 700 73 and 67, 103 and 114.  (512 rows of 151936, a CTA each:
+// k = 400 185 and 788; at 500 the list overflows, 846 and 787.)
+constexpr int MAX_K = 512;
+// Tokens that its list holds at least for top-p alone: 64, 128, 256 take 33, 34, 41 us for 96 fp32 rows
+// of 50257, 649, 656, 666 for 2048 rows of 151936, 31.8, 30.9, 32.0 for 16.
+constexpr int TOP_P_LIST = 128;
 constexpr int MAXC = 8;          // CTAs of a cluster
 constexpr int GROUPS = NT / 4;
+// A bound of up to this place comes from the maxima of groups of threads, a later one from a search
+// over the threads' own.  512 rows of 151936: k = 100 and 120 by the search 118 and 120 us, by groups
+// 122 and 134 (a lower bound, a longer list), k = 128 120 and 393 (it overflows).
+constexpr int GROUP_PLACES = GROUPS * 3 / 4;
 constexpr int STREAM_VOCAB = 1 << 18;   // tokens of a CTA at most (sums of the histogram)
 constexpr int MAX_SMEM = 220 * 1024;
 // Up to here two logits whose difference passes the largest float differ by a weight of 0; above it
@@ -114,9 +123,8 @@ struct Fixed {
 
 enum { CMD_GATHER = 0, CMD_SPLIT = 1, CMD_DONE = 2 };
 
-// -0 and +0 have one image (-0 + 0 = +0): equal logits go by id.
 __device__ __forceinline__ uint32_t order_image(float x) {
-  const uint32_t u = __float_as_uint(__fadd_rn(x, 0.f));
+  const uint32_t u = __float_as_uint(x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float order_value(uint32_t k) {
@@ -125,6 +133,9 @@ __device__ __forceinline__ float order_value(uint32_t k) {
 __device__ __forceinline__ unsigned long long key_of(float x, int idx) {
   return ((unsigned long long)order_image(x) << 32) | (uint32_t)~(uint32_t)idx;
 }
+// The image of -0 is one below that of +0, but equal logits go by id: one image for both.  (Applied where
+// keys are few, not in order_image: there its registers take 128 unfiltered draws from 48 to 50 us.)
+__device__ __forceinline__ uint32_t one_zero(uint32_t image) { return image + (image == 0x7fffffffu); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -460,8 +471,7 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
       w += mm[i];
     }
   };
-  // the bin that holds the cut, given what lies above every bin; there is one unless bins and key
-  // ranges disagree, which is flagged
+  // the bin that holds the cut, given what lies above every bin
   auto select = [&](const int *nn, const int *ab, const u64 *abm, int base, u64 base_m) {
     if (tid == 0) f.sel_bin = -1;
     __syncthreads();
@@ -471,7 +481,6 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
     if (mine >= 0) atomicMax(&f.sel_bin, mine);
     __syncthreads();
     const int s = max(f.sel_bin, 0);
-    if (tid == 0 && f.sel_bin < 0) raise_error(err, DFLASH_DERR_TIMEOUT);
     if (s / PB == tid) {
       const int i = s % PB;
       f.sel_n = nn[i];
@@ -501,22 +510,22 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
     if (tid == 0) f.n_list = 0;
     tell(count <= CAP ? CMD_GATHER : CMD_SPLIT, sh);
   };
-  // start of a stage: the first histogram's bin, and its range of keys, somewhat wider than it (the
-  // last bin begins at TAIL, not half a bin before its number)
+  // start of a stage: the first histogram's bin, and its range of keys, wider than it: a bin begins half
+  // a bin before its number, the last one at TAIL, which is 0.6 before
   auto begin = [&] {
     bin = select(n0, above0, above_m0, 0, 0);
     float x_hi = FLT_MAX, x_lo = -FLT_MAX;
     if (tid < C) {
       const double inv = (double)temp * 0.6931471805599453 / 32.0;
-      const double first = bin < NB - 1 ? bin - 0.51 : 32.0 * TAIL - 0.01;
-      x_hi = __double2float_ru(fmax((double)m - fmax(0.0, first * inv), -(double)FLT_MAX));
+      static_assert(32.0 * TAIL > NB - 1 - 0.61, "the last bin's tokens are in its range");
+      x_hi = __double2float_ru(fmax((double)m - fmax(0.0, (bin - 0.62) * inv), -(double)FLT_MAX));
       if (bin < NB - 1) x_lo = __double2float_rd(fmax((double)m - (bin + 0.51) * inv, -(double)FLT_MAX));
     }
     x_hi = __shfl_sync(0xffffffffu, x_hi, 0);
     x_lo = __shfl_sync(0xffffffffu, x_lo, 0);
     if (tid == 0) {
       f.range_lo = (u64)order_image(x_lo) << 32;
-      f.range_hi = ((u64)order_image(x_hi) + 1) << 32;
+      f.range_hi = ((u64)one_zero(order_image(x_hi)) + 1) << 32;
     }
     __syncthreads();
     lo = f.range_lo;
@@ -554,7 +563,8 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
         hi = h < hi ? h : hi;
         __syncthreads();   // sh has been read
         tell_range(f.sel_n);
-      } else if (f.n_list > CAP) {
+      } else if (f.n_list > CAP || f.n_list == 0) {
+        // (no token at all: bins and key ranges would disagree; the rounds run out, which is flagged)
         const int over = f.n_list;
         __syncthreads();
         tell_range(over);
@@ -605,7 +615,7 @@ __device__ __noinline__ u64 general_cut(Fixed &f, const Tables &tab, const Weigh
     const float x_lo = order_value((uint32_t)(r_lo >> 32)), x_hi = order_value((uint32_t)((r_hi - 1) >> 32));
     tokens.each([&](float x, int id) {
       if (x < x_lo || x > x_hi || is_far(x)) return;
-      const u64 k = key_of(x, id);
+      const u64 k = ((u64)one_zero(order_image(x)) << 32) | (uint32_t)~(uint32_t)id;
       if (k < r_lo || k >= r_hi) return;
       int b;
       uint32_t u;
@@ -734,7 +744,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   const bool brief = (filtered && top_k <= MAX_K) || by_min_p;
   const int j = brief && !by_min_p ? ((top_k > 0 ? top_k : TOP_P_LIST) + C - 1) / C : 0;
   float low = -INFINITY;
-  if (j > GROUPS * 3 / 4) {
+  if (j > GROUP_PLACES) {
     const uint32_t own = order_image(mx);
     uint32_t found = 0;
 #pragma unroll 1
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     f.own_n = 0;
   }
   __syncthreads();
-  if (j > 1 && j <= GROUPS * 3 / 4) {
+  if (j > 1 && j <= GROUP_PLACES) {
     // the j-th largest is the smallest with fewer than j larger ones
     if (tid < GROUPS) {
       const float own = f.group[tid];
@@ -887,7 +897,8 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     }
     __syncthreads();
     for (int i = tid; i < own_n; i += NT)
-      if (f.own_at + i < CAP) lead.list[f.own_at + i] = f.sorted[i];
+      if (f.own_at + i < CAP)
+        lead.list[f.own_at + i] = ((u64)one_zero((uint32_t)(f.sorted[i] >> 32)) << 32) | (uint32_t)f.sorted[i];
     if (tid < C) {
       Fixed &o = *cl.map_shared_rank(&f, tid);
       u64 r = 0, l = 0;
@@ -964,8 +975,8 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
           sum_f += e[i];
           ids[i] = keep[i] ? (int)~(uint32_t)f.sorted[at] : 0;
           if (DRAW && keep[i]) {
-            const float variate = noise[ids[i]], score = e[i] / variate;
-            const u64 k = variate >= 0.f && score >= 0.f ? argmax_key(score, ids[i]) : 0;
+            const float score = e[i] / noise[ids[i]];
+            const u64 k = score > 0.f ? argmax_key(score, ids[i]) : 0;
             best = k > best ? k : best;
           }
         }
@@ -1041,7 +1052,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
   } else {
     // the exact quotient only where an approximate one (2^-21) reaches the best so far; a thread's
     // ids ascend, so the first of equal scores has the lowest
-    float top = -1.f;
+    float top = 0.f;
     int top_id = 0;
     float e[2][E];                       // the noise of two vectors is in flight
     bool any[2];
@@ -1071,14 +1082,14 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
         else s0 += w;
         if (k && __fdividef(w, e[u][i]) * 1.000001f >= top) {
           const float score = __fdiv_rn(w, e[u][i]);
-          if (score > top && e[u][i] >= 0.f) {
+          if (score > top) {
             top = score;
             top_id = id + i;
           }
         }
       }
     });
-    if (top >= 0.f) best = argmax_key(top, top_id);
+    if (top > 0.f) best = argmax_key(top, top_id);
   }
   const float sum = warp_sum(s0 + s1);
   if (DRAW) best = warp_max_key(best);
@@ -1105,7 +1116,7 @@ __global__ void __launch_bounds__(NT, 2) sampling_kernel(const __grid_constant__
     if (rank == 0 && tid == 0) {
       best = 0;
       for (int r = 0; r < C; ++r) best = f.x_race[r] > best ? f.x_race[r] : best;
-      // no score: every kept token's variate is negative or NaN
+      // no score above 0: every kept token's variate is negative, infinite or NaN
       const int id = best ? argmax_key_index(best) : -1;
       p.ids[row] = id;
       if (id < 0) raise_error(p.err, DFLASH_DERR_SAMPLING);
@@ -1198,6 +1209,8 @@ template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaS
   if (p.rows >= 2 * sms && p.vocab <= STREAM_VOCAB) return launch<T, DRAW, false>(p, 1, s);
   // The fewest CTAs whose slices leave room for two of them on an SM (128 rows of 151936: 40 us with
   // clusters of 4, 53 with 8); more while rows are too few to fill the GPU and a slice stays worth a CTA
+  // (down to half of 4096: unfiltered rows of 4000 to 16000 0.1 to 0.4 us less, 16 filtered ones of
+  // 16000 9.5 us against 8.2; no smaller than 16384: 0.3 to 1.5 us more for 1 to 8 rows)
   int C = 1;
   while (C < MAXC && smem_bytes(slice_of(p.vocab, C), es) > 108 * 1024) C *= 2;
   while (C < MAXC && (int64_t)p.rows * C * 2 <= sms && slice_of(p.vocab, C) > 4096) C *= 2;

@@ -480,8 +480,10 @@ int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hid
  * counts the prefix and must be at least prefix_len wherever request b has
  * rows (else DFLASH_DERR_KV_CAPACITY and the request is skipped, as for rows
  * past the page table).
- * n_heads a multiple of n_kv_heads, at most 128 query heads per KV head;
- * head_dim 64 or 128.
+ * n_heads a multiple of n_kv_heads, at most 128 query heads per KV head and
+ * 1024 in all; head_dim 64 or 128.  The calls take batch <= 1024, total_rows *
+ * n_heads <= 2^28, positions below 2^31 (prefix_len < 2^30, pages_per_req <
+ * 2^24).
  */
 typedef struct {
   dflash_dtype dtype;
@@ -572,9 +574,16 @@ int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
  *             call, nothing is kept in it between calls.  Calls that may
  *             overlap on the GPU (two streams, two captured graphs) need one
  *             each.
- * batch <= 1024.  A page id outside the pool sets DFLASH_DERR_PAGE_RANGE and
- * page 0 is read in its place.  Cache rows past a request's last are never
- * used, whatever they hold.
+ * A page id outside the pool sets DFLASH_DERR_PAGE_RANGE and page 0 is read in
+ * its place.  Cache rows past a request's last are never used, and a key that a
+ * row does not see has no part in its result, whatever they hold (NaN and
+ * infinities too).
+ * Arithmetic: scores, maxima, sums and the join in float32, results rounded
+ * once.  With a bf16 cache the weights exp(score - max) are rounded to bf16 for
+ * the product with V (the tensor cores' operand), the sum that divides them is
+ * of the unrounded ones: beside its own rounding an output is off by at most
+ * 2^-8 sum_p softmax_p |V[p]|.  An fp32 cache keeps float32 throughout.
+ * Weighted sums are formed before the division: |V| up to 2^88.
  */
 int dflash_paged_attention_workspace_size(const dflash_layer_kv *kv, int32_t batch,
                                           int32_t total_rows, size_t *bytes);
@@ -615,7 +624,10 @@ typedef struct {
  * a row stride in elements; any alignment of the type.  probs must not
  * overlap logits.  The border of top-p is decided on sums of about 1e-9
  * relative error (2^-20 for the weight of the tail that lies far beyond it),
- * that of min-p in 64 bits; the same in every run.
+ * that of min-p in 64 bits; the same in every run.  A probability comes from
+ * float32 arithmetic and the hardware's exponential: relative error about (3
+ * (max x - x_v) log2(e) / T + 16) 2^-24 and the roundings of the sum (some tens
+ * of 2^-24).
  * vocab <= 524288 (bf16) or 262144 (fp32).
  */
 int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
@@ -625,11 +637,14 @@ int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const voi
 /*
  * Tokens drawn from that distribution without storing it: ids[r] = argmax over
  * the kept v of w_v / exp_noise[r][v] (the exponential race of
- * dflash_accept_commit_sampled: an exact draw, lowest id on ties, float32
- * IEEE division), read only where v is kept.
+ * dflash_accept_commit_sampled, lowest id on ties).  Quotients are rounded as
+ * IEEE float32; the weights have the error of the probabilities above, so the
+ * draw is of that distribution to about 2^-20.  Variates of tokens that are not
+ * kept have no part in it (they may be read).
  *   exp_noise  device float32 [rows, vocab] Exp(1) variates (> 0).  Tokens whose
- *              variate is negative or NaN are not drawn; where no kept token is
- *              left the row sets DFLASH_DERR_SAMPLING and gets id -1, prob 0
+ *              variate is negative, infinite or NaN are not drawn; where no kept
+ *              token is left the row sets DFLASH_DERR_SAMPLING and gets id -1,
+ *              prob 0
  *   ids        device int32 [rows]
  *   prob       optional device float32 [rows]: the drawn token's probability
  */
