@@ -10,9 +10,9 @@
 // cluster of them splits the keys and joins its (max, sum, weighted sum)
 // through distributed shared memory in rank order.
 //
-// Measured: 8 requests x 16 rows of 32 heads over 2064 keys of 8 heads 235 us
-// (18 TFLOP/s); one
-// token over 1001 keys 17 us; 64 tokens over 2001 keys each 351 us.
+// Measured (inputs beyond L2): 8 requests x 16 rows of 32 heads over 2064 keys
+// of 8 heads 237 us (18 TFLOP/s); one token over 1001 keys 24 us; 64 tokens over
+// 2001 keys each 350 us.
 //
 // Tokens of one CTA that belong to different requests are taken in turn, so a
 // CTA has no more tokens than requests have on average.
@@ -250,9 +250,9 @@ template <int D, int RPW>
 cudaError_t launch(const PagedAttnParams &p, const Split &split, int sms, cudaStream_t s) {
   const int64_t tiles = (p.rows.total_rows + split.tokens - 1) / split.tokens;
   const int64_t ctas = tiles * p.KVH * split.blocks;
-  // Keys split while the CTAs are fewer than two an SM: one token over 1001 keys 17 us against 90
-  // unsplit, 8 x 16 rows over 2064 keys 234 against 502.  (Up to four an SM: 32 x 16 rows 1212 us
-  // against 1392, but 64 single tokens 378 against 348.)
+  // Keys split while the CTAs are fewer than two an SM: one token over 1001 keys 24 us against 134
+  // unsplit, 8 x 16 rows over 2064 keys 237 against 508.  (Up to four an SM: 32 x 16 rows 1212 us
+  // against 1377, but 64 single tokens 380 against 351.)
   int C = 1;
   while (C < MAXC && ctas * C < 2 * sms) C *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -279,8 +279,8 @@ template <int D> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
   Split split;
   split.heads = std::min(G, MAX_ROWS);
   split.blocks = (G + split.heads - 1) / split.heads;
-  // (a token a CTA stages every key once a token: 8 x 16 rows 619 us against 234, 2000 rows of one
-  // prompt 3538 against 1438)
+  // (a token a CTA stages every key once a token: 8 x 16 rows 623 us against 237, 2000 rows of one
+  // prompt 3546 against 1442)
   split.tokens = 1;
   while (split.tokens < MAX_TOKENS && 2 * split.tokens * split.heads <= MAX_ROWS &&
          2LL * split.tokens * p.rows.B <= p.rows.total_rows)

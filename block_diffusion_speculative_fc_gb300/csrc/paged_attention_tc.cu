@@ -23,17 +23,21 @@
 // fewer, both hold the same rows and take even and odd tiles, which halves the
 // serial chain of a tile: those items are bound by the K/V bytes.  S and the
 // rounded weights w share their TMEM columns (w is the second product's A
-// operand, read from TMEM; V is read as staged, keys by dims).
+// operand, read from TMEM; V is read as staged, keys by dims).  The rounding of
+// w to bf16 is what the product's A operand holds beside bf16 values: 2^-8 of
+// sum_p softmax_p |V_p| at most, while l sums the unrounded weights.
 //
 // Measured (32 query heads on 8 KV heads of 128, graph replays): two prompts of
-// 2500 and 4096 tokens 215 us, 880 TFLOP/s of visible products; 32 requests x 16
-// rows over a shared prefix of 8192 and 256..4096 rows of their own 148 us
+// 2500 and 4096 tokens 216 us, 875 TFLOP/s of visible products; 32 requests x 16
+// rows over a shared prefix of 8192 and 256..4096 rows of their own 149 us
 // (kernel 130, plan and join 19); 64 single tokens of 64 heads over a prefix of
-// 16384 118 us; one token over 1001 keys 19 us.  A 128-key step takes a stream
-// about 5000 clocks: 2350 in the softmax (TMEM reads, the maximum, exponentials
-// and the rounding of 128 scores a thread), 1400 in its two products, the rest
-// waiting for its turn at the tensor pipe and for barriers: the tensor pipe is
-// 40% busy and the streams' warps bound it.
+// 16384 118 us; 128 requests x 16 rows over 64..14755 rows of their own and no
+// prefix 625 us (3.9 GB of keys and values at 6.3 TB/s: HBM bounds it), with one
+// row each 610 us; one token over 1001 keys 19 us.  Where HBM does not bound it a
+// 128-key step takes a stream about 5000 clocks: 2350 in the softmax (TMEM reads,
+// the maximum, exponentials and the rounding of 128 scores a thread), 1400 in its
+// two products, the rest waiting for its turn at the tensor pipe and for
+// barriers; the tensor pipe is 40% busy.
 //
 // Warps 0-3, 4-7: the streams; 8: TMA producer (a ring of K and V tiles, one
 // copy per page and 64 dims); 9, 10: issue the MMAs of a stream each; 11
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   const long long W = block_sum((long long)KVH * nkt * ceil_div(n, tpt), s_sum) +
                       (long long)KVH * nktp * ceil_div(rows, tpt);
   // At half an SM's share the SMs end more evenly, but there are twice the partial rows to write
-  // and join: shared-prefix verification 163 us against 150, shared-prefix tokens 126 against 120,
+  // and join: shared-prefix verification 160 us against 149, shared-prefix tokens 124 against 118,
   // prompts (whose requests' items are smaller than either) 216 both ways.
   long long U = (W + p.sms - 1) / p.sms;
   U = U < 2 ? 2 : U;
@@ -532,7 +536,8 @@ __device__ __noinline__ void list_spoiled(const Params &p, int *s_redo, int req,
 
 // The rows of the CTA's list over their visible keys alone, by its first 256 threads.  A warp takes 32
 // keys at a time, a key a lane for the scores, D / 32 dims a lane for the values; the row's weight (lse)
-// stands already, as no score of a hidden key enters it.
+// stands already, as no score of a hidden key enters it.  24 ns a key and row (12 with 64 dims): 16 rows
+// over 200000 keys 78 ms.
 template <int D> __device__ __noinline__ void redo_rows(const Params &p, int first, float *sm) {
   constexpr int W = 8, V = D / 32;
   float *s_q = sm, *s_m = s_q + D, *s_l = s_m + W, *s_o = s_l + W;      // [D], [W], [W], [W][D]
@@ -561,7 +566,7 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
         slot = (((int64_t)(pg >= 0 && pg < r.n_pages ? pg : 0) * kPageRows + key % kPageRows) * KVH + g) * D;
         const uint4 *k = reinterpret_cast<const uint4 *>((const bf16 *)p.a.k_pages + slot);
         float dot = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
           const uint4 u = k[c];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -579,14 +584,23 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
       l = l * alpha + warp_sum(w);
 #pragma unroll
       for (int c = 0; c < V; ++c) o[c] *= alpha;
-      for (int j = 0; j < n; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j) + lane * V;
+      for (int j0 = 0; j0 < n; j0 += 8) {  // eight keys' values in flight
+        uint32_t u[8][V / 2];
 #pragma unroll
-        for (int c = 0; c < V; c += 2) {
-          const uint32_t u = *reinterpret_cast<const uint32_t *>(v + c);
-          o[c] = fmaf(wj, __uint_as_float(u << 16), o[c]);
-          o[c + 1] = fmaf(wj, __uint_as_float(u & 0xffff0000u), o[c + 1]);
+        for (int j = 0; j < 8; ++j) {
+          const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j0 + j) + lane * V;
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c)
+            u[j][c] = j0 + j < n ? reinterpret_cast<const uint32_t *>(v)[c] : 0u;   // (a key that is none weighs 0)
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) {
+            o[2 * c] = fmaf(wj, __uint_as_float(u[j][c] << 16), o[2 * c]);
+            o[2 * c + 1] = fmaf(wj, __uint_as_float(u[j][c] & 0xffff0000u), o[2 * c + 1]);
+          }
         }
       }
     }

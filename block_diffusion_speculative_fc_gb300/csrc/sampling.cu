@@ -14,13 +14,13 @@
 // runs on shared memory.  Batches of many rows take a CTA a row, which reads it
 // again from L2 (or HBM) instead.
 //
-// Measured: 16 rows of 151936 bf16 logits with top-k and top-p 13.1 us (clusters
+// Measured: 16 rows of 151936 bf16 logits with top-k and top-p 13.5 us (clusters
 // of 8, latency: loads, five cluster barriers, the list's sort); 2048 rows of
-// mixed kinds 519 us, 3.6 TB/s of the floor's bytes (two CTAs of 16 warps an SM
+// mixed kinds 520 us, 3.6 TB/s of the floor's bytes (two CTAs of 16 warps an SM
 // take turns loading, scanning and storing; 417 us with top-k and top-p in every
-// row, 645 us with top-p alone, where 8% of the rows need the histogram); one
-// draw 8.8 us, 128 draws of 163840 logits 61 us (the rows with the histogram
-// take 40 us each, the others 10).
+// row, 650 us with top-p alone, where 8% of the rows need the histogram); one
+// draw 8.8 us, 128 draws of 163840 logits 54 to 68 us by their logits (the rows
+// with the histogram take about 50 us each, the others 10).
 //
 // Most rows keep few tokens, and those are found without a histogram or a
 // sort of the row.  Every CTA takes the j-th largest of its threads' maxima
@@ -1204,11 +1204,11 @@ template <typename T, bool DRAW> cudaError_t launch(const SampleParams &p, cudaS
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // A CTA a row once that fills the GPU: no cluster barriers, at the price of reading the row again
-  // (304 rows of 151936: 65 us against 82 with top-k and top-p, 67 against 74 unfiltered; 128 rows the
-  // other way round, 40 us against 36).
+  // (304 rows of 151936: 66 us against 84 with top-k and top-p, 67 against 74 unfiltered; 128 rows 35
+  // against 40 and 40 against 34).
   if (p.rows >= 2 * sms && p.vocab <= STREAM_VOCAB) return launch<T, DRAW, false>(p, 1, s);
   // The fewest CTAs whose slices leave room for two of them on an SM (128 rows of 151936: 40 us with
-  // clusters of 4, 53 with 8); more while rows are too few to fill the GPU and a slice stays worth a CTA
+  // clusters of 4, 52 with 8); more while rows are too few to fill the GPU and a slice stays worth a CTA
   // (down to half of 4096: unfiltered rows of 4000 to 16000 0.1 to 0.4 us less, 16 filtered ones of
   // 16000 9.5 us against 8.2; no smaller than 16384: 0.3 to 1.5 us more for 1 to 8 rows)
   int C = 1;
