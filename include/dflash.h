@@ -72,7 +72,8 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 } dflash_dtype;
 #define DFLASH_DERR_ROW_RANGE 0x40u   /* inject: negative n_rows, or rows outside [0, total_rows) */
                                       /* target side: a row_start pair that is no range of rows, or
                                          a row that two requests claim */
-#define DFLASH_DERR_SAMPLING 0x80u    /* a sampling parameter outside its range */
+#define DFLASH_DERR_SAMPLING 0x80u    /* a sampling parameter outside its range, or a draw without a
+                                         variate */
 #define DFLASH_DERR_EMPTY_ROW 0x100u  /* a row of logits with nothing to sample from */
 
 /*
@@ -483,7 +484,7 @@ int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hid
  * n_heads a multiple of n_kv_heads, at most 128 query heads per KV head and
  * 1024 in all; head_dim 64 or 128.  The calls take batch <= 1024, total_rows *
  * n_heads <= 2^28, positions below 2^31 (prefix_len < 2^30, pages_per_req <
- * 2^24).
+ * 2^24), n_pages < 2^25.
  */
 typedef struct {
   dflash_dtype dtype;
@@ -625,10 +626,9 @@ typedef struct {
  * overlap logits.  The border of top-p is decided on sums of about 1e-9
  * relative error (2^-20 for the weight of the tail that lies far beyond it),
  * that of min-p in 64 bits; the same in every run.  A probability comes from
- * float32 arithmetic and the hardware's exponential: relative error about (3
- * (max x - x_v) log2(e) / T + 16) 2^-24 and the roundings of the sum (some tens
- * of 2^-24).
- * vocab <= 524288 (bf16) or 262144 (fp32).
+ * float32 arithmetic and the hardware's exponential: relative error up to (3
+ * (max x - x_v) / T + 8) 2^-24 and the roundings of the sum (some tens of them).
+ * vocab <= 524288 (bf16) or 262144 (fp32), rows <= 2^24.
  */
 int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
                         dflash_dtype dtype, int64_t row_stride, const dflash_sampling *params,
