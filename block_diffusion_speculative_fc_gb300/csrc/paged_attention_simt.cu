@@ -11,7 +11,7 @@
 // through distributed shared memory in rank order.
 //
 // Measured (inputs beyond L2): 8 requests x 16 rows of 32 heads over 2064 keys
-// of 8 heads 237 us (18 TFLOP/s); one token over 1001 keys 24 us; 64 tokens over
+// of 8 heads 235 us (18 TFLOP/s); one token over 1001 keys 24 us; 64 tokens over
 // 2001 keys each 350 us.
 //
 // Tokens of one CTA that belong to different requests are taken in turn, so a
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
   float *Ps = Qs + QR * D;           // [QR][PS]
   __shared__ int s_owner[MAX_TOKENS], s_owners[MAX_TOKENS];
   __shared__ float s_m[QR], s_l[QR];
-  __shared__ unsigned long long s_claimed;   // rows of all ranges
+  unsigned &s_claimed = *reinterpret_cast<unsigned *>(Ps);   // rows of all ranges, until the first weights
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -57,25 +57,26 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
   if (tid < MAX_TOKENS) s_owners[tid] = 0;
   if (tid == 0) s_claimed = 0;
   __syncthreads();
-  unsigned long long claimed = 0;
+  unsigned claimed = 0;              // up to one more than there are (at most 2^28)
+  const unsigned over = (unsigned)r.total_rows + 1;
   for (int i = tid; i < r.B; i += THREADS) {
     const int a = r.row_start[i], e = r.row_start[i + 1];
     if (a < 0 || a > e || e > r.total_rows) {
       if (t0 == 0) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
       continue;
     }
-    claimed += (unsigned long long)(e - a);
+    claimed = min(claimed + (unsigned)(e - a), over);
     for (int t = max(a, t0); t < min(e, t0 + split.tokens); ++t) {
       s_owner[t - t0] = i;
       atomicAdd(&s_owners[t - t0], 1);
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) claimed += __shfl_xor_sync(0xffffffffu, claimed, o);
+  for (int o = 16; o > 0; o >>= 1) claimed = min(claimed + __shfl_xor_sync(0xffffffffu, claimed, o), over);
   if (lane == 0 && claimed) atomicAdd(&s_claimed, claimed);
   __syncthreads();
   if (tid < split.tokens && s_owners[tid] > 1) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
-  if (s_claimed > (unsigned long long)r.total_rows) {   // every CTA finds the same, and none writes
+  if (s_claimed >= over) {           // every CTA finds the same, and none writes
     if (tid == 0) raise_error(p.err, DFLASH_DERR_ROW_RANGE);
     return;
   }
@@ -251,7 +252,7 @@ cudaError_t launch(const PagedAttnParams &p, const Split &split, int sms, cudaSt
   const int64_t tiles = (p.rows.total_rows + split.tokens - 1) / split.tokens;
   const int64_t ctas = tiles * p.KVH * split.blocks;
   // Keys split while the CTAs are fewer than two an SM: one token over 1001 keys 24 us against 134
-  // unsplit, 8 x 16 rows over 2064 keys 237 against 508.  (Up to four an SM: 32 x 16 rows 1212 us
+  // unsplit, 8 x 16 rows over 2064 keys 235 against 508.  (Up to four an SM: 32 x 16 rows 1212 us
   // against 1377, but 64 single tokens 380 against 351.)
   int C = 1;
   while (C < MAXC && ctas * C < 2 * sms) C *= 2;
@@ -279,7 +280,7 @@ template <int D> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
   Split split;
   split.heads = std::min(G, MAX_ROWS);
   split.blocks = (G + split.heads - 1) / split.heads;
-  // (a token a CTA stages every key once a token: 8 x 16 rows 623 us against 237, 2000 rows of one
+  // (a token a CTA stages every key once a token: 8 x 16 rows 623 us against 235, 2000 rows of one
   // prompt 3546 against 1442)
   split.tokens = 1;
   while (split.tokens < MAX_TOKENS && 2 * split.tokens * split.heads <= MAX_ROWS &&
