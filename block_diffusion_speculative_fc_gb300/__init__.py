@@ -21,7 +21,7 @@ P_VOID = ctypes.POINTER(c_void_p)
 DFLASH_F32, DFLASH_BF16 = 0, 1
 DERR_BITS = {0x1: "KV_CAPACITY", 0x2: "PAGE_RANGE", 0x4: "TOKEN_RANGE", 0x8: "POSITION",
              0x10: "OUTPUT_ROW", 0x20: "TIMEOUT", 0x40: "ROW_RANGE", 0x80: "SAMPLING",
-             0x100: "EMPTY_ROW"}
+             0x100: "EMPTY_ROW", 0x200: "TREE", 0x400: "ROW_LIST"}
 EXPORTED = ["dflash_create", "dflash_destroy", "dflash_workspace_size", "dflash_bind_workspace",
             "dflash_inject_context", "dflash_draft_block", "dflash_accept_commit",
             "dflash_accept_commit_sampled",
@@ -29,6 +29,9 @@ EXPORTED = ["dflash_create", "dflash_destroy", "dflash_workspace_size", "dflash_
             "dflash_accept_commit_sampled_q",
             "dflash_rope_init", "dflash_append_kv", "dflash_paged_attention_workspace_size",
             "dflash_paged_attention", "dflash_target_probs", "dflash_sample_tokens",
+            "dflash_tree_plan", "dflash_append_kv_at", "dflash_tree_attention",
+            "dflash_accept_commit_tree", "dflash_key_weights", "dflash_choose_rows",
+            "dflash_keep_rows",
             "dflash_get_error", "dflash_status_string", "dflash_last_error",
             "dflash_profile_enable", "dflash_profile_disable", "dflash_profile_collect"]
 
@@ -135,6 +138,28 @@ def load_library(path=LIB_PATH):
     lib.dflash_paged_attention.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_int32,
                                            c_void_p, c_void_p, c_void_p, c_int64, c_float, c_int32,
                                            c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.dflash_tree_plan.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                     c_int32, c_void_p, c_void_p, c_void_p]
+    lib.dflash_append_kv_at.argtypes = (lib.dflash_append_kv.argtypes[:6] + [c_void_p]
+                                        + lib.dflash_append_kv.argtypes[6:])
+    lib.dflash_tree_attention.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_int32,
+                                          c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int64,
+                                          c_float, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,
+                                          c_void_p]
+    lib.dflash_accept_commit_tree.argtypes = [c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                                              c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, c_int32, c_void_p]
+    lib.dflash_key_weights.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_int32,
+                                       c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int64,
+                                       c_float, c_void_p, c_void_p, c_float, c_void_p, c_int32,
+                                       c_void_p]
+    lib.dflash_choose_rows.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_void_p,
+                                       c_void_p, c_int32, c_void_p, c_int32, c_int32, c_int32,
+                                       c_void_p, c_void_p, c_void_p]
+    lib.dflash_keep_rows.argtypes = [c_void_p, ctypes.POINTER(DflashLayerKV), c_int32, c_void_p,
+                                     c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                     c_void_p]
     lib.dflash_target_probs.argtypes = [c_void_p, c_int32, c_int32, c_void_p, ctypes.c_int, c_int64,
                                         ctypes.POINTER(DflashSampling), c_void_p, c_void_p]
     lib.dflash_sample_tokens.argtypes = [c_void_p, c_int32, c_int32, c_void_p, ctypes.c_int,
@@ -156,7 +181,9 @@ def load_library(path=LIB_PATH):
                  "dflash_accept_commit_sampled_q", "dflash_get_error", "dflash_profile_enable", "dflash_profile_disable",
                  "dflash_profile_collect", "dflash_rope_init", "dflash_append_kv",
                  "dflash_paged_attention_workspace_size", "dflash_paged_attention",
-                 "dflash_target_probs", "dflash_sample_tokens"]:
+                 "dflash_target_probs", "dflash_sample_tokens", "dflash_tree_plan",
+                 "dflash_append_kv_at", "dflash_tree_attention", "dflash_accept_commit_tree",
+                 "dflash_key_weights", "dflash_choose_rows", "dflash_keep_rows"]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -300,6 +327,59 @@ def dflash_sample_tokens(h, rows, vocab, logits, dtype, row_stride, params: Dfla
                          exp_noise, ids, prob, stream):
     _check(load_library().dflash_sample_tokens(h, rows, vocab, _p(logits), dtype, row_stride,
                                                params, _p(exp_noise), _p(ids), _p(prob), stream))
+
+
+def dflash_tree_plan(h, batch, total_rows, row_start, parent, root_pos, mask_words, mask, positions,
+                     stream):
+    _check(load_library().dflash_tree_plan(h, batch, total_rows, _p(row_start), _p(parent),
+                                           _p(root_pos), mask_words, _p(mask), _p(positions),
+                                           stream))
+
+
+def dflash_append_kv_at(h, kv: DflashLayerKV, batch, total_rows, row_start, kv_len, positions, q,
+                        q_stride, k, k_stride, v, v_stride, q_gain, k_gain, eps, rope: DflashRope,
+                        q_out, q_out_stride, stream):
+    _check(load_library().dflash_append_kv_at(h, kv, batch, total_rows, _p(row_start), _p(kv_len),
+                                              _p(positions), _p(q), q_stride, _p(k), k_stride,
+                                              _p(v), v_stride, _p(q_gain), _p(k_gain), eps, rope,
+                                              _p(q_out), q_out_stride, stream))
+
+
+def dflash_tree_attention(h, kv: DflashLayerKV, batch, total_rows, row_start, kv_len, mask,
+                          mask_words, q, q_stride, scale, out, out_stride, lse, workspace, nbytes,
+                          stream):
+    _check(load_library().dflash_tree_attention(h, kv, batch, total_rows, _p(row_start),
+                                                _p(kv_len), _p(mask), mask_words, _p(q), q_stride,
+                                                scale, _p(out), out_stride, _p(lse),
+                                                _p(workspace), nbytes, stream))
+
+
+def dflash_accept_commit_tree(h, batch, total_rows, row_start, parent, tokens, posterior, max_path,
+                              seq_len, accept_len, commit_len, bonus, out_tokens, path, row_weight,
+                              output_ids, out_stride, stream):
+    _check(load_library().dflash_accept_commit_tree(
+        h, batch, total_rows, _p(row_start), _p(parent), _p(tokens), _p(posterior), max_path,
+        _p(seq_len), _p(accept_len), _p(commit_len), _p(bonus), _p(out_tokens), _p(path),
+        _p(row_weight), _p(output_ids), out_stride, stream))
+
+
+def dflash_key_weights(h, kv: DflashLayerKV, batch, total_rows, row_start, kv_len, mask, mask_words,
+                       q, q_stride, scale, lse, row_weight, decay, weights, width, stream):
+    _check(load_library().dflash_key_weights(h, kv, batch, total_rows, _p(row_start), _p(kv_len),
+                                             _p(mask), mask_words, _p(q), q_stride, scale, _p(lse),
+                                             _p(row_weight), decay, _p(weights), width, stream))
+
+
+def dflash_choose_rows(h, kv: DflashLayerKV, batch, kv_len, weights, width, keep, first, last,
+                       max_keep, rows, count, stream):
+    _check(load_library().dflash_choose_rows(h, kv, batch, _p(kv_len), _p(weights), width, _p(keep),
+                                             first, last, max_keep, _p(rows), _p(count), stream))
+
+
+def dflash_keep_rows(h, kv: DflashLayerKV, batch, first, lists, max_rows, rows, count, weights,
+                     width, stream):
+    _check(load_library().dflash_keep_rows(h, kv, batch, _p(first), lists, max_rows, _p(rows),
+                                           _p(count), _p(weights), width, stream))
 
 
 def dflash_get_error(h, stream):

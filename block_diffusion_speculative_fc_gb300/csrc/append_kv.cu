@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
   }
   const int pos = (int)pos64, own = pos - r.prefix_len;
   const int page = r.page_table[(int64_t)b * r.pages_per_req + own / kPageRows];
-  const int half = p.rot >> 1;
+  const int half = p.rot >> 1, at = p.positions ? p.positions[t] : pos;
   for (int i = tid; i < half; i += nt) {
-    const unsigned long long turn = (unsigned long long)pos * p.turns[i];
+    const unsigned long long turn = (unsigned long long)at * p.turns[i];
     float sn, cs;   // of pi * x, x in [-1, 1): half turns
     sincospif((float)(int)(turn >> 32) * 0x1p-31f, &sn, &cs);
     s_cs[i] = make_float2(cs * p.amp, sn * p.amp);

@@ -157,6 +157,10 @@ cudaError_t prepare_kernels() {
   if (e == cudaSuccess) e = prepare_sampling();
   if (e == cudaSuccess) e = prepare_paged_attention_simt();
   if (e == cudaSuccess) e = prepare_paged_attention_tc();
+  if (e == cudaSuccess) e = prepare_tree();
+  if (e == cudaSuccess) e = prepare_key_weights_tc();
+  if (e == cudaSuccess) e = prepare_key_weights_simt();
+  if (e == cudaSuccess) e = prepare_choose_rows();
   return e;
 }
 

@@ -35,7 +35,7 @@ struct Split {
   int tokens, heads, blocks;   // of a CTA; blocks of heads in a group
 };
 
-template <int D, int RPW>
+template <int D, int RPW, bool TREE>
 __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_constant__ PagedAttnParams p,
                                                              const Split split) {
   constexpr int QR = WARPS * RPW, KS = D + 4, PS = KT + 4, C4 = D / 4, V = D / 32;
@@ -91,9 +91,14 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
       if (tid == 0) raise_error(p.err, DFLASH_DERR_KV_CAPACITY);
       continue;
     }
+    if (TREE && p.mask && n > 32 * p.mask_words) {
+      if (tid == 0) raise_error(p.err, DFLASH_DERR_TREE);
+      continue;
+    }
     const int rows = (next - first) * hn, tok = t0 + first;   // query row i: token tok + i / hn
-    const int low = p.causal ? kv + (tok - a) + 1 : kv + n;   // keys that the first token sees
-    const int keys = p.causal ? low + (next - first) - 1 : low;
+    // keys that the first token sees (with a mask: that every token sees)
+    const int low = TREE && p.mask ? kv : p.causal ? kv + (tok - a) + 1 : kv + n;
+    const int keys = TREE && p.mask ? kv + n : p.causal ? low + (next - first) - 1 : low;
     for (int i = tid; i < rows * C4; i += THREADS) {
       const int q = i / C4;
       const float4 x = *(reinterpret_cast<const float4 *>((const float *)p.q + (int64_t)(tok + q / hn) * p.q_stride +
@@ -133,6 +138,19 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
       }
       __syncthreads();
       if (warp >= rows) continue;
+      uint32_t seen[RPW];            // of the tile's keys, where a mask decides on some
+      const bool masked = TREE && p.mask && k0 + KT > low;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i) {
+          const int q = min(warp + WARPS * i, rows - 1), at = k0 - kv, j = at >> 5;
+          const uint32_t *row = p.mask + (int64_t)(tok + q / hn) * p.mask_words;
+          const uint32_t w0 = j < 0 ? 0xffffffffu : j < p.mask_words ? row[j] : 0u;
+          const uint32_t w1 = j + 1 < 0 ? 0xffffffffu : j + 1 < p.mask_words ? row[j + 1] : 0u;
+          seen[i] = __funnelshift_r(w0, w1, at & 31);
+          if (keys - k0 < KT) seen[i] &= (1u << (keys - k0)) - 1u;
+        }
+      }
       float s[RPW];
 #pragma unroll
       for (int i = 0; i < RPW; ++i) s[i] = 0.f;
@@ -150,7 +168,8 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
       }
 #pragma unroll
       for (int i = 0; i < RPW; ++i) {
-        const float x = k0 + lane < lim[i] ? s[i] : -INFINITY;
+        const bool sees = masked ? (seen[i] >> lane & 1u) != 0 : k0 + lane < lim[i];
+        const float x = sees ? s[i] : -INFINITY;
         const float mx = fmaxf(m[i], warp_max(x));
         // where every score so far is -infinity there is nothing to rescale
         const float base = mx == -INFINITY ? 0.f : mx;
@@ -183,7 +202,8 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
       } else {                       // a key that a row does not see may hold anything
 #pragma unroll
         for (int i = 0; i < RPW; ++i)
-          for (int k = 0; k < min(KT, lim[i] - k0); ++k) {
+          for (int k = 0; k < min(KT, (masked ? keys : lim[i]) - k0); ++k) {
+            if (masked && !(seen[i] >> k & 1u)) continue;
             __align__(16) float v[V];
             value(k, v);
             const float w = Ps[(warp + WARPS * i) * PS + k];
@@ -197,14 +217,23 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
       if (V == 4) reinterpret_cast<float4 *>(out)[lane] = *reinterpret_cast<const float4 *>(x);
       else reinterpret_cast<float2 *>(out)[lane] = *reinterpret_cast<const float2 *>(x);
     };
+    // with masks a row may see nothing: zeros
+    auto divide = [](float x, float sum) { return TREE && sum == 0.f ? 0.f : x / sum; };
+    auto store_lse = [&](int q, float mx, float sum) {
+      if (TREE && p.lse && lane == 0)
+        p.lse[(int64_t)(tok + q / hn) * p.H + g * G + h0 + q % hn] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    };
     __syncthreads();                 // the queries have been read
     if (C == 1) {
 #pragma unroll
       for (int i = 0; i < RPW; ++i) {
         __align__(16) float x[V];
 #pragma unroll
-        for (int c = 0; c < V; ++c) x[c] = o[i][c] / l[i];
-        if (warp + WARPS * i < rows) store(warp + WARPS * i, x);
+        for (int c = 0; c < V; ++c) x[c] = divide(o[i][c], l[i]);
+        if (warp + WARPS * i < rows) {
+          store(warp + WARPS * i, x);
+          store_lse(warp + WARPS * i, m[i], l[i]);
+        }
       }
       continue;
     }
@@ -236,8 +265,9 @@ __global__ void __launch_bounds__(THREADS) paged_simt_kernel(const __grid_consta
         for (int c = 0; c < V; ++c) x[c] = fmaf(f, ok[c], x[c]);
       }
 #pragma unroll
-      for (int c = 0; c < V; ++c) x[c] /= sum;
+      for (int c = 0; c < V; ++c) x[c] = divide(x[c], sum);
       store(q, x);
+      store_lse(q, mx, sum);
     }
     cl.sync();                       // read by every rank before the next tokens' queries come
   }
@@ -247,7 +277,7 @@ template <int D, int RPW> size_t smem() {
   return sizeof(float) * (KT * (D + 4) + KT * D + WARPS * RPW * (D + KT + 4));
 }
 
-template <int D, int RPW>
+template <int D, int RPW, bool TREE>
 cudaError_t launch(const PagedAttnParams &p, const Split &split, int sms, cudaStream_t s) {
   const int64_t tiles = (p.rows.total_rows + split.tokens - 1) / split.tokens;
   const int64_t ctas = tiles * p.KVH * split.blocks;
@@ -269,10 +299,10 @@ cudaError_t launch(const PagedAttnParams &p, const Split &split, int sms, cudaSt
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   cfg.gridDim = dim3((unsigned)(tiles * C), (unsigned)(p.KVH * split.blocks));
-  return cudaLaunchKernelEx(&cfg, paged_simt_kernel<D, RPW>, p, split);
+  return cudaLaunchKernelEx(&cfg, paged_simt_kernel<D, RPW, TREE>, p, split);
 }
 
-template <int D> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
+template <int D, bool TREE> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -287,14 +317,17 @@ template <int D> cudaError_t launch(const PagedAttnParams &p, cudaStream_t s) {
          2LL * split.tokens * p.rows.B <= p.rows.total_rows)
     split.tokens *= 2;
   const int rows = split.tokens * split.heads;
-  if (rows <= WARPS) return launch<D, 1>(p, split, sms, s);
-  if (rows <= 2 * WARPS) return launch<D, 2>(p, split, sms, s);
-  if (rows <= 4 * WARPS) return launch<D, 4>(p, split, sms, s);
-  return launch<D, 8>(p, split, sms, s);
+  if (rows <= WARPS) return launch<D, 1, TREE>(p, split, sms, s);
+  if (rows <= 2 * WARPS) return launch<D, 2, TREE>(p, split, sms, s);
+  if (rows <= 4 * WARPS) return launch<D, 4, TREE>(p, split, sms, s);
+  return launch<D, 8, TREE>(p, split, sms, s);
 }
 template <int D, int RPW> cudaError_t prepare() {
-  return cudaFuncSetAttribute(paged_simt_kernel<D, RPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)smem<D, RPW>());
+  const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, RPW, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem<D, RPW>());
+  return e == cudaSuccess ? cudaFuncSetAttribute(paged_simt_kernel<D, RPW, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem<D, RPW>())
+                          : e;
 }
 template <int D> cudaError_t prepare() {
   cudaError_t e = prepare<D, 1>();
@@ -306,7 +339,8 @@ template <int D> cudaError_t prepare() {
 }  // namespace
 
 cudaError_t launch_paged_attention_simt(const PagedAttnParams &p, cudaStream_t s) {
-  return p.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
+  if (p.tree) return p.D == 64 ? launch<64, true>(p, s) : launch<128, true>(p, s);
+  return p.D == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);
 }
 
 cudaError_t prepare_paged_attention_simt() {

@@ -50,6 +50,7 @@
 #include "common.cuh"
 #include "paged_rows.cuh"
 #include "target_ops.h"
+#include "tcgen.cuh"
 
 namespace dflash {
 namespace {
@@ -68,8 +69,7 @@ constexpr int BUCKETS = 128;              // sizes that the item list is ordered
 // a second time.
 constexpr int P_COL = KT / 2;
 constexpr float TAU = 8.f;
-constexpr uint32_t WAIT_NS = 20000;       // longest sleep of one try
-constexpr uint32_t WAIT_LIMIT = 1u << 16; // tries (about a second)
+constexpr float LN2 = 0.6931471805599453f;
 
 template <int D> struct Cfg {
   static constexpr int TILE = KT * D * 2;             // K (or V) tile
@@ -88,7 +88,7 @@ template <int D> struct Cfg {
 struct Item {
   int g, tok0, ntok, req;                 // KV head, first token, tokens, request (-1: prefix)
   int page0, ntiles, keys_left, part;     // first page, tiles, keys from the first to the segment's end, partial rows (-1: final)
-  int lim_base, lim_slope, pad0, pad1;    // keys that row's token sees: lim_base + lim_slope * token
+  int lim_base, lim_slope, pad0, pad1;    // keys that row's token sees: lim_base + lim_slope * token (with a mask: and those of it)
 };
 struct Request {
   int start, n, ctx, splits;              // first row, rows (0: skipped), own rows before them
@@ -101,8 +101,8 @@ struct Head {
 
 // A row of an item to do again.
 struct Redo {
-  int at, req, page0, lim;                // token * H + head, request, first page, keys that the row sees
-  int part, next, pad0, pad1;             // partial row (-1: final), next of the CTA's list (-1: none)
+  int at, req, page0, lim;                // token * H + head, request, first page, keys to go through
+  int part, next, all, pad;               // partial row (-1: final), next of the CTA's list (-1: none), of the keys those that the row sees without a look at its mask
 };
 
 struct Params {
@@ -113,152 +113,12 @@ struct Params {
   Item *items;
   Request *req;
   int *row_req;                           // [total_rows]
-  Redo *redo;                             // [total_rows * H]
+  Redo *redo;                             // rows to do again, of every split
   float *part_o, *part_lse;               // [partial rows][D], [partial rows]
   int sms;
   float scale_log2;                       // |scale| log2 e
   int negative;                           // scale < 0: S changes its sign
 };
-
-// ------------------------------------------------------------------ PTX
-__device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *b, uint32_t count) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(b), "r"(parity), "r"(WAIT_NS)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait for the phase of parity `parity`; false = gave up.  The thread
-// sleeps in the barrier: eight warps that polled took a quarter of the shared
-// memory bandwidth that the products need.
-__device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity) {
-  for (uint32_t i = 0; i < WAIT_LIMIT; ++i)
-    if (mbar_try(b, parity)) return true;
-  return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity) { return mbar_wait(su32(b), parity); }
-__device__ __forceinline__ void tma3(void *dst, const CUtensorMap *tm, uint64_t *bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
-      "l"((uint64_t)tm), "r"(su32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-// D += A B^T: both operands in shared memory, or A in TMEM
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar))
-               : "memory");
-}
-// 32 columns of the warp's TMEM lanes, without the wait
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(*reinterpret_cast<uint64_t *>(&d))
-      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
-        "l"(*reinterpret_cast<uint64_t *>(&c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(*reinterpret_cast<uint64_t *>(&d))
-      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
-  return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ void store32(void *p, const uint32_t *v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Shared-memory operand descriptors, 128-byte swizzle: K-major (rows of 128
-// bytes along K, 8-row groups 1 KB apart); MN-major (a row per K index, 64
-// elements along N; `lbo` bytes between 64-element blocks).
-__device__ __forceinline__ uint64_t desc_base(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) { return desc_base(saddr) | ((uint64_t)1 << 16); }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
-  return desc_base(saddr) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16);
-}
-// kind::f16: bf16 A and B, fp32 D; b_mn: B is MN-major
-constexpr uint32_t idesc(int M, int N, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
 
 // Places of V(t) and K(t) in an item's load order: the first `ahead` K tiles,
 // then V(0), K(ahead), V(1), K(ahead + 1), ...
@@ -360,6 +220,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       claimed = e - a;
       if (kv < prefix || (int64_t)kv + (e - a) - prefix > (int64_t)r.pages_per_req * kPageRows) {
         raise_error(p.a.err, DFLASH_DERR_KV_CAPACITY);
+      } else if (p.a.mask && e - a > 32 * p.a.mask_words) {
+        raise_error(p.a.err, DFLASH_DERR_TREE);
       } else {
         start = a;
         n = e - a;
@@ -463,7 +325,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
       it.keys_left = c + nq - s * tiles * KT;
       it.part = s_part[q] >= 0 ? s_part[q] + (g * ns + s) * Rq + rt * 2 * tpt * G : -1;
       it.lim_slope = p.a.causal;
-      it.lim_base = (p.a.causal ? c + 1 - st : c + nq) - s * tiles * KT;
+      it.lim_base = (p.a.mask ? c : p.a.causal ? c + 1 - st : c + nq) - s * tiles * KT;
     }
     it.pad0 = it.pad1 = 0;
     return it;
@@ -508,12 +370,59 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 // the result gives them away (`odd`); the warp then looks for the last of them here (fewer than 2 * 128 +
 // 128 keys lie between `lim`, the keys that a row sees, and `end`) and lists the rows before it, which
 // the CTA does again once it has no more items: nothing waits for it then, however many keys they see.
-template <int D>
+
+// 32 bits of what a row of the mask says of the new rows from number `first` on; of the keys before
+// the new rows (negative numbers) it sees all.  A mask that is none holds nothing.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, int first) {
+  const int i = first >> 5;
+  auto word = [&](int j) { return j < 0 ? 0xffffffffu : mask && j < words ? __ldg(mask + j) : 0u; };
+  return __funnelshift_r(word(i), word(i + 1), first & 31);
+}
+__device__ __forceinline__ const uint32_t *mask_of(const PagedAttnParams &a, int token) {
+  return a.mask ? a.mask + (int64_t)token * a.mask_words : nullptr;
+}
+// bits of the first n keys of 32
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+template <int D, bool TREE>
 __device__ __noinline__ void list_spoiled(const Params &p, int *s_redo, int req, int g, int page0, int at, int part,
                                           int lim, int end, bool odd) {
   const int from = __reduce_min_sync(0xffffffffu, odd ? lim : end);
   const int *list = p.a.rows.page_table + (int64_t)req * p.a.rows.pages_per_req + page0;
   constexpr int C = D / 8;                 // 16-byte chunks of a key's values
+  auto list_row = [&](int all, int keys) {
+    const int i = atomicAdd(&p.head->redo, 1);
+    Redo e;
+    e.at = at, e.req = req, e.page0 = page0, e.lim = keys;
+    e.part = part, e.next = atomicExch(s_redo, i), e.all = all, e.pad = 0;
+    p.redo[i] = e;
+  };
+  if (TREE) {                              // every such key against every row's mask
+    const int lo = max(from, 0);
+    const uint32_t *mask = mask_of(p.a, at / p.a.H);
+    bool hit = false;
+    for (int i0 = 0; i0 < (end - lo) * C; i0 += 32) {
+      const int i = i0 + (int)(threadIdx.x & 31);
+      bool bad = false;
+      if (i < (end - lo) * C) {
+        const int key = lo + i / C, pg = list[key / kPageRows];
+        const int64_t slot = (int64_t)(pg >= 0 && pg < p.a.rows.n_pages ? pg : 0) * kPageRows + key % kPageRows;
+        const uint4 v = *(reinterpret_cast<const uint4 *>((const bf16 *)p.a.v_pages + (slot * p.a.KVH + g) * D) + i % C);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          bad = bad || (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+      }
+      for (uint32_t b = __ballot_sync(0xffffffffu, bad); b; b &= b - 1) {
+        const int key = lo + (i0 + __ffs(b) - 1) / C;
+        hit = hit || !(mask_bits(mask, p.a.mask_words, key - lim) & 1u);
+      }
+    }
+    if (odd && hit) list_row(lim, end);
+    return;
+  }
   int last = -1;
   for (int i = (int)(threadIdx.x & 31); i < (end - from) * C; i += 32) {
     const int key = from + i / C, pg = list[key / kPageRows];
@@ -525,20 +434,14 @@ __device__ __noinline__ void list_spoiled(const Params &p, int *s_redo, int req,
       if ((w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u) last = key;
   }
   last = __reduce_max_sync(0xffffffffu, last);
-  if (odd && lim <= last) {                // (a row has such keys in one split at most)
-    const int i = atomicAdd(&p.head->redo, 1);
-    Redo e;
-    e.at = at, e.req = req, e.page0 = page0, e.lim = lim;
-    e.part = part, e.next = atomicExch(s_redo, i), e.pad0 = e.pad1 = 0;
-    p.redo[i] = e;
-  }
+  if (odd && lim <= last) list_row(lim, lim);   // (a row has such keys in one split at most)
 }
 
 // The rows of the CTA's list over their visible keys alone, by its first 256 threads.  A warp takes 32
 // keys at a time, a key a lane for the scores, D / 32 dims a lane for the values; the row's weight (lse)
 // stands already, as no score of a hidden key enters it.  24 ns a key and row (12 with 64 dims): 16 rows
 // over 200000 keys 78 ms.
-template <int D> __device__ __noinline__ void redo_rows(const Params &p, int first, float *sm) {
+template <int D, bool TREE> __device__ __noinline__ void redo_rows(const Params &p, int first, float *sm) {
   constexpr int W = 8, V = D / 32;
   float *s_q = sm, *s_m = s_q + D, *s_l = s_m + W, *s_o = s_l + W;      // [D], [W], [W], [W][D]
   const int H = p.a.H, KVH = p.a.KVH, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -550,6 +453,7 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
     next = e.next;
     const int t = e.at / H, h = e.at % H, g = h / (H / KVH);
     const int *list = r.page_table + (int64_t)e.req * r.pages_per_req + e.page0;
+    const uint32_t *mask = TREE ? mask_of(p.a, t) : nullptr;
     sync();                                // the row before has been read
     for (int d = threadIdx.x; d < D; d += 256)
       s_q[d] = to_f32(((const bf16 *)p.a.q)[(int64_t)t * p.a.q_stride + (int64_t)h * D + d]);
@@ -561,7 +465,8 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
       const int key = k0 + lane, n = min(32, e.lim - k0);
       int64_t slot = 0;
       float x = -INFINITY;
-      if (lane < n) {
+      const uint32_t seen = TREE ? mask_bits(mask, p.a.mask_words, k0 - e.all) & first_bits(n) : first_bits(n);
+      if (seen >> lane & 1u) {
         const int pg = list[key / kPageRows];
         slot = (((int64_t)(pg >= 0 && pg < r.n_pages ? pg : 0) * kPageRows + key % kPageRows) * KVH + g) * D;
         const uint4 *k = reinterpret_cast<const uint4 *>((const bf16 *)p.a.k_pages + slot);
@@ -591,7 +496,7 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
           const bf16 *v = (const bf16 *)p.a.v_pages + __shfl_sync(0xffffffffu, slot, j0 + j) + lane * V;
 #pragma unroll
           for (int c = 0; c < V / 2; ++c)
-            u[j][c] = j0 + j < n ? reinterpret_cast<const uint32_t *>(v)[c] : 0u;   // (a key that is none weighs 0)
+            u[j][c] = seen >> (j0 + j) & 1u ? reinterpret_cast<const uint32_t *>(v)[c] : 0u;   // (other keys weigh 0)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -628,7 +533,7 @@ template <int D> __device__ __noinline__ void redo_rows(const Params &p, int fir
   }
 }
 
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
   constexpr int NS = C::NSLOT, NB = D / 64;
@@ -971,6 +876,14 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           };
           const int vis = lim - t * KT;                        // visible keys of this tile
           const bool whole = __all_sync(0xffffffffu, vis >= KT);
+          uint32_t bits[KT / 32];                              // of them, where the new rows are among them
+          if (TREE && !whole) {
+            const uint32_t *mask = mask_of(p.a, tok);
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i)
+              bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) & first_bits(it.keys_left - t * KT - 32 * i);
+          }
+          auto sees = [&](int e) { return TREE ? (bits[e >> 5] >> (e & 31) & 1u) != 0 : e < vis; };
           auto maximum = [&](int half, float a0) {
             if (whole) {
               float a1 = __uint_as_float(sv[0]), a2 = __uint_as_float(sv[1]), a3 = __uint_as_float(sv[2]);
@@ -987,14 +900,15 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               return max3(fmaxf(a0, a1), a2, a3);
             }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) a0 = half * 64 + i < vis ? fmaxf(a0, __uint_as_float(sv[i])) : a0;
+            for (int i = 0; i < 64; ++i) a0 = sees(half * 64 + i) ? fmaxf(a0, __uint_as_float(sv[i])) : a0;
             return a0;
           };
           load(0);
           float mx = maximum(0, -INFINITY);
           load(1);
           mx = maximum(1, mx);
-          mx = vis > 0 ? mx * sl : -INFINITY;
+          if (TREE) mx = whole || (bits[0] | bits[1] | bits[2] | bits[3]) ? mx * sl : -INFINITY;
+          else mx = vis > 0 ? mx * sl : -INFINITY;
           float alpha = 1.f;
           if (mx > m + TAU || m == -INFINITY) {
             if (m != -INFINITY) alpha = ex2(m - mx);
@@ -1011,8 +925,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
               float2 q = make_float2(ex2(a.x), ex2(a.y));
               if (!whole) {
-                q.x = e < vis ? q.x : 0.f;
-                q.y = e + 1 < vis ? q.y : 0.f;
+                q.x = sees(e) ? q.x : 0.f;
+                q.y = sees(e + 1) ? q.y : 0.f;
               }
               sum = add2(sum, q);
               __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
@@ -1073,8 +987,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (both) release(order_v(n - 2, n, ahead));
         }
         if (live) {
-          // a split may hold no key that the row sees; a whole row of -infinities has no result (NaN)
-          const float inv = l == 0.f && it.part >= 0 ? 0.f : 1.f / l;
+          // a split may hold no key that the row sees; a whole row of -infinities has no result (NaN),
+          // with masks zeros, as one that sees nothing
+          const float inv = l == 0.f && (TREE || it.part >= 0) ? 0.f : 1.f / l;
           // keys of these tiles that the row does not see
           const int end = min(n * KT, it.keys_left);
           const bool hides = own && lim < end && l != 0.f;
@@ -1085,6 +1000,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           const int at = it.part + mine * G + row_head;        // partial row
           float *po = p.part_o + (int64_t)at * D;
           if (own && it.part >= 0) p.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+          if (TREE && own && it.part < 0 && p.a.lse)
+            p.a.lse[(int64_t)tok * p.a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
@@ -1128,7 +1045,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             }
           }
           if (__builtin_expect(__any_sync(0xffffffffu, odd), 0))
-            list_spoiled<D>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
+            list_spoiled<D, TREE>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
         }
         tc_fence_before();
         mbar_arrive(&o_read[x]);
@@ -1145,7 +1062,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
   __syncthreads();
   // (every copy has landed and every product ended: the ring is free)
   if (__builtin_expect(*s_redo >= 0, 0)) {
-    if (threadIdx.x < 256) redo_rows<D>(p, *s_redo, reinterpret_cast<float *>(ring));
+    if (threadIdx.x < 256) redo_rows<D, TREE>(p, *s_redo, reinterpret_cast<float *>(ring));
     __syncthreads();
   }
   pdl_trigger();   // every global write of this CTA is done
@@ -1159,7 +1076,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 // A warp a (row, head): out = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max)
 // over the prefix splits and the own splits whose first key the row sees.
 // Eight lanes read one partial row, so that a warp has four in flight.
-template <int D>
+template <int D, bool TREE>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const Head *head = p.head;
@@ -1217,7 +1134,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         }
       }
     }
-    const float inv = 1.f / warp_sum(den);
+    const float sum = warp_sum(den), inv = TREE && sum == 0.f ? 0.f : 1.f / sum;
+    if (TREE && lane == 0 && p.a.lse)
+      p.a.lse[(int64_t)t * H + h] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * LN2;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -1241,34 +1160,6 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 }
 
 // ------------------------------------------------------------------ host
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-EncodeTiledFn encoder() {
-  static EncodeTiledFn fn = [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return (EncodeTiledFn)ptr;
-  }();
-  return fn;
-}
-bool encode_pages(CUtensorMap *tm, const void *base, int n_pages, int kvh, int D) {
-  EncodeTiledFn fn = encoder();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)kvh, (cuuint64_t)n_pages * kPageRows};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)kvh * D * 2};
-  cuuint32_t box[3] = {64, 1, 64};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_rows(CUtensorMap *tm, const void *q, int total_rows, int H, int D, int64_t stride, int G) {
   EncodeTiledFn fn = encoder();
   if (!fn) return false;
@@ -1297,20 +1188,22 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   const int tpt = 128 / (H / KVH);
   const int64_t rows = (int64_t)total_rows * H, tiles = (int64_t)total_rows / (2 * tpt) + 1;
   const int64_t max_items = KVH * (B + tiles) + (prefix > 0 ? KVH * tiles : 0) + EXTRA;
-  const int64_t cap = rows * (prefix > 0 ? 2 : 1) +
-                      (int64_t)EXTRA * std::min(2 * tpt, total_rows) * (H / KVH);
+  const int64_t extra = (int64_t)EXTRA * std::min(2 * tpt, total_rows) * (H / KVH);
+  const int64_t cap = rows * (prefix > 0 ? 2 : 1) + extra;
   L.head = take(sizeof(Head));
   L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);
   L.row_req = take(4 * (size_t)total_rows);
-  L.redo = take(sizeof(Redo) * (size_t)rows);
+  // a row may be done again in every split that holds new rows (without masks in one): up to 1024 of
+  // them in 9 tiles, and no more items than there are
+  L.redo = take(sizeof(Redo) * (size_t)std::min(9 * rows, rows + extra));
   L.part_lse = take(4 * cap);
   L.part_o = take(4 * cap * D);
   L.total = o;
   return L;
 }
 
-template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, cudaStream_t s) {
+template <int D, bool TREE> cudaError_t launch(const PagedAttnParams &a, void *workspace, cudaStream_t s) {
   const Layout L = layout(a.rows.B, a.rows.total_rows, a.H, a.KVH, D, a.rows.prefix_len);
   char *ws = (char *)workspace;
   Params p;
@@ -1336,15 +1229,18 @@ template <int D> cudaError_t launch(const PagedAttnParams &a, void *workspace, c
   // a thread a request; barriers of 256 threads are cheaper than those of 1024
   cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(a.rows.B <= 256 ? 256 : PLAN_THREADS), 0, s, p);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attention_kernel<D>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
+  e = launch_pdl(paged_attention_kernel<D, TREE>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.rows.total_rows * a.H;
   const int grid = (int)std::min<int64_t>((warps + 7) / 8, 16LL * p.sms);
-  return launch_pdl(paged_join_kernel<D>, dim3(grid), dim3(256), 0, s, p);
+  return launch_pdl(paged_join_kernel<D, TREE>, dim3(grid), dim3(256), 0, s, p);
 }
 template <int D> cudaError_t prepare() {
-  return cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<D, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  return e == cudaSuccess ? cudaFuncSetAttribute(paged_attention_kernel<D, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM)
+                          : e;
 }
 
 }  // namespace
@@ -1354,7 +1250,8 @@ size_t paged_attention_tc_workspace(int B, int total_rows, int H, int KVH, int D
 }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnParams &p, void *workspace, cudaStream_t s) {
-  return p.D == 64 ? launch<64>(p, workspace, s) : launch<128>(p, workspace, s);
+  if (p.tree) return p.D == 64 ? launch<64, true>(p, workspace, s) : launch<128, true>(p, workspace, s);
+  return p.D == 64 ? launch<64, false>(p, workspace, s) : launch<128, false>(p, workspace, s);
 }
 
 cudaError_t prepare_paged_attention_tc() {

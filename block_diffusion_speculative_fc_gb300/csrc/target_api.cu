@@ -69,6 +69,119 @@ PagedRows paged_rows(const dflash_layer_kv *kv, int32_t batch, int32_t total_row
   return r;
 }
 
+int append(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch, int32_t total_rows,
+           const int32_t *row_start, const int32_t *kv_len, const int32_t *positions, const void *q,
+           int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+           int64_t v_stride, const void *q_gain, const void *k_gain, float eps,
+           const dflash_rope *rope, void *q_out, int64_t q_out_stride,
+           dflash_stream_t stream) {
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (int st = check_layer(kv, batch, total_rows)) return st;
+  if (!rope) return fail(DFLASH_EINVAL, "rope is NULL");
+  if (rope->rotary_dim < 0 || rope->rotary_dim % 2 || rope->rotary_dim > kv->head_dim)
+    return fail(DFLASH_EINVAL, "rotary_dim must be even and at most head_dim");
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(DFLASH_EINVAL, "eps must be >= 0 and finite");
+  if ((q == nullptr) != (q_out == nullptr)) return fail(DFLASH_EINVAL, "q and q_out go together");
+  if (!q && q_gain) return fail(DFLASH_EINVAL, "q_gain without q");
+  const bool empty = batch == 0 || total_rows == 0;
+  if (!empty && (!row_start || !kv_len || !k || !v))
+    return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
+  const size_t es = elem(kv->dtype);
+  const int64_t qw = (int64_t)kv->n_heads * kv->head_dim, kw = (int64_t)kv->n_kv_heads * kv->head_dim;
+  if (!empty && ((q && (q_stride < qw || q_out_stride < qw)) || k_stride < kw || v_stride < kw))
+    return fail(DFLASH_EINVAL, "a row stride is below the row's width");
+  if ((q && (!aligned16(q, q_stride, es) || !aligned16(q_out, q_out_stride, es))) ||
+      !aligned16(k, k_stride, es) || !aligned16(v, v_stride, es) || (uintptr_t)q_gain % 16 ||
+      (uintptr_t)k_gain % 16)
+    return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
+  if (q && q == q_out && q_stride != q_out_stride && total_rows > 1)
+    return fail(DFLASH_EINVAL, "q_out is q with another row stride");
+  if (int st = handle_ready(h, &p.err)) return st;
+  if (empty) return DFLASH_OK;
+  p.rows = paged_rows(kv, batch, total_rows, row_start, kv_len);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.positions = positions;
+  p.q_gain = q_gain;
+  p.k_gain = k_gain;
+  p.q_out = q_out;
+  p.k_pages = kv->k_pages;
+  p.v_pages = kv->v_pages;
+  p.H = q ? kv->n_heads : 0;
+  p.KVH = kv->n_kv_heads;
+  p.eps = eps;
+  p.rot = rope->rotary_dim;
+  p.inter = rope->interleaved;
+  p.amp = rope->amplitude;
+  std::memcpy(p.turns, rope->turns, sizeof(p.turns));
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, "append_kv", s);
+  return handle_timed_end(h, idx, "append_kv", s, launch_append_kv(kv->dtype, kv->head_dim, p, s));
+}
+
+int check_batch(int32_t batch, int32_t total_rows) {
+  if (batch < 0 || total_rows < 0) return fail(DFLASH_EINVAL, "negative batch or total_rows");
+  if (batch > 1024) return fail(DFLASH_ECAPACITY, "batch > 1024");
+  if (total_rows > (1 << 28)) return fail(DFLASH_ECAPACITY, "total_rows > 2^28");
+  return DFLASH_OK;
+}
+
+int check_mask(const uint32_t *mask, int32_t mask_words) {
+  if (mask ? mask_words < 1 || mask_words > kMaxTreeRows / 32 : mask_words != 0)
+    return fail(DFLASH_EINVAL, "mask_words must be 1 to 32, 0 without a mask");
+  if (!aligned4(mask)) return fail(DFLASH_EINVAL, "mask must be 4-byte aligned");
+  return DFLASH_OK;
+}
+
+// The two attention calls; of *p what tells them apart is filled.
+int attend(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch, int32_t total_rows,
+           const int32_t *row_start, const int32_t *kv_len, const void *q, int64_t q_stride,
+           float scale, void *out, int64_t out_stride, void *workspace, size_t bytes,
+           const char *name, dflash_stream_t stream, PagedAttnParams &p) {
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  size_t need = 0;
+  if (int st = dflash_paged_attention_workspace_size(kv, batch, total_rows, &need)) return st;
+  if (p.causal != 0 && p.causal != 1) return fail(DFLASH_EINVAL, "causal must be 0 or 1");
+  if (std::isnan(scale) || std::isinf(scale)) return fail(DFLASH_EINVAL, "scale must be finite");
+  if (batch == 0 || total_rows == 0) return handle_ready(h, &p.err);
+  if (!row_start || !kv_len || !q || !out) return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (q == out) return fail(DFLASH_EINVAL, "out must not be q");
+  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
+  const size_t es = elem(kv->dtype);
+  const int64_t qw = (int64_t)kv->n_heads * kv->head_dim;
+  if (q_stride < qw || out_stride < qw) return fail(DFLASH_EINVAL, "a row stride is below the row's width");
+  if (!aligned16(q, q_stride, es) || !aligned16(out, out_stride, es))
+    return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
+  if (!workspace || (uintptr_t)workspace % 256)
+    return fail(DFLASH_EINVAL, "workspace must be non-NULL and 256-byte aligned");
+  if (bytes < need) return fail(DFLASH_ECAPACITY, "workspace too small");
+  if (int st = handle_ready(h, &p.err)) return st;
+  p.rows = paged_rows(kv, batch, total_rows, row_start, kv_len);
+  p.q = q;
+  p.k_pages = kv->k_pages;
+  p.v_pages = kv->v_pages;
+  p.out = out;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.H = kv->n_heads;
+  p.KVH = kv->n_kv_heads;
+  p.D = kv->head_dim;
+  p.scale = scale;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, name, s);
+  return handle_timed_end(h, idx, name, s,
+                          kv->dtype == DFLASH_BF16 ? launch_paged_attention_tc(p, workspace, s)
+                                                   : launch_paged_attention_simt(p, s));
+}
+
 // Checks shared by the two sampling calls; *p is filled but for the outputs.
 int sampling_params(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,
                     dflash_dtype dtype, int64_t row_stride, const dflash_sampling *sp,
@@ -161,55 +274,20 @@ int dflash_append_kv(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
                      int64_t v_stride, const void *q_gain, const void *k_gain, float eps,
                      const dflash_rope *rope, void *q_out, int64_t q_out_stride,
                      dflash_stream_t stream) {
-  AppendParams p;
-  std::memset(&p, 0, sizeof(p));
-  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
-  if (int st = check_layer(kv, batch, total_rows)) return st;
-  if (!rope) return fail(DFLASH_EINVAL, "rope is NULL");
-  if (rope->rotary_dim < 0 || rope->rotary_dim % 2 || rope->rotary_dim > kv->head_dim)
-    return fail(DFLASH_EINVAL, "rotary_dim must be even and at most head_dim");
-  if (!(eps >= 0.f) || std::isinf(eps)) return fail(DFLASH_EINVAL, "eps must be >= 0 and finite");
-  if ((q == nullptr) != (q_out == nullptr)) return fail(DFLASH_EINVAL, "q and q_out go together");
-  if (!q && q_gain) return fail(DFLASH_EINVAL, "q_gain without q");
-  const bool empty = batch == 0 || total_rows == 0;
-  if (!empty && (!row_start || !kv_len || !k || !v))
-    return fail(DFLASH_EINVAL, "a required pointer is NULL");
-  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
-  const size_t es = elem(kv->dtype);
-  const int64_t qw = (int64_t)kv->n_heads * kv->head_dim, kw = (int64_t)kv->n_kv_heads * kv->head_dim;
-  if (!empty && ((q && (q_stride < qw || q_out_stride < qw)) || k_stride < kw || v_stride < kw))
-    return fail(DFLASH_EINVAL, "a row stride is below the row's width");
-  if ((q && (!aligned16(q, q_stride, es) || !aligned16(q_out, q_out_stride, es))) ||
-      !aligned16(k, k_stride, es) || !aligned16(v, v_stride, es) || (uintptr_t)q_gain % 16 ||
-      (uintptr_t)k_gain % 16)
-    return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
-  if (q && q == q_out && q_stride != q_out_stride && total_rows > 1)
-    return fail(DFLASH_EINVAL, "q_out is q with another row stride");
-  if (int st = handle_ready(h, &p.err)) return st;
-  if (empty) return DFLASH_OK;
-  p.rows = paged_rows(kv, batch, total_rows, row_start, kv_len);
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.q_out_stride = q_out_stride;
-  p.q_gain = q_gain;
-  p.k_gain = k_gain;
-  p.q_out = q_out;
-  p.k_pages = kv->k_pages;
-  p.v_pages = kv->v_pages;
-  p.H = q ? kv->n_heads : 0;
-  p.KVH = kv->n_kv_heads;
-  p.eps = eps;
-  p.rot = rope->rotary_dim;
-  p.inter = rope->interleaved;
-  p.amp = rope->amplitude;
-  std::memcpy(p.turns, rope->turns, sizeof(p.turns));
-  cudaStream_t s = (cudaStream_t)stream;
-  const int idx = handle_timed_begin(h, "append_kv", s);
-  return handle_timed_end(h, idx, "append_kv", s, launch_append_kv(kv->dtype, kv->head_dim, p, s));
+  return append(h, kv, batch, total_rows, row_start, kv_len, nullptr, q, q_stride, k, k_stride, v, v_stride,
+                q_gain, k_gain, eps, rope, q_out, q_out_stride, stream);
+}
+
+int dflash_append_kv_at(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                        int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                        const int32_t *positions, const void *q, int64_t q_stride, const void *k,
+                        int64_t k_stride, const void *v, int64_t v_stride, const void *q_gain,
+                        const void *k_gain, float eps, const dflash_rope *rope, void *q_out,
+                        int64_t q_out_stride, dflash_stream_t stream) {
+  if (batch > 0 && total_rows > 0 && !positions) return fail(DFLASH_EINVAL, "positions is NULL");
+  if (!aligned4(positions)) return fail(DFLASH_EINVAL, "positions must be 4-byte aligned");
+  return append(h, kv, batch, total_rows, row_start, kv_len, positions, q, q_stride, k, k_stride, v, v_stride,
+                q_gain, k_gain, eps, rope, q_out, q_out_stride, stream);
 }
 
 int dflash_paged_attention_workspace_size(const dflash_layer_kv *kv, int32_t batch,
@@ -230,41 +308,210 @@ int dflash_paged_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t 
                            dflash_stream_t stream) {
   PagedAttnParams p;
   std::memset(&p, 0, sizeof(p));
+  p.causal = causal;
+  return attend(h, kv, batch, total_rows, row_start, kv_len, q, q_stride, scale, out, out_stride, workspace, bytes,
+                "paged_attention", stream, p);
+}
+
+int dflash_tree_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                          int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                          const uint32_t *mask, int32_t mask_words, const void *q, int64_t q_stride,
+                          float scale, void *out, int64_t out_stride, float *lse, void *workspace,
+                          size_t bytes, dflash_stream_t stream) {
+  if (int st = check_mask(mask, mask_words)) return st;
+  if (!aligned4(lse)) return fail(DFLASH_EINVAL, "lse must be 4-byte aligned");
+  PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.causal = mask == nullptr;
+  p.mask = mask;
+  p.mask_words = mask_words;
+  p.lse = lse;
+  p.tree = 1;
+  return attend(h, kv, batch, total_rows, row_start, kv_len, q, q_stride, scale, out, out_stride, workspace, bytes,
+                "tree_attention", stream, p);
+}
+
+int dflash_tree_plan(dflash_handle *h, int32_t batch, int32_t total_rows, const int32_t *row_start,
+                     const int32_t *parent, const int32_t *root_pos, int32_t mask_words,
+                     uint32_t *mask, int32_t *positions, dflash_stream_t stream) {
+  TreePlanParams p;
   if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
-  size_t need = 0;
-  if (int st = dflash_paged_attention_workspace_size(kv, batch, total_rows, &need)) return st;
-  if (causal != 0 && causal != 1) return fail(DFLASH_EINVAL, "causal must be 0 or 1");
-  if (std::isnan(scale) || std::isinf(scale)) return fail(DFLASH_EINVAL, "scale must be finite");
-  if (batch == 0 || total_rows == 0) return handle_ready(h, &p.err);
-  if (!row_start || !kv_len || !q || !out) return fail(DFLASH_EINVAL, "a required pointer is NULL");
-  if (q == out) return fail(DFLASH_EINVAL, "out must not be q");
-  if (!aligned4(row_start, kv_len)) return fail(DFLASH_EINVAL, "row_start and kv_len must be 4-byte aligned");
-  const size_t es = elem(kv->dtype);
-  const int64_t qw = (int64_t)kv->n_heads * kv->head_dim;
-  if (q_stride < qw || out_stride < qw) return fail(DFLASH_EINVAL, "a row stride is below the row's width");
-  if (!aligned16(q, q_stride, es) || !aligned16(out, out_stride, es))
-    return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
-  if (!workspace || (uintptr_t)workspace % 256)
-    return fail(DFLASH_EINVAL, "workspace must be non-NULL and 256-byte aligned");
-  if (bytes < need) return fail(DFLASH_ECAPACITY, "workspace too small");
+  if (int st = check_batch(batch, total_rows)) return st;
+  if (mask_words < 1 || mask_words > kMaxTreeRows / 32) return fail(DFLASH_EUNSUPPORTED, "mask_words must be 1 to 32");
+  const bool empty = batch == 0 || total_rows == 0;
+  if (!empty && (!row_start || !parent || !root_pos || !mask))
+    return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(row_start, parent, root_pos, mask, positions))
+    return fail(DFLASH_EINVAL, "arrays must be 4-byte aligned");
   if (int st = handle_ready(h, &p.err)) return st;
+  if (empty) return DFLASH_OK;
+  p.row_start = row_start;
+  p.parent = parent;
+  p.root_pos = root_pos;
+  p.mask = mask;
+  p.positions = positions;
+  p.B = batch;
+  p.total_rows = total_rows;
+  p.mask_words = mask_words;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, "tree_plan", s);
+  return handle_timed_end(h, idx, "tree_plan", s, launch_tree_plan(p, s));
+}
+
+int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_rows,
+                              const int32_t *row_start, const int32_t *parent,
+                              const int32_t *tokens, const int32_t *posterior, int32_t max_path,
+                              int32_t *seq_len, int32_t *accept_len, int32_t *commit_len,
+                              int32_t *bonus, int32_t *out_tokens, int32_t *path,
+                              float *row_weight, int32_t *output_ids, int32_t out_stride,
+                              dflash_stream_t stream) {
+  AcceptTreeParams p;
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (int st = check_batch(batch, total_rows)) return st;
+  if (max_path < 1 || max_path > kMaxTreeRows) return fail(DFLASH_EUNSUPPORTED, "max_path must be 1 to 1024");
+  const bool empty = batch == 0 || total_rows == 0;
+  if (!empty && (!row_start || !parent || !tokens || !posterior || !seq_len || !accept_len || !commit_len || !bonus ||
+                 !out_tokens || !path))
+    return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (output_ids && out_stride <= 0) return fail(DFLASH_EINVAL, "out_stride must be positive");
+  if (!aligned4(row_start, parent, tokens, posterior, seq_len, accept_len, commit_len, bonus, out_tokens, path,
+                row_weight, output_ids))
+    return fail(DFLASH_EINVAL, "arrays must be 4-byte aligned");
+  if (int st = handle_ready(h, &p.err)) return st;
+  if (empty) return DFLASH_OK;
+  p.row_start = row_start;
+  p.parent = parent;
+  p.tokens = tokens;
+  p.posterior = posterior;
+  p.seq_len = seq_len;
+  p.accept_len = accept_len;
+  p.commit_len = commit_len;
+  p.bonus = bonus;
+  p.out_tokens = out_tokens;
+  p.path = path;
+  p.row_weight = row_weight;
+  p.output_ids = output_ids;
+  p.B = batch;
+  p.total_rows = total_rows;
+  p.max_path = max_path;
+  p.out_stride = out_stride;
+  const void *lm_head;
+  int hidden, dtype;
+  if (int st = handle_lm_head(h, &lm_head, &hidden, &p.vocab, &dtype)) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, "accept_tree", s);
+  return handle_timed_end(h, idx, "accept_tree", s, launch_accept_tree(p, s));
+}
+
+int dflash_key_weights(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                       int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                       const uint32_t *mask, int32_t mask_words, const void *q, int64_t q_stride,
+                       float scale, const float *lse, const float *row_weight, float decay,
+                       float *weights, int32_t width, dflash_stream_t stream) {
+  KeyWeightParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (int st = check_layer(kv, batch, total_rows)) return st;
+  if (int st = check_mask(mask, mask_words)) return st;
+  if (std::isnan(scale) || std::isinf(scale)) return fail(DFLASH_EINVAL, "scale must be finite");
+  if (!(decay >= 0.f && decay <= 1.f)) return fail(DFLASH_EINVAL, "decay must be 0 to 1");
+  if (width <= 0) return fail(DFLASH_EINVAL, "width must be positive");
+  const bool empty = batch == 0 || total_rows == 0;
+  if (!empty && (!row_start || !kv_len || !q || !lse || !weights))
+    return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(row_start, kv_len, lse, row_weight, weights))
+    return fail(DFLASH_EINVAL, "arrays must be 4-byte aligned");
+  if (q_stride < (int64_t)kv->n_heads * kv->head_dim) return fail(DFLASH_EINVAL, "a row stride is below the row's width");
+  if (!aligned16(q, q_stride, elem(kv->dtype)))
+    return fail(DFLASH_EINVAL, "pointers and row strides must be multiples of 16 bytes");
+  if (int st = handle_ready(h, &p.err)) return st;
+  if (empty) return DFLASH_OK;
   p.rows = paged_rows(kv, batch, total_rows, row_start, kv_len);
+  p.mask = mask;
+  p.mask_words = mask_words;
   p.q = q;
   p.k_pages = kv->k_pages;
-  p.v_pages = kv->v_pages;
-  p.out = out;
   p.q_stride = q_stride;
-  p.out_stride = out_stride;
   p.H = kv->n_heads;
   p.KVH = kv->n_kv_heads;
   p.D = kv->head_dim;
   p.scale = scale;
-  p.causal = causal;
+  p.lse = lse;
+  p.row_weight = row_weight;
+  p.decay = decay;
+  p.weights = weights;
+  p.width = width;
   cudaStream_t s = (cudaStream_t)stream;
-  const int idx = handle_timed_begin(h, "paged_attention", s);
-  return handle_timed_end(h, idx, "paged_attention", s,
-                          kv->dtype == DFLASH_BF16 ? launch_paged_attention_tc(p, workspace, s)
-                                                   : launch_paged_attention_simt(p, s));
+  const int idx = handle_timed_begin(h, "key_weights", s);
+  return handle_timed_end(h, idx, "key_weights", s,
+                          kv->dtype == DFLASH_BF16 ? launch_key_weights_tc(p, s) : launch_key_weights_simt(p, s));
+}
+
+int dflash_choose_rows(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                       const int32_t *kv_len, const float *weights, int32_t width,
+                       const int32_t *keep, int32_t first, int32_t last, int32_t max_keep,
+                       int32_t *rows, int32_t *count, dflash_stream_t stream) {
+  ChooseParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (int st = check_layer(kv, batch, 0)) return st;
+  if (width <= 0 || max_keep <= 0) return fail(DFLASH_EINVAL, "width and max_keep must be positive");
+  if (first < 0 || last < 0) return fail(DFLASH_EINVAL, "negative first or last");
+  if (batch > 0 && (!kv_len || !weights || !keep || !rows || !count))
+    return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(kv_len, weights, keep, rows, count)) return fail(DFLASH_EINVAL, "arrays must be 4-byte aligned");
+  if (int st = handle_ready(h, &p.err)) return st;
+  if (batch == 0) return DFLASH_OK;
+  p.kv_len = kv_len;
+  p.keep = keep;
+  p.weights = weights;
+  p.rows = rows;
+  p.count = count;
+  p.B = batch;
+  p.KVH = kv->n_kv_heads;
+  p.width = width;
+  p.prefix_len = kv->prefix_len;
+  p.first = first;
+  p.last = last;
+  p.max_keep = max_keep;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, "choose_rows", s);
+  return handle_timed_end(h, idx, "choose_rows", s, launch_choose_rows(p, s));
+}
+
+int dflash_keep_rows(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                     const int32_t *first, int32_t lists, int32_t max_rows, const int32_t *rows,
+                     const int32_t *count, float *weights, int32_t width, dflash_stream_t stream) {
+  KeepParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!h) return fail(DFLASH_EINVAL, "handle is NULL");
+  if (int st = check_layer(kv, batch, 0)) return st;
+  if (lists != 1 && lists != kv->n_kv_heads) return fail(DFLASH_EINVAL, "lists must be 1 or n_kv_heads");
+  if (max_rows <= 0) return fail(DFLASH_EINVAL, "max_rows must be positive");
+  if (weights && width <= 0) return fail(DFLASH_EINVAL, "width must be positive");
+  if (batch > 0 && (!rows || !count)) return fail(DFLASH_EINVAL, "a required pointer is NULL");
+  if (!aligned4(first, rows, count, weights)) return fail(DFLASH_EINVAL, "arrays must be 4-byte aligned");
+  if (int st = handle_ready(h, &p.err)) return st;
+  if (batch == 0) return DFLASH_OK;
+  p.first = first;
+  p.rows = rows;
+  p.count = count;
+  p.page_table = kv->page_table;
+  p.k_pages = kv->k_pages;
+  p.v_pages = kv->v_pages;
+  p.weights = weights;
+  p.B = batch;
+  p.KVH = kv->n_kv_heads;
+  p.lists = lists;
+  p.max_rows = max_rows;
+  p.width = width;
+  p.prefix_len = kv->prefix_len;
+  p.pages_per_req = kv->pages_per_req;
+  p.n_pages = kv->n_pages;
+  p.row_bytes = kv->head_dim * (int)elem(kv->dtype);
+  cudaStream_t s = (cudaStream_t)stream;
+  const int idx = handle_timed_begin(h, "keep_rows", s);
+  return handle_timed_end(h, idx, "keep_rows", s, launch_keep_rows(p, s));
 }
 
 int dflash_target_probs(dflash_handle *h, int32_t rows, int32_t vocab, const void *logits,

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/dflash.h"
 
 namespace dflash {
@@ -32,6 +34,7 @@ struct AppendParams {
   int64_t q_stride, k_stride, v_stride, q_out_stride;   // elements
   const void *q_gain, *k_gain;
   void *q_out, *k_pages, *v_pages;
+  const int *positions;      // [total_rows] rotary positions (NULL: the cache rows)
   int H, KVH;                // H = 0: no queries
   float eps;
   int rot, inter;
@@ -49,6 +52,10 @@ struct PagedAttnParams {
   int H, KVH, D;
   float scale;
   int causal;
+  const uint32_t *mask;      // [total_rows, mask_words]: new rows that a row sees (NULL: by `causal`)
+  int mask_words;
+  float *lse;                // [total_rows, H] or NULL
+  int tree;                  // a mask or lse may be given
   unsigned int *err;
 };
 cudaError_t launch_paged_attention_simt(const PagedAttnParams &p, cudaStream_t s);   // fp32
@@ -76,5 +83,71 @@ struct SampleParams {
 int sampling_max_vocab(int dtype);
 cudaError_t launch_sampling(int dtype, const SampleParams &p, cudaStream_t s);
 cudaError_t prepare_sampling();
+
+// ---- trees of drafted tokens ----
+constexpr int kMaxTreeRows = 1024;
+
+struct TreePlanParams {
+  const int *row_start, *parent, *root_pos;
+  uint32_t *mask;
+  int *positions;            // or NULL
+  int B, total_rows, mask_words;
+  unsigned int *err;
+};
+cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s);
+
+struct AcceptTreeParams {
+  const int *row_start, *parent, *tokens, *posterior;
+  int *seq_len, *accept_len, *commit_len, *bonus, *out_tokens, *path;
+  float *row_weight;         // or NULL
+  int *output_ids;           // or NULL
+  int B, total_rows, max_path, out_stride, vocab;
+  unsigned int *err;
+};
+cudaError_t launch_accept_tree(const AcceptTreeParams &p, cudaStream_t s);
+cudaError_t prepare_tree();
+
+// ---- eviction ----
+struct KeyWeightParams {
+  PagedRows rows;
+  const uint32_t *mask;      // as in PagedAttnParams
+  int mask_words;
+  const void *q, *k_pages;
+  int64_t q_stride;
+  int H, KVH, D;
+  float scale;
+  const float *lse;          // [total_rows, H]
+  const float *row_weight;   // [total_rows] or NULL
+  float decay;
+  float *weights;            // [B, KVH, width]
+  int width;
+  unsigned int *err;
+};
+cudaError_t launch_key_weights_tc(const KeyWeightParams &p, cudaStream_t s);     // bf16
+cudaError_t launch_key_weights_simt(const KeyWeightParams &p, cudaStream_t s);   // fp32
+cudaError_t prepare_key_weights_tc();
+cudaError_t prepare_key_weights_simt();
+
+struct ChooseParams {
+  const int *kv_len, *keep;
+  const float *weights;      // [B, KVH, width]
+  int *rows, *count;         // [B, KVH, max_keep], [B, KVH]
+  int B, KVH, width, prefix_len, first, last, max_keep;
+  unsigned int *err;
+};
+cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s);
+cudaError_t prepare_choose_rows();
+
+struct KeepParams {
+  const int *first;          // [B] or NULL (prefix_len)
+  const int *rows, *count;   // [B, lists, max_rows], [B, lists]
+  const int *page_table;
+  void *k_pages, *v_pages;
+  float *weights;            // [B, KVH, width] or NULL
+  int B, KVH, lists, max_rows, width, prefix_len, pages_per_req, n_pages;
+  int row_bytes;             // of a head
+  unsigned int *err;
+};
+cudaError_t launch_keep_rows(const KeepParams &p, cudaStream_t s);
 
 }  // namespace dflash

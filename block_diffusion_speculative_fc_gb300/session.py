@@ -16,7 +16,9 @@ from . import (DFLASH_BF16, DFLASH_F32, DflashConfig, DflashKV, DflashWeights, _
                dflash_selector_workspace_size, dflash_set_selector, dflash_draft_block_selector,
                dflash_accept_commit_sampled_q, dflash_append_kv, dflash_paged_attention,
                dflash_paged_attention_workspace_size, dflash_target_probs, dflash_sample_tokens,
-               DflashSampling, _check, load_library)
+               dflash_append_kv_at, dflash_tree_plan, dflash_tree_attention,
+               dflash_accept_commit_tree, dflash_key_weights, dflash_choose_rows,
+               dflash_keep_rows, DflashSampling, _check, load_library)
 from .target import check, dtype_code, rows_of
 
 
@@ -192,9 +194,11 @@ class DraftSession:
         return batch
 
     def append_kv(self, layer, q, k, v, row_start, kv_len, rope, q_gain=None, k_gain=None,
-                  eps=1e-6, q_out=None):
+                  eps=1e-6, q_out=None, positions=None):
         """Head norms, rotary positions, append to layer's pages: q [rows, H, D]
-        (or None), k, v [rows, KVH, D], rows of any stride; q_out like q."""
+        (or None), k, v [rows, KVH, D], rows of any stride; q_out like q.
+        positions: int32 [rows] rotary positions where they are not the cache
+        rows (a tree's rows, a cache with evicted rows)."""
         batch = self._ragged(layer, row_start, kv_len)
         dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, k.shape[0]
         ks = rows_of(k, "k", layer.n_kv_heads, D, dt, dev)
@@ -208,11 +212,16 @@ class DraftSession:
         for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
             if g is not None:
                 check(g, name, dt, dev, (D,))
-        dflash_append_kv(self.h, layer.struct, batch, rows, row_start, kv_len, q, qs, k, ks, v, vs,
-                         q_gain, k_gain, eps, rope, q_out, qos, _stream())
+        if positions is None:
+            dflash_append_kv(self.h, layer.struct, batch, rows, row_start, kv_len, q, qs, k, ks, v,
+                             vs, q_gain, k_gain, eps, rope, q_out, qos, _stream())
+            return
+        check(positions, "positions", torch.int32, dev, (rows,))
+        dflash_append_kv_at(self.h, layer.struct, batch, rows, row_start, kv_len, positions, q, qs,
+                            k, ks, v, vs, q_gain, k_gain, eps, rope, q_out, qos, _stream())
 
     def attention_workspace(self, layer, batch, total_rows):
-        """Device workspace for paged_attention calls of at most this size."""
+        """Device workspace for paged_attention and tree_attention calls of at most this size."""
         self._on_device(layer.device, "layer")
         n = dflash_paged_attention_workspace_size(layer.struct, batch, total_rows)
         return torch.empty(n, dtype=torch.uint8, device=layer.device)
@@ -228,6 +237,142 @@ class DraftSession:
         dflash_paged_attention(self.h, layer.struct, batch, rows, row_start, kv_len, q, qs,
                                D ** -0.5 if scale is None else scale, 1 if causal else 0, out, os_,
                                workspace, workspace.numel(), _stream())
+
+    # ---- verification of a tree of drafted tokens, eviction (include/dflash.h)
+    def tree_plan(self, row_start, parent, mask, positions=None, root=None):
+        """Ancestor masks (int32 [rows, words], 32 rows a word) and rotary
+        positions (int32 [rows]) of the requests' trees from parent int32
+        [rows]; root int32 [batch]: position of a request's row 0 (kv_len)."""
+        dev = self.device
+        batch, rows = row_start.shape[0] - 1, parent.shape[0]
+        check(row_start, "row_start", torch.int32, dev, (batch + 1,))
+        check(parent, "parent", torch.int32, dev, (rows,))
+        words = self._mask(mask, rows)
+        if root is None:
+            raise ValueError("root: the position of every request's row 0 is needed")
+        check(root, "root", torch.int32, dev, (batch,))
+        if positions is not None:
+            check(positions, "positions", torch.int32, dev, (rows,))
+        dflash_tree_plan(self.h, batch, rows, row_start, parent, root, words, mask, positions,
+                         _stream())
+
+    def _mask(self, mask, rows):
+        if mask is None:
+            return 0
+        check(mask, "mask", torch.int32, self.device)
+        if mask.dim() != 2 or mask.shape[0] != rows:
+            raise ValueError(f"mask: shape [{rows}, words] is needed, not {tuple(mask.shape)}")
+        return mask.shape[1]
+
+    def tree_attention(self, layer, q, row_start, kv_len, out, workspace, mask=None, scale=None,
+                       lse=None):
+        """paged_attention of rows that see the cache and, of their request's new
+        rows, those of their mask (int32 [rows, words]; None: those up to
+        themselves); lse float32 [rows, H]: log of the rows' softmax sums."""
+        batch = self._ragged(layer, row_start, kv_len)
+        dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, q.shape[0]
+        qs = rows_of(q, "q", layer.n_heads, D, dt, dev)
+        os_ = rows_of(out, "out", layer.n_heads, D, dt, dev, rows)
+        words = self._mask(mask, rows)
+        if lse is not None:
+            check(lse, "lse", torch.float32, dev, (rows, layer.n_heads))
+        check(workspace, "workspace", torch.uint8, dev)
+        dflash_tree_attention(self.h, layer.struct, batch, rows, row_start, kv_len, mask, words, q,
+                              qs, D ** -0.5 if scale is None else scale, out, os_, lse, workspace,
+                              workspace.numel(), _stream())
+
+    def accept_tree(self, row_start, parent, tokens, posterior, seq_len, accept_len, commit_len,
+                    bonus, out_tokens, path, output_ids=None, row_weight=None):
+        """Walk down the trees along the target's tokens, and commit: tokens and
+        posterior int32 [rows]; out_tokens, path int32 [batch, max_path];
+        row_weight float32 [rows]: 1 for the path's rows."""
+        dev, i32 = self.device, torch.int32
+        batch, rows = row_start.shape[0] - 1, parent.shape[0]
+        check(row_start, "row_start", i32, dev, (batch + 1,))
+        for t, name in ((parent, "parent"), (tokens, "tokens"), (posterior, "posterior")):
+            check(t, name, i32, dev, (rows,))
+        for t, name in ((seq_len, "seq_len"), (accept_len, "accept_len"),
+                        (commit_len, "commit_len"), (bonus, "bonus")):
+            check(t, name, i32, dev, (batch,))
+        check(path, "path", i32, dev)
+        if path.dim() != 2 or path.shape[0] != batch:
+            raise ValueError(f"path: shape [{batch}, max_path] is needed, not {tuple(path.shape)}")
+        check(out_tokens, "out_tokens", i32, dev, path.shape)
+        if row_weight is not None:
+            check(row_weight, "row_weight", torch.float32, dev, (rows,))
+        stride = 0
+        if output_ids is not None:
+            check(output_ids, "output_ids", i32, dev)
+            if output_ids.dim() != 2 or output_ids.shape[0] < batch:
+                raise ValueError(f"output_ids: shape [{batch}, length] is needed")
+            stride = output_ids.shape[1]
+        dflash_accept_commit_tree(self.h, batch, rows, row_start, parent, tokens, posterior,
+                                  path.shape[1], seq_len, accept_len, commit_len, bonus, out_tokens,
+                                  path, row_weight, output_ids, stride, _stream())
+
+    def _weights(self, layer, weights, batch):
+        check(weights, "weights", torch.float32, layer.device)
+        if weights.dim() != 3 or weights.shape[0] != batch or weights.shape[1] != layer.n_kv_heads:
+            raise ValueError(f"weights: shape [{batch}, {layer.n_kv_heads}, width] is needed, not "
+                             f"{tuple(weights.shape)}")
+        return weights.shape[2]
+
+    def key_weights(self, layer, q, row_start, kv_len, lse, weights, mask=None, row_weight=None,
+                    decay=1.0, scale=None):
+        """weights float32 [batch, KVH, width] <- decay * weights + the attention
+        weight of q's rows (lse of tree_attention, mask as there) on every own
+        cache row; row_weight float32 [rows]: a factor a row."""
+        batch = self._ragged(layer, row_start, kv_len)
+        dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, q.shape[0]
+        qs = rows_of(q, "q", layer.n_heads, D, dt, dev)
+        words = self._mask(mask, rows)
+        check(lse, "lse", torch.float32, dev, (rows, layer.n_heads))
+        if row_weight is not None:
+            check(row_weight, "row_weight", torch.float32, dev, (rows,))
+        width = self._weights(layer, weights, batch)
+        dflash_key_weights(self.h, layer.struct, batch, rows, row_start, kv_len, mask, words, q, qs,
+                           D ** -0.5 if scale is None else scale, lse, row_weight, decay, weights,
+                           width, _stream())
+
+    def choose_rows(self, layer, weights, kv_len, keep, rows, count, first=0, last=0):
+        """The own rows that a budget keeps: keep int32 [batch] of them, the first
+        `first`, the last `last` and the heaviest between; rows int32 [batch,
+        KVH, max_keep] ascending, count int32 [batch, KVH]."""
+        self._on_device(layer.device, "layer")
+        dev, i32, batch = layer.device, torch.int32, kv_len.shape[0]
+        check(kv_len, "kv_len", i32, dev, (batch,))
+        check(keep, "keep", i32, dev, (batch,))
+        width = self._weights(layer, weights, batch)
+        check(count, "count", i32, dev, (batch, layer.n_kv_heads))
+        check(rows, "rows", i32, dev)
+        if rows.dim() != 3 or rows.shape[:2] != count.shape:
+            raise ValueError(f"rows: shape [{batch}, {layer.n_kv_heads}, max_keep] is needed, not "
+                             f"{tuple(rows.shape)}")
+        dflash_choose_rows(self.h, layer.struct, batch, kv_len, weights, width, keep, first, last,
+                           rows.shape[2], rows, count, _stream())
+
+    def keep_rows(self, layer, rows, count, first=None, weights=None):
+        """Moves listed cache rows together in place: rows int32 [batch, lists,
+        max_rows] ascending (lists 1 or KVH; [batch, max_rows]: 1), count int32
+        [batch, lists]; first int32 [batch]: position that the rows count from
+        (None: behind the shared prefix); weights move along."""
+        self._on_device(layer.device, "layer")
+        dev, i32, batch = layer.device, torch.int32, rows.shape[0]
+        if batch > layer.batch:
+            raise ValueError(f"rows: at most the page table's {layer.batch} requests")
+        check(rows, "rows", i32, dev)
+        if rows.dim() not in (2, 3) or (rows.dim() == 3 and rows.shape[1] not in (1, layer.n_kv_heads)):
+            raise ValueError(f"rows: shape [batch, 1 or {layer.n_kv_heads}, max_rows] is needed, not "
+                             f"{tuple(rows.shape)}")
+        lists = rows.shape[1] if rows.dim() == 3 else 1
+        check(count, "count", i32, dev)
+        if count.numel() != batch * lists or count.shape[:1] != rows.shape[:1]:
+            raise ValueError(f"count: shape [{batch}, {lists}] is needed, not {tuple(count.shape)}")
+        if first is not None:
+            check(first, "first", i32, dev, (batch,))
+        width = self._weights(layer, weights, batch) if weights is not None else 0
+        dflash_keep_rows(self.h, layer.struct, batch, first, lists, rows.shape[-1], rows, count,
+                         weights, width, _stream())
 
     def _sampling(self, logits, temperature, top_k, top_p, min_p):
         self._on_device(logits.device, "logits")

@@ -75,6 +75,10 @@ typedef enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 } dflash_dtype;
 #define DFLASH_DERR_SAMPLING 0x80u    /* a sampling parameter outside its range, or a draw without a
                                          variate */
 #define DFLASH_DERR_EMPTY_ROW 0x100u  /* a row of logits with nothing to sample from */
+#define DFLASH_DERR_TREE 0x200u       /* a parent that is no earlier row of its request, or a request
+                                         of more rows than the call or its mask has room for */
+#define DFLASH_DERR_ROW_LIST 0x400u   /* a list of kept rows that does not ascend, or a count, budget
+                                         or row outside its range */
 
 /*
  * Draft model shape.  The draft shares the target's embedding and lm_head,
@@ -652,6 +656,176 @@ int dflash_sample_tokens(dflash_handle *h, int32_t rows, int32_t vocab, const vo
                          dflash_dtype dtype, int64_t row_stride, const dflash_sampling *params,
                          const float *exp_noise, int32_t *ids, float *prob,
                          dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of a tree of drafted tokens.
+ *
+ * A drafter that proposes several tokens for a position (the selector's
+ * candidates, for one) gives a tree instead of a block.  Its rows are appended
+ * like any others, row i of request b in cache row kv_len[b] + i, with row 0 the
+ * anchor; a row's position is that of its depth, and it attends to the cache
+ * and to its own ancestors:
+ *   dflash_tree_plan           positions and masks from the parents, once a step
+ *   dflash_append_kv_at        the rows' K/V, rotated to those positions
+ *   dflash_tree_attention      each layer's attention under the mask
+ *   dflash_accept_commit_tree  the walk down the tree along the target's tokens
+ *   dflash_keep_rows           each layer's accepted rows, moved together
+ * Where the target's tokens are drawn for every row (dflash_sample_tokens on the
+ * rows' logits), the walk commits exactly the target's distribution: each
+ * committed token is the draw of the row before it, whatever was proposed.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Masks and positions of the requests' trees.
+ *   parent     device int32 [total_rows]: the parent's number among its
+ *              request's rows, smaller than the row's own; -1: the row follows
+ *              the cache directly (row 0, the root)
+ *   root_pos   device int32 [batch]: position of a row without a parent (kv_len,
+ *              unless rows of the cache have been evicted)
+ *   mask       device uint32 [total_rows, mask_words]: bit j % 32 of word j / 32 is
+ *              set where row j of the request is the row itself or an ancestor
+ *   positions  optional device int32 [total_rows]: root_pos + depth
+ * A request has at most 32 mask_words rows, mask_words 1 to 32; one that has
+ * more, or a parent out of its range, sets DFLASH_DERR_TREE and is skipped whole.
+ */
+int dflash_tree_plan(dflash_handle *h, int32_t batch, int32_t total_rows, const int32_t *row_start,
+                     const int32_t *parent, const int32_t *root_pos, int32_t mask_words,
+                     uint32_t *mask, int32_t *positions, dflash_stream_t stream);
+
+/*
+ * dflash_append_kv with the rotary position of every row given: row t is rotated
+ * to positions[t] (device int32 [total_rows]) and stored where dflash_append_kv
+ * stores it, at cache row kv_len[b] + row.  For the rows of a tree, and for caches
+ * whose rows have been evicted, where a row's place no longer is its position.
+ */
+int dflash_append_kv_at(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                        int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                        const int32_t *positions, const void *q, int64_t q_stride, const void *k,
+                        int64_t k_stride, const void *v, int64_t v_stride, const void *q_gain,
+                        const void *k_gain, float eps, const dflash_rope *rope, void *q_out,
+                        int64_t q_out_stride, dflash_stream_t stream);
+
+/*
+ * dflash_paged_attention of rows that see all kv_len[b] cache rows before them and,
+ * of the request's new rows, those that their mask names (any mask, a tree's or
+ * not; bits past the request's rows count for nothing).
+ *   mask       device uint32 [total_rows, mask_words], mask_words 1 to 32, or
+ *              NULL (mask_words 0): every row sees the new rows up to itself
+ *   lse        optional device float32 [total_rows, n_heads]:
+ *              ln sum_p exp(scale q[t, h] . K[p, h / group]) over what the row sees
+ * A row that sees nothing (or scores of -infinity alone) gets zeros, lse -infinity.
+ * A request of more than 32 mask_words rows sets DFLASH_DERR_TREE and is skipped.
+ * Everything else, the workspace (of dflash_paged_attention_workspace_size) among
+ * it, as for dflash_paged_attention; lse has the error of its scores, about (D + 8)
+ * 2^-24 of the largest scale sum_d |q_d k_d|, and that of its own rounding.
+ */
+int dflash_tree_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                          int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                          const uint32_t *mask, int32_t mask_words, const void *q, int64_t q_stride,
+                          float scale, void *out, int64_t out_stride, float *lse, void *workspace,
+                          size_t bytes, dflash_stream_t stream);
+
+/*
+ * Walk and commit.  From row 0 of a request the walk goes to the first row whose
+ * parent is the row it stands on and whose token is the target's there, until
+ * there is none (or the path has max_path rows).
+ *   tokens, posterior  device int32 [total_rows]: a row's token, and the target's
+ *                      token after it (argmax or draw)
+ *   path        device int32 [batch, max_path]: the rows walked over, row 0 first,
+ *               padded with -1: the list that dflash_keep_rows takes, commit_len its
+ *               count
+ *   out_tokens  device int32 [batch, max_path]: the tokens of path[1..], the bonus
+ *               (the target's token after the last row), padded with 0
+ *   accept_len, commit_len, bonus, seq_len, output_ids, out_stride: as in
+ *               dflash_accept_commit, with the path's rows in place of the block's
+ *   row_weight  optional device float32 [total_rows]: 1 for the path's rows, 0 for
+ *               the request's others
+ * At most 1024 rows a request; more, or a parent out of its range (a first row with
+ * one), set DFLASH_DERR_TREE.  A committed token outside the vocabulary sets
+ * DFLASH_DERR_TOKEN_RANGE, a commit past out_stride DFLASH_DERR_OUTPUT_ROW.  Nothing is
+ * written for such a request, nor for one without rows.
+ */
+int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_rows,
+                              const int32_t *row_start, const int32_t *parent,
+                              const int32_t *tokens, const int32_t *posterior, int32_t max_path,
+                              int32_t *seq_len, int32_t *accept_len, int32_t *commit_len,
+                              int32_t *bonus, int32_t *out_tokens, int32_t *path,
+                              float *row_weight, int32_t *output_ids, int32_t out_stride,
+                              dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction from a layer's cache by the attention weight that its rows get.
+ *
+ * dflash_key_weights adds up what falls on every cached row, dflash_choose_rows
+ * names the rows that a budget keeps, dflash_keep_rows moves them together; the
+ * caller then sets kv_len to prefix_len + count.  Rows keep the rotation of their
+ * positions; rows appended later take theirs from dflash_append_kv_at.  Every KV
+ * head has rows of its own (as many as the others).  The shared prefix is never
+ * cut.  Row p below is an own row: position prefix_len + p.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Attention weight of the new rows on their request's own rows:
+ *   weights[b][g][p] <- decay weights[b][g][p] + sum_t row_weight[t] sum_{h of g}
+ *                       exp(scale q[t, h] . K[p, g] - lse[t, h])
+ * over the request's new rows t that see row p; rows of this call itself (p from
+ * kv_len[b] - prefix_len on) begin at 0, and with decay 0 nothing is read of the old.
+ *   row_start, kv_len, mask, mask_words, q, scale: as for dflash_tree_attention,
+ *              which gives lse
+ *   row_weight optional device float32 [total_rows] (NULL: 1), such as the accepted
+ *              rows' of dflash_accept_commit_tree
+ *   decay      0 to 1
+ *   weights    device float32 [batch, n_kv_heads, width]; rows past a request's last
+ *              are left as they are.  A request with more than `width` own rows sets
+ *              DFLASH_DERR_KV_CAPACITY and is skipped
+ * A row whose lse is not finite, or whose row_weight is 0, counts for nothing.  Sums
+ * are in float32 and in the same order in every run; a term has the relative error of
+ * its exponent: (D + 8) 2^-24 of the largest scale sum_d |q_d k_d|, and 2^-23 |lse|.
+ */
+int dflash_key_weights(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                       int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
+                       const uint32_t *mask, int32_t mask_words, const void *q, int64_t q_stride,
+                       float scale, const float *lse, const float *row_weight, float decay,
+                       float *weights, int32_t width, dflash_stream_t stream);
+
+/*
+ * Which own rows a budget keeps, per request and KV head: all n = kv_len[b] -
+ * prefix_len of them when n <= keep[b]; else the first a = min(first, keep[b]), the
+ * last z = min(last, keep[b] - a), and of those between the keep[b] - a - z with the
+ * largest weights, lower rows first among equal ones (-0 equals 0; NaN counts as
+ * -infinity).
+ *   weights   device float32 [batch, n_kv_heads, width]
+ *   keep      device int32 [batch], 0 to max_keep
+ *   rows      device int32 [batch, n_kv_heads, max_keep]: the kept rows, ascending; what
+ *             lies behind the count is left as it is
+ *   count     device int32 [batch, n_kv_heads]
+ * kv_len below prefix_len or n above `width` sets DFLASH_DERR_KV_CAPACITY, a keep out of
+ * range DFLASH_DERR_ROW_LIST; the request is skipped.  Of the layer the shape and prefix_len
+ * are read.  batch <= 1024.
+ */
+int dflash_choose_rows(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                       const int32_t *kv_len, const float *weights, int32_t width,
+                       const int32_t *keep, int32_t first, int32_t last, int32_t max_keep,
+                       int32_t *rows, int32_t *count, dflash_stream_t stream);
+
+/*
+ * Moves listed rows of a layer's cache together, in place: for i < count, cache row
+ * first[b] + rows[i] goes to cache row first[b] + i, keys and values, and its weight
+ * with it.
+ *   first     device int32 [batch], positions (kv_len for a tree's path); NULL: prefix_len
+ *   rows      device int32 [batch, lists, max_rows], ascending, >= 0
+ *   count     device int32 [batch, lists], 0 to max_rows
+ *   lists     1 (the heads of a request share a list) or n_kv_heads
+ *   weights   optional device float32 [batch, n_kv_heads, width] of dflash_key_weights
+ * Cache rows behind the moved ones keep what they held.  first below prefix_len, or a
+ * list whose last row lies past the page table (or width), sets DFLASH_DERR_KV_CAPACITY, a
+ * count out of range or a list that does not ascend DFLASH_DERR_ROW_LIST, a page outside the
+ * pool DFLASH_DERR_PAGE_RANGE: that list is skipped whole.  No cache row may belong to two
+ * requests (beyond the prefix).
+ */
+int dflash_keep_rows(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
+                     const int32_t *first, int32_t lists, int32_t max_rows, const int32_t *rows,
+                     const int32_t *count, float *weights, int32_t width, dflash_stream_t stream);
 
 /* Static description of a status code. */
 const char *dflash_status_string(int status);
