@@ -23,9 +23,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------------ choose
-constexpr int CHOOSE_THREADS = 1024, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 2048;
-constexpr int HELD = 48 * 1024;           // weights that a CTA holds
-constexpr size_t CHOOSE_SMEM = HELD * 4 + 2 * BINS * 4;
+constexpr int CHOOSE_THREADS = 512, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 2048;
+constexpr int E = 16;                     // weights of a thread and step
+constexpr int STEP = 32 * E;              // of a warp
+constexpr int MAXC = 8;
 
 // larger image: larger weight; NaN as -infinity, -0 as 0
 __device__ __forceinline__ uint32_t order_image(float v) {
@@ -34,10 +35,11 @@ __device__ __forceinline__ uint32_t order_image(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(CHOOSE_THREADS) choose_rows_kernel(const __grid_constant__ ChooseParams p) {
-  extern __shared__ uint32_t s_dyn[];
-  uint32_t *s_val = s_dyn, *s_hist = s_dyn + HELD;             // [HELD], [2][BINS]
-  __shared__ int s_warp[2][CHOOSE_WARPS], s_bin, s_above, s_total[2];
+// HELD: a warp's rows are one step, whose images stay in registers; else they are read again in each pass.
+template <bool HELD>
+__global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __grid_constant__ ChooseParams p) {
+  __shared__ __align__(16) uint32_t s_hist[2][BINS];
+  __shared__ int s_warp[2][CHOOSE_WARPS], s_bin, s_above, s_count, s_total[2];
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -59,33 +61,55 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_rows_kernel(const __gri
   }
   const float *w = p.weights + (int64_t)list * p.width;
   const int a = min(p.first, keep), z = min(p.last, keep - a), m = keep - a - z;
-  // this CTA's rows
-  const int seg = (n + C - 1) / C, lo = min(n, rank * seg), hi = min(n, lo + seg);
-  auto image = [&](int i) { return i - lo < HELD ? s_val[i - lo] : order_image(w[i]); };
-  for (int i = lo + tid; i < min(hi, lo + HELD); i += CHOOSE_THREADS) s_val[i - lo] = order_image(w[i]);
-  // ---- the cut: the m-th largest image of rows a .. n-z-1
-  uint32_t cut = 0;                       // its bits found so far
-  int need = m;                           // how many of those that agree with them are taken
-  const int from = max(lo, a), to = min(hi, n - z);
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    uint32_t *hist = s_hist + (pass & 1) * BINS;
+  // a warp's rows: a run of consecutive ones, whole steps of 32
+  const int run = (int)(((int64_t)n + C * CHOOSE_WARPS * 32 - 1) / (C * CHOOSE_WARPS * 32)) * 32;
+  const int w0 = (int)min((int64_t)n, (int64_t)(rank * CHOOSE_WARPS + warp) * run), w1 = min(n - w0, run) + w0;
+  uint32_t u[E];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = i0 + 32 * e + lane;
+      u[e] = i < w1 ? order_image(w[i]) : 0u;
+    }
+  };
+  // f(row, its image, whether there is one) for all of the warp's rows, in order
+  auto each = [&](auto f) {
+    if (HELD) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (w0 + 32 * e < w1) f(w0 + 32 * e + lane, u[e], w0 + 32 * e + lane < w1);
+    } else {
+      for (int i0 = w0; i0 < w1; i0 += STEP) {
+        load(i0);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (i0 + 32 * e < w1) f(i0 + 32 * e + lane, u[e], i0 + 32 * e + lane < w1);
+      }
+    }
+  };
+  if (HELD) load(w0);
+  // ---- the cut: the m-th largest image of rows a .. n-z-1, as far down as it takes to tell rows apart
+  uint32_t cut = 0;                       // its high bits
+  int need = m, shift = 32;               // how many of the rows that agree with them are taken; the bits below
+  for (int pass = 0; pass < 3 && m > 0; ++pass) {
+    const int above_bits = shift, bits = pass == 2 ? 10 : 11;
+    uint32_t *hist = s_hist[pass & 1];
     for (int i = tid; i < BINS; i += CHOOSE_THREADS) hist[i] = 0;
     __syncthreads();
-    for (int i = from + tid; i < to; i += CHOOSE_THREADS) {
-      const uint32_t u = image(i);
-      if (pass == 0 || (u ^ cut) >> (shift + bits) == 0) atomicAdd(&hist[u >> shift & ((1u << bits) - 1)], 1u);
-    }
+    shift -= bits;
+    each([&](int i, uint32_t x, bool live) {
+      if (live && i >= a && i < n - z && (pass == 0 || x >> above_bits == cut))
+        atomicAdd(&hist[x >> shift & ((1u << bits) - 1)], 1u);
+    });
     cl.sync();
-    // bins from the top, two a thread: counts of all CTAs, those above, and the bin that holds the cut
-    const int hi_bin = BINS - 1 - 2 * tid;
-    uint32_t c0 = 0, c1 = 0;
+    // bins from the top, four a thread: counts of all CTAs, those above, and the bin that holds the cut
+    uint4 c = make_uint4(0, 0, 0, 0);
     for (int k = 0; k < C; ++k) {
-      const uint32_t *h = cl.map_shared_rank(hist, k);
-      c0 += h[hi_bin];
-      c1 += h[hi_bin - 1];
+      const uint4 h = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, k))[BINS / 4 - 1 - tid];
+      c.x += h.w, c.y += h.z, c.z += h.y, c.w += h.x;
     }
-    int inc = (int)(c0 + c1);
+    const int own = (int)(c.x + c.y + c.z + c.w);
+    int inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, inc, o);
@@ -93,36 +117,32 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_rows_kernel(const __gri
     }
     if (lane == 31) s_warp[0][warp] = inc;
     __syncthreads();
-    int before = lane < warp ? s_warp[0][lane] : 0;             // (as many warps as lanes)
-    before = __reduce_add_sync(0xffffffffu, before);
-    const int above = before + inc - (int)(c0 + c1);
-    if (above < need && need <= above + (int)c0) {
-      s_bin = hi_bin;
-      s_above = above;
-    } else if (above + (int)c0 < need && need <= above + (int)(c0 + c1)) {
-      s_bin = hi_bin - 1;
-      s_above = above + (int)c0;
+    int above = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[0][lane] : 0) + inc - own;
+    if (above < need && need <= above + own) {
+      const int cs[4] = {(int)c.x, (int)c.y, (int)c.z, (int)c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (above < need && need <= above + cs[k]) {
+          s_bin = BINS - 1 - 4 * tid - k;
+          s_above = above;
+          s_count = cs[k];
+        }
+        above += cs[k];
+      }
     }
     __syncthreads();
-    if (need > 0) {
-      cut |= (uint32_t)s_bin << shift;
-      need -= s_above;
-    }
+    cut = cut << bits | (uint32_t)s_bin;
+    need -= s_above;
+    if (need == s_count) break;           // all of them are taken
   }
-  // m == 0: nothing of the middle is taken
-  const bool none = m == 0;
-  auto above_cut = [&](int i, uint32_t u) { return i < a || i >= n - z || (!none && u > cut); };
-  auto at_cut = [&](int i, uint32_t u) { return i >= a && i < n - z && !none && u == cut; };
-  // ---- places: a warp a run of consecutive rows
-  const int run = ((hi - lo + CHOOSE_WARPS - 1) / CHOOSE_WARPS + 31) / 32 * 32;
-  const int w0 = min(hi, lo + warp * run), w1 = min(hi, w0 + run);
+  // ---- places
+  auto above_cut = [&](int i, uint32_t x) { return i < a || i >= n - z || (m > 0 && x >> shift > cut); };
+  auto at_cut = [&](int i, uint32_t x) { return i >= a && i < n - z && m > 0 && x >> shift == cut; };
   int above = 0, equal = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t u = i < w1 ? image(i) : 0;
-    above += __popc(__ballot_sync(0xffffffffu, i < w1 && above_cut(i, u)));
-    equal += __popc(__ballot_sync(0xffffffffu, i < w1 && at_cut(i, u)));
-  }
+  each([&](int i, uint32_t x, bool live) {
+    above += __popc(__ballot_sync(0xffffffffu, live && above_cut(i, x)));
+    equal += __popc(__ballot_sync(0xffffffffu, live && at_cut(i, x)));
+  });
   __syncthreads();
   if (lane == 0) {
     s_warp[0][warp] = above;
@@ -140,49 +160,74 @@ __global__ void __launch_bounds__(CHOOSE_THREADS) choose_rows_kernel(const __gri
     above += *cl.map_shared_rank(&s_total[0], k);
     equal += *cl.map_shared_rank(&s_total[1], k);
   }
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t u = i < w1 ? image(i) : 0, before = (1u << lane) - 1;
-    const bool is_above = i < w1 && above_cut(i, u), is_equal = i < w1 && at_cut(i, u);
+  const uint32_t before = (1u << lane) - 1;
+  each([&](int i, uint32_t x, bool live) {
+    const bool is_above = live && above_cut(i, x), is_equal = live && at_cut(i, x);
     const uint32_t ba = __ballot_sync(0xffffffffu, is_above), be = __ballot_sync(0xffffffffu, is_equal);
     const int eq = equal + __popc(be & before);
     if (is_above || (is_equal && eq < need)) rows[above + __popc(ba & before) + min(eq, need)] = i;
     above += __popc(ba);
     equal += __popc(be);
-  }
+  });
   cl.sync();                              // no CTA leaves while another reads its totals
 }
 
 // ------------------------------------------------------------------ keep
-constexpr int KEEP_THREADS = 256, UNITS = 8;
+constexpr int KEEP_THREADS = 256, UNITS = 4;
 
-// `bytes` of a row in this CTA's slice: 16 a lane.
+// A slice of 16 LANES bytes of the listed rows, UNITS rows a thread and step.  A step's rows are loaded
+// while the step before is stored (sources of later steps lie behind its places), and their slots are
+// looked up a step earlier still: list, page and row are three loads that wait for one another.
 template <int LANES>
 __device__ __forceinline__ void move_rows(uint4 *pages, const int *table, const int *list, int count, int own,
                                           int64_t row_step, int lane16) {
-  // pages: the slice of head g in cache row 0; row_step: 16-byte chunks from one cache row to the next
-  constexpr int RP = KEEP_THREADS / LANES;
+  // pages: head g of cache row 0; row_step: 16-byte chunks from one cache row to the next
+  constexpr int RP = KEEP_THREADS / LANES, ROWS = RP * UNITS;
   const int r = threadIdx.x / LANES, c = threadIdx.x % LANES + lane16;
-  auto slot = [&](int row) { return ((int64_t)table[row / kPageRows] * kPageRows + row % kPageRows) * row_step + c; };
-  for (int i0 = 0; i0 < count; i0 += RP * UNITS) {
-    uint4 v[UNITS];
-    int64_t to[UNITS];
+  struct Step {
+    int from[UNITS], to[UNITS];            // slots; -1: stays where it is
+  };
+  auto look_up = [&](int i0, Step &s) {
+    int src[UNITS];
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int i = i0 + u * RP + r;
-      to[u] = -1;
-      if (i < count) {
-        const int src = list[i];
-        if (src != i) {
-          v[u] = pages[slot(own + src)];
-          to[u] = slot(own + i);
-        }
+      src[u] = i < count ? __ldg(list + i) : i;
+    }
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const int i = i0 + u * RP + r, f = own + src[u], t = own + i;
+      s.from[u] = s.to[u] = -1;
+      if (src[u] != i) {
+        s.from[u] = __ldg(table + f / kPageRows) * kPageRows + f % kPageRows;
+        s.to[u] = __ldg(table + t / kPageRows) * kPageRows + t % kPageRows;
       }
     }
-    __syncthreads();
+  };
+  auto load = [&](const Step &s, uint4 *v) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-      if (to[u] >= 0) pages[to[u]] = v[u];
+      if (s.from[u] >= 0) v[u] = pages[s.from[u] * row_step + c];
+  };
+  auto store = [&](const Step &s, const uint4 *v) {
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+      if (s.to[u] >= 0) pages[s.to[u] * row_step + c] = v[u];
+  };
+  Step s0, s1, s2;
+  uint4 v0[UNITS], v1[UNITS];
+  look_up(0, s0);
+  look_up(ROWS, s1);
+  load(s0, v0);
+  for (int i0 = 0; i0 < count; i0 += ROWS) {
+    load(s1, v1);
+    look_up(i0 + 2 * ROWS, s2);
+    __syncthreads();                       // the rows of this step are loaded
+    store(s0, v0);
+    s0 = s1;
+    s1 = s2;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) v0[u] = v1[u];
   }
 }
 
@@ -204,6 +249,7 @@ __global__ void __launch_bounds__(KEEP_THREADS) keep_rows_kernel(const __grid_co
   const int own = first - p.prefix_len;
   // ---- the list as a whole: ascending, its last row and its pages there
   bool falls = false;
+#pragma unroll 4
   for (int i = tid; i < count; i += KEEP_THREADS) falls = falls || list[i] <= (i > 0 ? list[i - 1] : -1);
   if (__syncthreads_or(falls)) {
     if (reports) raise_error(p.err, DFLASH_DERR_ROW_LIST);
@@ -253,16 +299,12 @@ template <int LANES> cudaError_t launch_keep(const KeepParams &p, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t lists = (int64_t)p.B * p.KVH;
   int C = 1;
-  while (C < 8 && lists * C * 2 <= sms && p.width / C >= 2048) C *= 2;
+  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(lists * C));
   cfg.blockDim = dim3(CHOOSE_THREADS);
-  cfg.dynamicSmemBytes = CHOOSE_SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -272,11 +314,8 @@ cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, choose_rows_kernel, p);
-}
-
-cudaError_t prepare_choose_rows() {
-  return cudaFuncSetAttribute(choose_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CHOOSE_SMEM);
+  return (int64_t)C * CHOOSE_WARPS * STEP >= p.width ? cudaLaunchKernelEx(&cfg, choose_rows_kernel<true>, p)
+                                                     : cudaLaunchKernelEx(&cfg, choose_rows_kernel<false>, p);
 }
 
 cudaError_t launch_keep_rows(const KeepParams &p, cudaStream_t s) {

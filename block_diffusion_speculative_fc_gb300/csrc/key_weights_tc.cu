@@ -24,6 +24,7 @@
 #include <cuda.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "target_ops.h"
@@ -34,18 +35,19 @@ namespace {
 
 constexpr int KT = 128;                   // keys of a tile
 constexpr int CH = 128;                   // query rows of a product (of its columns)
-constexpr int QB = 256;                   // query rows held at a time
 constexpr int NBUF = 4;                   // products' results in TMEM, two a sum group
 constexpr int SUM_THREADS = 256, THREADS = SUM_THREADS + 64;
 constexpr int MAX_B = 1024;
 
-template <int D> struct Cfg {
+// QB: query rows held at a time
+template <int D, int QB> struct Cfg {
   static constexpr int TILE = KT * D * 2;
-  static constexpr int NSLOT = D == 128 ? 4 : 8;
+  static constexpr int NSLOT = (QB == 128 ? 5 : 4) * (D == 128 ? 1 : 2);
   static constexpr int Q_TILE = CH * D * 2;
   static constexpr int OFF_RING = (QB / CH) * Q_TILE;
   static constexpr int OFF_Z = OFF_RING + NSLOT * TILE;       // [QB] float
-  static constexpr int OFF_PLAN = OFF_Z + QB * 4;             // [MAX_B + 1] int64
+  static constexpr int OFF_COUNTS = OFF_Z + QB * 4;           // [QB / 32]
+  static constexpr int OFF_PLAN = OFF_COUNTS + QB / 8;        // [MAX_B + 1] int64
   static constexpr int OFF_BARS = OFF_PLAN + (MAX_B + 1) * 8;
   static constexpr int N_BARS = 2 * NSLOT + 2 * NBUF + 2;
   static constexpr int SMEM = 1024 + OFF_BARS + N_BARS * 8 + 16;
@@ -97,14 +99,15 @@ __device__ __forceinline__ bool reaches(const Run &u, bool masked, int G, int k0
   return masked || k0 - u.q.ctx <= min(last, u.rows - 1) / G;
 }
 
-template <int D>
+template <int D, int QB>
 __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, QB>;
   constexpr int NS = C::NSLOT, NB = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *ring = smem + C::OFF_RING;
-  float *s_z = (float *)(smem + C::OFF_Z);
+  float *s_z = (float *)(smem + C::OFF_Z);                    // what a row's exponents begin with
+  uint32_t *s_counts = (uint32_t *)(smem + C::OFF_COUNTS);    // rows that count
   long long *s_base = (long long *)(smem + C::OFF_PLAN);      // cost of the requests before
   uint64_t *full = (uint64_t *)(smem + C::OFF_BARS), *empty = full + NS;
   uint64_t *s_full = empty + NS, *s_free = s_full + NBUF, *q_full = s_free + NBUF, *done = q_full + 1;
@@ -202,17 +205,18 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
       const int *list = r.page_table + (int64_t)u.b * r.pages_per_req;
       const int keys = u.q.ctx + u.q.n, npages = (keys + kPageRows - 1) / kPageRows;
       for (int rb = 0; rb < u.blocks && ok; ++rb) {
-        int batch = 0;
+        auto pages_of = [&](int j) {       // of 16 tiles, one a lane
+          const int jj = j + (lane >> 1), pn = jj < u.j1 ? 2 * tile_of(u, jj) + (lane & 1) : npages;
+          return pn < npages ? __ldg(list + pn) : 0;
+        };
+        int ahead = pages_of(u.j0), batch = 0;
         for (int j = u.j0; j < u.j1 && ok; ++j) {
-          if ((j - u.j0) % 16 == 0) {      // pages of the next 16 tiles, one a lane
-            const int jj = j + (lane >> 1), pn = jj < u.j1 ? 2 * tile_of(u, jj) + (lane & 1) : npages;
-            batch = 0;
-            if (pn < npages) {
-              batch = __ldg(list + pn);
-              if (batch < 0 || batch >= r.n_pages) {
-                raise_error(a.err, DFLASH_DERR_PAGE_RANGE);
-                batch = 0;
-              }
+          if ((j - u.j0) % 16 == 0) {
+            batch = ahead;
+            ahead = pages_of(j + 16);
+            if (batch < 0 || batch >= r.n_pages) {
+              raise_error(a.err, DFLASH_DERR_PAGE_RANGE);
+              batch = 0;
             }
           }
           const int t = tile_of(u, j), i = (j - u.j0) % 16;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
         // the block's queries and what their exponents begin with; every product with the block
         // before has been read
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        {
+        if (tid < QB) {
           const int row = rb * QB + tid, tok = u.q.start + row / G, h = u.g * G + row % G;
           float z = -INFINITY;
           if (row < u.rows) {
@@ -308,13 +312,16 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
             if (isfinite(l) && w > 0.f && isfinite(w)) z = log2f(w) - l * 1.4426950408889634f;
           }
           s_z[tid] = z;
+          const uint32_t counts = __ballot_sync(0xffffffffu, z != -INFINITY);
+          if (lane == 0) s_counts[warp] = counts;
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const int held = min(QB, (u.rows - rb * QB + 31) / 32 * 32);
+#pragma unroll 8
         for (int i = tid; i < held * (D / 8); i += SUM_THREADS) {
           const int row = i / (D / 8), c = i % (D / 8), at_row = rb * QB + row;
           uint4 v = make_uint4(0, 0, 0, 0);    // rows that count for nothing
-          if (s_z[row] != -INFINITY)
+          if (s_counts[row >> 5] >> (row & 31) & 1u)
             v = *(reinterpret_cast<const uint4 *>((const bf16 *)a.q + (int64_t)(u.q.start + at_row / G) * a.q_stride +
                                                   (int64_t)(u.g * G + at_row % G) * D) + c);
           const int in = row & (CH - 1);
@@ -323,14 +330,28 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
         }
         fence_async_smem();
         mbar_arrive(q_full);
-        for (int j = u.j0; j < u.j1; ++j) {
-          if ((j & 1) != x || !ok) continue;
-          const int k0 = tile_of(u, j) * KT, key = k0 + key_lane;
-          if (!reaches(u, masked, G, k0, rb * QB + QB - 1)) continue;
-          const bool begins = rb == 0 || !reaches(u, masked, G, k0, rb * QB - 1);
-          const bool live = key < u.q.ctx + u.q.n;
+        const int keys = u.q.ctx + u.q.n;
+        auto begins = [&](int k0) { return rb == 0 || !reaches(u, masked, G, k0, rb * QB - 1); };
+        // what the sum of tile j's key is added to (loaded a tile ahead)
+        auto read_old = [&](int j) {
           float old = 0.f;
-          if (live && (begins ? key < u.q.ctx && a.decay != 0.f : true)) old = out[key];
+          if (j < u.j1) {
+            const int k0 = tile_of(u, j) * KT, key = k0 + key_lane;
+            if (reaches(u, masked, G, k0, rb * QB + QB - 1) && key < keys &&
+                (begins(k0) ? key < u.q.ctx && a.decay != 0.f : true))
+              old = out[key];
+          }
+          return old;
+        };
+        const int first = u.j0 + ((u.j0 ^ x) & 1);
+        float next_old = read_old(first);
+        for (int j = first; j < u.j1; j += 2) {
+          const float old = next_old;
+          next_old = read_old(j + 2);
+          const int k0 = tile_of(u, j) * KT, key = k0 + key_lane;
+          if (!ok || !reaches(u, masked, G, k0, rb * QB + QB - 1)) continue;
+          const bool live = key < keys;
+          const int num = key - u.q.ctx;       // among the new rows
           float sum = 0.f;
           for (int ch = 0; ch < QB / CH; ++ch) {
             const int row0 = rb * QB + ch * CH;
@@ -343,64 +364,84 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
             tc_fence_after();
             const uint32_t t_s = tmem + lanes + buf * CH;
             const float *z = s_z + ch * CH;
+            const uint32_t *counts = s_counts + ch * (CH / 32);
+            // columns c .. c+31 whose row sees this key
+            auto sees = [&](int c) {
+              const int r0 = row0 + c;
+              if (num < 0 || !live) return 0xffffffffu;
+              if (!masked) {
+                const int64_t from = (int64_t)num * G - r0;
+                return from <= 0 ? 0xffffffffu : from >= 32 ? 0u : 0xffffffffu << from;
+              }
+              uint32_t cols = 0;
+              int tok = r0 / G;
+              for (int at = tok * G - r0; at < 32 && tok < u.q.n; at += G, ++tok)
+                if (__ldg(a.mask + (int64_t)(u.q.start + tok) * a.mask_words + (num >> 5)) >> (num & 31) & 1u) {
+                  const uint32_t upto = at + G >= 32 ? 0xffffffffu : (1u << (at + G)) - 1u;
+                  cols |= upto & (at > 0 ? 0xffffffffu << at : 0xffffffffu);
+                }
+              return cols;
+            };
+            const float2 c2 = make_float2(p.c, p.c);
+            float2 s0, s1;
+            // a piece's terms; with SELECT those of `cols` alone
+            auto add = [&](const uint32_t *v, const float *zz, uint32_t cols, auto select) {
+              constexpr bool SELECT = decltype(select)::value;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 z4 = *reinterpret_cast<const float4 *>(zz + i);
+                const float2 e0 = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2,
+                                       make_float2(z4.x, z4.y));
+                const float2 e1 = fma2(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2,
+                                       make_float2(z4.z, z4.w));
+                float2 w0 = make_float2(ex2(e0.x), ex2(e0.y)), w1 = make_float2(ex2(e1.x), ex2(e1.y));
+                if (SELECT) {
+                  w0.x = cols >> i & 1u ? w0.x : 0.f;
+                  w0.y = cols >> (i + 1) & 1u ? w0.y : 0.f;
+                  w1.x = cols >> (i + 2) & 1u ? w1.x : 0.f;
+                  w1.y = cols >> (i + 3) & 1u ? w1.y : 0.f;
+                }
+                s0 = add2(s0, w0);
+                s1 = add2(s1, w1);
+              }
+            };
             // every row of the product sees every key of the tile
             const bool whole = k0 + KT <= u.q.ctx || (!masked && k0 + KT - 1 - u.q.ctx <= row0 / G);
-            float part = 0.f;
-            if (whole) {
-              const float2 c2 = make_float2(p.c, p.c);
-              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-              auto add = [&](const uint32_t *v, const float *zz, int n) {
-#pragma unroll
-                for (int i = 0; i < n; i += 4) {
-                  const float4 z4 = *reinterpret_cast<const float4 *>(zz + i);
-                  const float2 e0 = fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), c2,
-                                         make_float2(z4.x, z4.y));
-                  const float2 e1 = fma2(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), c2,
-                                         make_float2(z4.z, z4.w));
-                  s0 = add2(s0, make_float2(ex2(e0.x), ex2(e0.y)));
-                  s1 = add2(s1, make_float2(ex2(e1.x), ex2(e1.y)));
-                }
-              };
-              uint32_t v[32];
-              if (rows <= 16) {
-                tmem_ld16(t_s, v);
-                tmem_ld_wait();
-                add(v, z, 16);
-              } else {
-                for (int i = 0; i < rows; i += 32) {
-                  tmem_ld32(t_s + i, v);
-                  tmem_ld_wait();
-                  add(v, z + i, 32);
-                }
-              }
-              part = (s0.x + s0.y) + (s1.x + s1.y);
-            }
-            // Row by row, where rows see some of the keys, or where a row that counts for nothing has
+            // Terms one by one where rows see some of the keys, or where a row that counts for nothing has
             // met a key that is not finite.
-            if (!whole || __any_sync(0xffffffffu, live && isnan(part))) {
-              part = 0.f;
-              const int num = key - u.q.ctx;     // among the new rows
-              for (int i = 0; i < rows; i += 16) {
-                uint32_t v[16];
-                tmem_ld16(t_s + i, v);
-                tmem_ld_wait();
+            auto pass = [&](auto select) {
+              s0 = s1 = make_float2(0.f, 0.f);
+              uint32_t v0[32], v1[32];
+              auto cols = [&](int c) { return decltype(select)::value ? counts[c >> 5] & (whole ? 0xffffffffu : sees(c)) : 0u; };
+              if (rows <= 16) {
+                tmem_ld16(t_s, v0);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  if (i + e >= rows) continue;
-                  const int tok = (row0 + i + e) / G;
-                  bool sees = num < 0 || whole || !masked && num <= tok;
-                  if (!whole && masked && num >= 0 && live)
-                    sees = a.mask[(int64_t)(u.q.start + tok) * a.mask_words + (num >> 5)] >> (num & 31) & 1u;
-                  const float w = ex2(fmaf(__uint_as_float(v[e]), p.c, z[i + e]));
-                  if (sees && z[i + e] != -INFINITY) part += w;
+                for (int i = 16; i < 32; ++i) v0[i] = 0;         // (beyond the rows: weigh 0)
+                tmem_ld_wait32(v0);
+                add(v0, z, cols(0), select);
+              } else {
+                tmem_ld32(t_s, v0);
+                for (int i = 0; i < rows; i += 64) {             // the next piece is on its way
+                  tmem_ld_wait32(v0);
+                  if (i + 32 < rows) tmem_ld32(t_s + i + 32, v1);
+                  add(v0, z + i, cols(i), select);
+                  if (i + 32 < rows) {
+                    tmem_ld_wait32(v1);
+                    if (i + 64 < rows) tmem_ld32(t_s + i + 64, v0);
+                    add(v1, z + i + 32, cols(i + 32), select);
+                  }
                 }
               }
-            }
+              return (s0.x + s0.y) + (s1.x + s1.y);
+            };
+            float part = 0.f;
+            if (whole) part = pass(std::false_type());
+            if (!whole || __any_sync(0xffffffffu, live && isnan(part))) part = pass(std::true_type());
             sum += part;
             tc_fence_before();
             mbar_arrive(&s_free[buf]);
           }
-          if (live && ok) out[key] = (begins ? old * a.decay : old) + sum;
+          if (live && ok) out[key] = (begins(k0) ? old * a.decay : old) + sum;
         }
       }
     }
@@ -415,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, 1) key_weights_kernel(const __grid_co
   }
 }
 
-template <int D> cudaError_t launch(const KeyWeightParams &a, cudaStream_t s) {
+template <int D, int QB> cudaError_t launch(const KeyWeightParams &a, cudaStream_t s) {
   Params p;
   memset(&p, 0, sizeof(p));
   if (!encode_pages(&p.tmK, a.k_pages, a.rows.n_pages, a.KVH, D)) return cudaErrorInvalidValue;
@@ -424,7 +465,15 @@ template <int D> cudaError_t launch(const KeyWeightParams &a, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   p.a = a;
   p.c = a.scale * 1.4426950408889634f;
-  return launch_pdl(key_weights_kernel<D>, dim3(sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
+  return launch_pdl(key_weights_kernel<D, QB>, dim3(sms), dim3(THREADS), Cfg<D, QB>::SMEM, s, p);
+}
+template <int D, int QB> cudaError_t prepare() {
+  return cudaFuncSetAttribute(key_weights_kernel<D, QB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<D, QB>::SMEM);
+}
+template <int D> cudaError_t launch(const KeyWeightParams &a, cudaStream_t s) {
+  const bool few = (int64_t)a.rows.total_rows * (a.H / a.KVH) <= 128LL * a.rows.B;
+  return few ? launch<D, 128>(a, s) : launch<D, 256>(a, s);
 }
 
 }  // namespace
@@ -434,11 +483,10 @@ cudaError_t launch_key_weights_tc(const KeyWeightParams &p, cudaStream_t s) {
 }
 
 cudaError_t prepare_key_weights_tc() {
-  const cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Cfg<64>::SMEM);
-  return e == cudaSuccess ? cudaFuncSetAttribute(key_weights_kernel<128>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::SMEM)
-                          : e;
+  cudaError_t e = prepare<64, 128>();
+  if (e == cudaSuccess) e = prepare<64, 256>();
+  if (e == cudaSuccess) e = prepare<128, 128>();
+  return e == cudaSuccess ? prepare<128, 256>() : e;
 }
 
 }  // namespace dflash
