@@ -232,7 +232,7 @@ __device__ __forceinline__ void move_rows(uint4 *pages, const int *table, const 
 }
 
 template <int LANES>
-__global__ void __launch_bounds__(KEEP_THREADS) keep_rows_kernel(const __grid_constant__ KeepParams p) {
+__global__ void __launch_bounds__(KEEP_THREADS, 4) keep_rows_kernel(const __grid_constant__ KeepParams p) {
   const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x, part = blockIdx.x;
   const int chunks = p.row_bytes / 16, slices = chunks / LANES;
   const bool reports = part == 0 && tid == 0;
@@ -299,9 +299,12 @@ template <int LANES> cudaError_t launch_keep(const KeepParams &p, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t lists = (int64_t)p.B * p.KVH;
   int C = 1;
-  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width) C *= 2;
+  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width && lists * C <= sms) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(lists * C));
   cfg.blockDim = dim3(CHOOSE_THREADS);

@@ -414,6 +414,8 @@ int dflash_key_weights(dflash_handle *h, const dflash_layer_kv *kv, int32_t batc
   if (int st = check_layer(kv, batch, total_rows)) return st;
   if (int st = check_mask(mask, mask_words)) return st;
   if (std::isnan(scale) || std::isinf(scale)) return fail(DFLASH_EINVAL, "scale must be finite");
+  if (scale != 0.f && (std::fabs(scale) < 0x1p-100f || std::fabs(scale) > 0x1p100f))
+    return fail(DFLASH_EUNSUPPORTED, "scale must be 0 or of magnitude 2^-100 to 2^100");
   if (!(decay >= 0.f && decay <= 1.f)) return fail(DFLASH_EINVAL, "decay must be 0 to 1");
   if (width <= 0) return fail(DFLASH_EINVAL, "width must be positive");
   const bool empty = batch == 0 || total_rows == 0;

@@ -771,7 +771,7 @@ int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_row
  * over the request's new rows t that see row p; rows of this call itself (p from
  * kv_len[b] - prefix_len on) begin at 0, and with decay 0 nothing is read of the old.
  *   row_start, kv_len, mask, mask_words, q, scale: as for dflash_tree_attention,
- *              which gives lse
+ *              which gives lse; scale 0 or of magnitude 2^-100 to 2^100
  *   row_weight optional device float32 [total_rows] (NULL: 1), such as the accepted
  *              rows' of dflash_accept_commit_tree
  *   decay      0 to 1

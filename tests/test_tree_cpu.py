@@ -104,6 +104,10 @@ def test_sizes(handle):  # noqa: F811
     for most in (0, -1, 1025):
         refused(-2, accept, handle, most=most)
     refused(-1, accept, handle, ids=FAKE, stride=0)
+    refused(-2, weigh, handle, scale=2.0 ** -101)
+    refused(-2, weigh, handle, scale=-2.0 ** 101)
+    for scale in (0.0, 2.0 ** -100, -2.0 ** 100):
+        refused(-6, weigh, handle, scale=scale)
     for bad in [dict(decay=-0.1), dict(decay=1.1), dict(decay=math.nan), dict(width=0)]:
         refused(-1, weigh, handle, **bad)
     for bad in [dict(width=0), dict(most=0), dict(first=-1), dict(last=-1)]:
