@@ -46,8 +46,7 @@ template <int D, int QB> struct Cfg {
   static constexpr int PC = QB < 256 ? QB : 256, HALVES = PC / 128;
   static constexpr int PER_SM = QB == 128 ? 2 : 1;            // CTAs
   static constexpr int NSLOT = 2 * (D == 128 ? 1 : 2);
-  static constexpr int ISSUERS = QB == 128 ? 1 : NG;          // warps that issue MMAs
-  static constexpr int GROUP = 128 * HALVES, SUM_THREADS = NG * GROUP, THREADS = SUM_THREADS + 32 + 32 * ISSUERS;
+  static constexpr int GROUP = 128 * HALVES, SUM_THREADS = NG * GROUP, THREADS = SUM_THREADS + 64;
   static constexpr int OFF_RING = QB * D * 2;
   static constexpr int OFF_ONES = OFF_RING + NSLOT * TILE;    // [KT][16] bf16
   static constexpr int OFF_Z = OFF_ONES + KT * 32;            // [QB][16] bf16
@@ -150,7 +149,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
       mbar_init(&parts[2 * i + 1], 128);
     }
     mbar_init(q_full, C::SUM_THREADS);
-    mbar_init(done, C::ISSUERS);
+    mbar_init(done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == ISSUER) {
@@ -302,10 +301,10 @@ key_weights_kernel(const __grid_constant__ Params p) {
         mbar_wait(&full[v % NS], (v / NS) & 1);
     }
   } else if (warp >= ISSUER) {
-    // -------------------------------------------------------------- MMA issuers
-    // The issue of a product's MMAs takes as long as the tensor cores do, the waits and addresses
-    // before it some 500 clocks more: an issuer a group where products bound the call.
-    const int own = warp - ISSUER;         // group, of all where there is one issuer
+    // -------------------------------------------------------------- MMA issuer
+    // Two tiles at a time, a group's each: their first products, then their second ones.  So the groups
+    // stay out of phase, one's sums run while the other's product does.  (With an issuer a group they
+    // fell into step and waited for each other's products: windows 60 us.)
     if (lane == 0) {
       const uint64_t k_desc = desc_k(su32(ring)), q_desc = desc_k(su32(smem));
       const uint64_t ones_desc = desc_plain(su32(s_ones), 128, 256), z_desc = desc_plain(su32(s_z), 128, 256);
@@ -316,30 +315,32 @@ key_weights_kernel(const __grid_constant__ Params p) {
           const Limits lim(u, masked, G, rb * QB, QB);
           const int rows = min(QB, u.rows - rb * QB), products = (rows + PC - 1) / PC;
           ok = mbar_wait(q_full, n_q++ & 1);
-          for (int j = u.j0; j < u.j1 && ok; ++j) {
-            if (tile_of(u, j) * KT > lim.block) continue;
-            const uint32_t slot = n_tile % NS, phase = (n_tile / NS) & 1;
-            ++n_tile;
-            const int x = j % NG;
-            if (C::ISSUERS > 1 && x != own) continue;
-            ok = mbar_wait(&full[slot], phase);
-            const uint64_t kd = k_desc + slot * (C::TILE >> 4);
-            for (int pr = 0; pr < products && ok; ++pr) {
+          for (int j0 = u.j0 & ~1; j0 < u.j1 && ok; j0 += 2) {
+            const bool has0 = j0 >= u.j0 && tile_of(u, j0) * KT <= lim.block;
+            const bool has1 = j0 + 1 < u.j1 && tile_of(u, j0 + 1) * KT <= lim.block;
+            for (int pr = 0; pr < products; ++pr) {
               const int cols = min(PC, rows - pr * PC);
               const uint32_t id = idesc(128, cols <= 16 ? 16 : (cols + 31) / 32 * 32, false);
-              const uint64_t qd = q_desc + pr * ((PC * D * 2) >> 4);
-              ok = mbar_wait(&s_free[x], (parity >> x & 1) ^ 1);
-              parity ^= 1u << x;
-              if (!ok) break;
-              tc_fence_after();
+              const uint64_t qd = q_desc + pr * ((PC * D * 2) >> 4), zd = z_desc + pr * ((PC * 32) >> 4);
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                umma_ss(tmem + x * PC, kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3),
-                        qd + (i >> 2) * ((PC * 128) >> 4) + 2 * (i & 3), id, i ? 1u : 0u);
-              umma_ss(tmem + x * PC, ones_desc, z_desc + pr * ((PC * 32) >> 4), id, 1u);
-              umma_commit(&s_full[x]);
+              for (int x = 0; x < NG; ++x) {
+                if (!(x ? has1 : has0) || !ok) continue;
+                const uint32_t tile = n_tile + (x && has0 ? 1 : 0), slot = tile % NS;
+                const uint64_t kd = k_desc + slot * (C::TILE >> 4);
+                ok = mbar_wait(&full[slot], (tile / NS) & 1) && mbar_wait(&s_free[x], (parity >> x & 1) ^ 1);
+                parity ^= 1u << x;
+                if (!ok) continue;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                  umma_ss(tmem + x * PC, kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3),
+                          qd + (i >> 2) * ((PC * 128) >> 4) + 2 * (i & 3), id, i ? 1u : 0u);
+                umma_ss(tmem + x * PC, ones_desc, zd, id, 1u);
+                umma_commit(&s_full[x]);
+                if (pr == products - 1) umma_commit(&empty[slot]);
+              }
             }
-            umma_commit(&empty[slot]);
+            n_tile += has0 + has1;
           }
         }
       }
