@@ -27,19 +27,24 @@ constexpr int CHOOSE_THREADS = 512, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 2
 constexpr int E = 16;                     // weights of a thread and step
 constexpr int STEP = 32 * E;              // of a warp
 constexpr int MAXC = 8;
+constexpr int LIST = 4096;                // rows near the cut that are told apart in a list
+constexpr int PER = LIST / CHOOSE_THREADS;
 
 // larger image: larger weight; NaN as -infinity, -0 as 0
 __device__ __forceinline__ uint32_t order_image(float v) {
-  if (isnan(v)) v = -INFINITY;
-  const uint32_t u = __float_as_uint(v + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(v + 0.f), x = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+  return x > 0xff800000u ? 0x007fffffu : max(x, 0x007fffffu);
 }
 
 // HELD: a warp's rows are one step, whose images stay in registers; else they are read again in each pass.
 template <bool HELD>
 __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __grid_constant__ ChooseParams p) {
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
-  __shared__ int s_warp[2][CHOOSE_WARPS], s_bin, s_above, s_count, s_total[2];
+  __shared__ uint32_t s_list[LIST];
+  __shared__ uint8_t s_from[LIST];                              // warp of the cluster that listed a row
+  __shared__ int s_warp[2][CHOOSE_WARPS], s_of[2][MAXC * CHOOSE_WARPS], s_total[2];
+  __shared__ int s_bin, s_above, s_count, s_listed, s_need;
+  __shared__ uint32_t s_cut;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -61,9 +66,13 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
   }
   const float *w = p.weights + (int64_t)list * p.width;
   const int a = min(p.first, keep), z = min(p.last, keep - a), m = keep - a - z;
-  // a warp's rows: a run of consecutive ones, whole steps of 32
-  const int run = (int)(((int64_t)n + C * CHOOSE_WARPS * 32 - 1) / (C * CHOOSE_WARPS * 32)) * 32;
-  const int w0 = (int)min((int64_t)n, (int64_t)(rank * CHOOSE_WARPS + warp) * run), w1 = min(n - w0, run) + w0;
+  for (int i = rank * CHOOSE_THREADS + tid; i < a + z; i += C * CHOOSE_THREADS)
+    rows[i < a ? i : m + i] = i < a ? i : n - z + (i - a);
+  if (m == 0) return;
+  // a warp's rows: a run of those between, whole steps of 32
+  const int M = n - a - z, id = rank * CHOOSE_WARPS + warp;
+  const int run = (int)(((int64_t)M + C * CHOOSE_WARPS * 32 - 1) / (C * CHOOSE_WARPS * 32)) * 32;
+  const int w0 = a + (int)min((int64_t)M, (int64_t)id * run), w1 = min(n - z - w0, run) + w0;
   uint32_t u[E];
   auto load = [&](int i0) {
 #pragma unroll
@@ -88,19 +97,26 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
     }
   };
   if (HELD) load(w0);
-  // ---- the cut: the m-th largest image of rows a .. n-z-1, as far down as it takes to tell rows apart
-  uint32_t cut = 0;                       // its high bits
-  int need = m, shift = 32;               // how many of the rows that agree with them are taken; the bits below
-  for (int pass = 0; pass < 3 && m > 0; ++pass) {
-    const int above_bits = shift, bits = pass == 2 ? 10 : 11;
+  // ---- the cut, the m-th largest image: as many of its high bits as it takes to leave few rows
+  uint32_t cut = 0;                       // those bits
+  int need = m, count = M, shift = 32;    // of the rows that agree with them, how many are taken; the bits below
+  if (tid == 0) s_listed = 0;
+  for (int i = tid; i < 2 * MAXC * CHOOSE_WARPS; i += CHOOSE_THREADS) (&s_of[0][0])[i] = 0;
+  for (int pass = 0; pass < 3 && need < count && (pass == 0 || count > LIST); ++pass) {
+    const int upper = shift, bits = pass == 2 ? 10 : 11;
     uint32_t *hist = s_hist[pass & 1];
-    for (int i = tid; i < BINS; i += CHOOSE_THREADS) hist[i] = 0;
+    reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     shift -= bits;
-    each([&](int i, uint32_t x, bool live) {
-      if (live && i >= a && i < n - z && (pass == 0 || x >> above_bits == cut))
-        atomicAdd(&hist[x >> shift & ((1u << bits) - 1)], 1u);
-    });
+    const uint32_t mask = (1u << bits) - 1;
+    if (pass == 0)
+      each([&](int, uint32_t x, bool live) {
+        if (live) atomicAdd(&hist[x >> 21], 1u);
+      });
+    else
+      each([&](int, uint32_t x, bool live) {
+        if (live && x >> upper == cut) atomicAdd(&hist[x >> shift & mask], 1u);
+      });
     cl.sync();
     // bins from the top, four a thread: counts of all CTAs, those above, and the bin that holds the cut
     uint4 c = make_uint4(0, 0, 0, 0);
@@ -133,16 +149,80 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
     __syncthreads();
     cut = cut << bits | (uint32_t)s_bin;
     need -= s_above;
-    if (need == s_count) break;           // all of them are taken
+    count = s_count;
+  }
+  // ---- rows above the cut's bits, by warp; those that agree with them are all taken, or all alike, or
+  // go to a list
+  const bool listed = need < count && shift > 0;
+  int above = 0, equal = 0;
+  each([&](int, uint32_t x, bool live) {
+    const uint32_t high = x >> shift;
+    above += __popc(__ballot_sync(0xffffffffu, live && high > cut));
+    const bool eq = live && high == cut;
+    const uint32_t be = __ballot_sync(0xffffffffu, eq);
+    if (!listed) {
+      equal += __popc(be);
+    } else if (be) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_listed, __popc(be));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(be & ((1u << lane) - 1));
+      if (eq) {
+        s_list[at] = x;
+        s_from[at] = (uint8_t)id;
+      }
+    }
+  });
+  if (listed) {
+    cl.sync();
+    if (rank == 0) {
+      // the cluster's lists, PER rows a thread, and their cut bit by bit
+      uint32_t x[PER];
+      int from[PER], total = 0;
+      for (int k = 0; k < C; ++k) total += *cl.map_shared_rank(&s_listed, k);
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        int at = j * CHOOSE_THREADS + tid, k = 0;
+        from[j] = -1;
+        x[j] = 0;
+        if (at < total) {
+          for (int c = *cl.map_shared_rank(&s_listed, 0); at >= c; c = *cl.map_shared_rank(&s_listed, k)) {
+            at -= c;
+            ++k;
+          }
+          x[j] = cl.map_shared_rank(s_list, k)[at];
+          from[j] = cl.map_shared_rank(s_from, k)[at];
+        }
+      }
+      cut <<= shift;
+      int more = 0;                       // rows above the bits tried last that were enough
+      for (int bit = shift - 1, turn = 0; bit >= 0; --bit, turn ^= 1) {
+        const uint32_t tried = cut | 1u << bit;
+        int some = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) some += x[j] >= tried;
+        some = __reduce_add_sync(0xffffffffu, some);
+        if (lane == 0) s_warp[turn][warp] = some;
+        __syncthreads();
+        some = __reduce_add_sync(0xffffffffu, lane < CHOOSE_WARPS ? s_warp[turn][lane] : 0);
+        if (some >= need) cut = tried;
+        else more = some;                 // (the fewest tried: those above the final cut)
+      }
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (from[j] >= 0 && x[j] >= cut) atomicAdd(&s_of[x[j] > cut ? 0 : 1][from[j]], 1);
+      if (tid == 0) {
+        s_cut = cut;
+        s_need = need - more;
+      }
+    }
+    cl.sync();
+    cut = *cl.map_shared_rank(&s_cut, 0);
+    need = *cl.map_shared_rank(&s_need, 0);
+    above += *cl.map_shared_rank(&s_of[0][id], 0);
+    equal = *cl.map_shared_rank(&s_of[1][id], 0);
+    shift = 0;
   }
   // ---- places
-  auto above_cut = [&](int i, uint32_t x) { return i < a || i >= n - z || (m > 0 && x >> shift > cut); };
-  auto at_cut = [&](int i, uint32_t x) { return i >= a && i < n - z && m > 0 && x >> shift == cut; };
-  int above = 0, equal = 0;
-  each([&](int i, uint32_t x, bool live) {
-    above += __popc(__ballot_sync(0xffffffffu, live && above_cut(i, x)));
-    equal += __popc(__ballot_sync(0xffffffffu, live && at_cut(i, x)));
-  });
   __syncthreads();
   if (lane == 0) {
     s_warp[0][warp] = above;
@@ -156,16 +236,18 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
     s_total[1] = equal + s_warp[1][warp];
   }
   cl.sync();
+  above += a;
   for (int k = 0; k < rank; ++k) {
     above += *cl.map_shared_rank(&s_total[0], k);
     equal += *cl.map_shared_rank(&s_total[1], k);
   }
   const uint32_t before = (1u << lane) - 1;
   each([&](int i, uint32_t x, bool live) {
-    const bool is_above = live && above_cut(i, x), is_equal = live && at_cut(i, x);
+    const uint32_t high = x >> shift;
+    const bool is_above = live && high > cut, is_equal = live && high == cut;
     const uint32_t ba = __ballot_sync(0xffffffffu, is_above), be = __ballot_sync(0xffffffffu, is_equal);
-    const int eq = equal + __popc(be & before);
-    if (is_above || (is_equal && eq < need)) rows[above + __popc(ba & before) + min(eq, need)] = i;
+    if (is_above) rows[above + __popc(ba & before) + min(equal + __popc(be & before), need)] = i;
+    else if (is_equal && equal + __popc(be & before) < need) rows[above + __popc(ba & before) + equal + __popc(be & before)] = i;
     above += __popc(ba);
     equal += __popc(be);
   });
@@ -175,59 +257,57 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
 // ------------------------------------------------------------------ keep
 constexpr int KEEP_THREADS = 256, UNITS = 4;
 
-// A slice of 16 LANES bytes of the listed rows, UNITS rows a thread and step.  A step's rows are loaded
-// while the step before is stored (sources of later steps lie behind its places), and their slots are
-// looked up a step earlier still: list, page and row are three loads that wait for one another.
+// A slice of 16 LANES bytes of the listed rows, UNITS rows a thread and step.  List, page and row are three
+// loads that wait for one another, so they are three steps, two and one ahead of the store (sources of
+// later steps lie behind the places of this one).
 template <int LANES>
 __device__ __forceinline__ void move_rows(uint4 *pages, const int *table, const int *list, int count, int own,
                                           int64_t row_step, int lane16) {
   // pages: head g of cache row 0; row_step: 16-byte chunks from one cache row to the next
   constexpr int RP = KEEP_THREADS / LANES, ROWS = RP * UNITS;
   const int r = threadIdx.x / LANES, c = threadIdx.x % LANES + lane16;
-  struct Step {
-    int from[UNITS], to[UNITS];            // slots; -1: stays where it is
-  };
-  auto look_up = [&](int i0, Step &s) {
-    int src[UNITS];
+  int src[UNITS], from[UNITS], to[UNITS], old_to[UNITS];       // rows; slots (-1: stays where it is)
+  uint4 v[UNITS], old[UNITS];
+  auto look_up = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int i = i0 + u * RP + r;
       src[u] = i < count ? __ldg(list + i) : i;
     }
+  };
+  auto find = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int i = i0 + u * RP + r, f = own + src[u], t = own + i;
-      s.from[u] = s.to[u] = -1;
+      from[u] = to[u] = -1;
       if (src[u] != i) {
-        s.from[u] = __ldg(table + f / kPageRows) * kPageRows + f % kPageRows;
-        s.to[u] = __ldg(table + t / kPageRows) * kPageRows + t % kPageRows;
+        from[u] = __ldg(table + f / kPageRows) * kPageRows + f % kPageRows;
+        to[u] = __ldg(table + t / kPageRows) * kPageRows + t % kPageRows;
       }
     }
   };
-  auto load = [&](const Step &s, uint4 *v) {
+  auto load = [&] {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-      if (s.from[u] >= 0) v[u] = pages[s.from[u] * row_step + c];
+      if (from[u] >= 0) v[u] = pages[from[u] * row_step + c];
   };
-  auto store = [&](const Step &s, const uint4 *v) {
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-      if (s.to[u] >= 0) pages[s.to[u] * row_step + c] = v[u];
-  };
-  Step s0, s1, s2;
-  uint4 v0[UNITS], v1[UNITS];
-  look_up(0, s0);
-  look_up(ROWS, s1);
-  load(s0, v0);
+  look_up(0);
+  find(0);
+  look_up(ROWS);
+  load();
   for (int i0 = 0; i0 < count; i0 += ROWS) {
-    load(s1, v1);
-    look_up(i0 + 2 * ROWS, s2);
-    __syncthreads();                       // the rows of this step are loaded
-    store(s0, v0);
-    s0 = s1;
-    s1 = s2;
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) v0[u] = v1[u];
+    for (int u = 0; u < UNITS; ++u) {
+      old[u] = v[u];
+      old_to[u] = to[u];
+    }
+    find(i0 + ROWS);
+    look_up(i0 + 2 * ROWS);
+    __syncthreads();                       // the rows of this step are loaded
+    load();
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+      if (old_to[u] >= 0) pages[old_to[u] * row_step + c] = old[u];
   }
 }
 
@@ -304,7 +384,7 @@ cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t lists = (int64_t)p.B * p.KVH;
   int C = 1;
-  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width && lists * C <= sms) C *= 2;
+  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width && lists * C < 2 * sms) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(lists * C));
   cfg.blockDim = dim3(CHOOSE_THREADS);
