@@ -160,6 +160,7 @@ cudaError_t prepare_kernels() {
   if (e == cudaSuccess) e = prepare_tree();
   if (e == cudaSuccess) e = prepare_key_weights_tc();
   if (e == cudaSuccess) e = prepare_key_weights_simt();
+  if (e == cudaSuccess) e = prepare_choose_rows();
   return e;
 }
 

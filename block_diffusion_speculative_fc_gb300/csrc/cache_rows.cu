@@ -24,9 +24,8 @@ namespace cg = cooperative_groups;
 
 // ------------------------------------------------------------------ choose
 constexpr int CHOOSE_THREADS = 512, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 2048;
-constexpr int E = 16;                     // weights of a thread and step
-constexpr int STEP = 32 * E;              // of a warp
 constexpr int MAXC = 8;
+constexpr int MOST_HELD = 16384;          // weights that a CTA holds in shared memory
 constexpr int LIST = 4096;                // rows near the cut that are told apart in a list
 constexpr int PER = LIST / CHOOSE_THREADS;
 
@@ -36,9 +35,10 @@ __device__ __forceinline__ uint32_t order_image(float v) {
   return x > 0xff800000u ? 0x007fffffu : max(x, 0x007fffffu);
 }
 
-// HELD: a warp's rows are one step, whose images stay in registers; else they are read again in each pass.
+// HELD: the images of a CTA's rows stay in shared memory; else the weights are read again in each pass.
 template <bool HELD>
-__global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __grid_constant__ ChooseParams p) {
+__global__ void __launch_bounds__(CHOOSE_THREADS, 3) choose_rows_kernel(const __grid_constant__ ChooseParams p) {
+  extern __shared__ uint32_t s_image[];                         // [rows of the CTA], a warp's after another's
   __shared__ __align__(16) uint32_t s_hist[2][BINS];
   __shared__ uint32_t s_list[LIST];
   __shared__ uint8_t s_from[LIST];                              // warp of the cluster that listed a row
@@ -73,55 +73,30 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
   const int M = n - a - z, id = rank * CHOOSE_WARPS + warp;
   const int run = (int)(((int64_t)M + C * CHOOSE_WARPS * 32 - 1) / (C * CHOOSE_WARPS * 32)) * 32;
   const int w0 = a + (int)min((int64_t)M, (int64_t)id * run), w1 = min(n - z - w0, run) + w0;
-  uint32_t u[E];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = i0 + 32 * e + lane;
-      u[e] = i < w1 ? order_image(w[i]) : 0u;
-    }
-  };
+  uint32_t *held = s_image + warp * run;
   // f(row, its image, whether there is one) for all of the warp's rows, in order
-  auto each = [&](auto f) {
-    if (HELD) {
+  auto each = [&](auto read, auto f) {
+    constexpr int U = 8;
+    int i0 = w0;
+    for (; i0 + 32 * U <= w1; i0 += 32 * U) {
+      uint32_t x[U];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (w0 + 32 * e < w1) f(w0 + 32 * e + lane, u[e], w0 + 32 * e + lane < w1);
-    } else {
-      for (int i0 = w0; i0 < w1; i0 += STEP) {
-        load(i0);
+      for (int e = 0; e < U; ++e) x[e] = read(i0 + 32 * e + lane);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (i0 + 32 * e < w1) f(i0 + 32 * e + lane, u[e], i0 + 32 * e + lane < w1);
-      }
+      for (int e = 0; e < U; ++e) f(i0 + 32 * e + lane, x[e], true);
+    }
+    for (; i0 < w1; i0 += 32) {
+      const int i = i0 + lane;
+      f(i, i < w1 ? read(i) : 0u, i < w1);
     }
   };
-  if (HELD) load(w0);
-  // ---- the cut, the m-th largest image: as many of its high bits as it takes to leave few rows
-  uint32_t cut = 0;                       // those bits
-  int need = m, count = M, shift = 32;    // of the rows that agree with them, how many are taken; the bits below
-  if (tid == 0) s_listed = 0;
-  for (int i = tid; i < 2 * MAXC * CHOOSE_WARPS; i += CHOOSE_THREADS) (&s_of[0][0])[i] = 0;
-  for (int pass = 0; pass < 3 && need < count && (pass == 0 || count > LIST); ++pass) {
-    const int upper = shift, bits = pass == 2 ? 10 : 11;
-    uint32_t *hist = s_hist[pass & 1];
-    reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    shift -= bits;
-    const uint32_t mask = (1u << bits) - 1;
-    if (pass == 0)
-      each([&](int, uint32_t x, bool live) {
-        if (live) atomicAdd(&hist[x >> 21], 1u);
-      });
-    else
-      each([&](int, uint32_t x, bool live) {
-        if (live && x >> upper == cut) atomicAdd(&hist[x >> shift & mask], 1u);
-      });
-    cl.sync();
-    // bins from the top, four a thread: counts of all CTAs, those above, and the bin that holds the cut
-    uint4 c = make_uint4(0, 0, 0, 0);
-    for (int k = 0; k < C; ++k) {
-      const uint4 h = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, k))[BINS / 4 - 1 - tid];
+  auto from_weights = [&](int i) { return order_image(w[i]); };
+  auto image = [&](int i) { return HELD ? held[i - w0] : order_image(w[i]); };
+  // the bin from the top where the counts reach `need`: it, those above it, those in it (all threads)
+  auto find_bin = [&](uint32_t *hist, int ranks, int need) {
+    uint4 c = make_uint4(0, 0, 0, 0);      // four bins a thread
+    for (int k = 0; k < ranks; ++k) {
+      const uint4 h = reinterpret_cast<const uint4 *>(cl.map_shared_rank(hist, ranks > 1 ? k : rank))[BINS / 4 - 1 - tid];
       c.x += h.w, c.y += h.z, c.z += h.y, c.w += h.x;
     }
     const int own = (int)(c.x + c.y + c.z + c.w);
@@ -147,6 +122,30 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
       }
     }
     __syncthreads();
+  };
+  // ---- the cut, the m-th largest image: as many of its high bits as it takes to leave few rows
+  uint32_t cut = 0;                       // those bits
+  int need = m, count = M, shift = 32;    // of the rows that agree with them, how many are taken; the bits below
+  if (tid == 0) s_listed = 0;
+  for (int i = tid; i < 2 * MAXC * CHOOSE_WARPS; i += CHOOSE_THREADS) (&s_of[0][0])[i] = 0;
+  for (int pass = 0; pass < 3 && need < count && (pass == 0 || count > LIST); ++pass) {
+    const int upper = shift, bits = pass == 2 ? 10 : 11;
+    uint32_t *hist = s_hist[pass & 1];
+    reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    shift -= bits;
+    const uint32_t mask = (1u << bits) - 1;
+    if (pass == 0)
+      each(from_weights, [&](int i, uint32_t x, bool live) {
+        if (HELD && live) held[i - w0] = x;
+        if (live) atomicAdd(&hist[x >> 21], 1u);
+      });
+    else
+      each(image, [&](int, uint32_t x, bool live) {
+        if (live && x >> upper == cut) atomicAdd(&hist[x >> shift & mask], 1u);
+      });
+    cl.sync();
+    find_bin(hist, C, need);
     cut = cut << bits | (uint32_t)s_bin;
     need -= s_above;
     count = s_count;
@@ -155,27 +154,24 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
   // go to a list
   const bool listed = need < count && shift > 0;
   int above = 0, equal = 0;
-  each([&](int, uint32_t x, bool live) {
+  each(image, [&](int, uint32_t x, bool live) {
     const uint32_t high = x >> shift;
-    above += __popc(__ballot_sync(0xffffffffu, live && high > cut));
-    const bool eq = live && high == cut;
-    const uint32_t be = __ballot_sync(0xffffffffu, eq);
-    if (!listed) {
-      equal += __popc(be);
-    } else if (be) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&s_listed, __popc(be));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(be & ((1u << lane) - 1));
-      if (eq) {
+    above += live && high > cut;
+    if (live && high == cut) {
+      ++equal;
+      if (listed) {
+        const int at = atomicAdd(&s_listed, 1);
         s_list[at] = x;
         s_from[at] = (uint8_t)id;
       }
     }
   });
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
   if (listed) {
     cl.sync();
     if (rank == 0) {
-      // the cluster's lists, PER rows a thread, and their cut bit by bit
+      // the cluster's lists, PER rows a thread, and the rest of the cut's bits
       uint32_t x[PER];
       int from[PER], total = 0;
       for (int k = 0; k < C; ++k) total += *cl.map_shared_rank(&s_listed, k);
@@ -193,26 +189,26 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
           from[j] = cl.map_shared_rank(s_from, k)[at];
         }
       }
-      cut <<= shift;
-      int more = 0;                       // rows above the bits tried last that were enough
-      for (int bit = shift - 1, turn = 0; bit >= 0; --bit, turn ^= 1) {
-        const uint32_t tried = cut | 1u << bit;
-        int some = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) some += x[j] >= tried;
-        some = __reduce_add_sync(0xffffffffu, some);
-        if (lane == 0) s_warp[turn][warp] = some;
+      for (int low = shift; low > 0;) {
+        const int upper = low, bits = min(low, 11);
+        low -= bits;
         __syncthreads();
-        some = __reduce_add_sync(0xffffffffu, lane < CHOOSE_WARPS ? s_warp[turn][lane] : 0);
-        if (some >= need) cut = tried;
-        else more = some;                 // (the fewest tried: those above the final cut)
+        reinterpret_cast<uint4 *>(s_hist[0])[tid] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (from[j] >= 0 && x[j] >> upper == cut) atomicAdd(&s_hist[0][x[j] >> low & ((1u << bits) - 1)], 1u);
+        __syncthreads();
+        find_bin(s_hist[0], 1, need);
+        cut = cut << bits | (uint32_t)s_bin;
+        need -= s_above;
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j)
         if (from[j] >= 0 && x[j] >= cut) atomicAdd(&s_of[x[j] > cut ? 0 : 1][from[j]], 1);
       if (tid == 0) {
         s_cut = cut;
-        s_need = need - more;
+        s_need = need;
       }
     }
     cl.sync();
@@ -241,15 +237,21 @@ __global__ void __launch_bounds__(CHOOSE_THREADS, 2) choose_rows_kernel(const __
     above += *cl.map_shared_rank(&s_total[0], k);
     equal += *cl.map_shared_rank(&s_total[1], k);
   }
+  // a row's place: kept rows before it
   const uint32_t before = (1u << lane) - 1;
-  each([&](int i, uint32_t x, bool live) {
+  int at = above + min(equal, need), left = need - min(equal, need);   // alike rows that are still taken
+  each(image, [&](int i, uint32_t x, bool live) {
     const uint32_t high = x >> shift;
-    const bool is_above = live && high > cut, is_equal = live && high == cut;
-    const uint32_t ba = __ballot_sync(0xffffffffu, is_above), be = __ballot_sync(0xffffffffu, is_equal);
-    if (is_above) rows[above + __popc(ba & before) + min(equal + __popc(be & before), need)] = i;
-    else if (is_equal && equal + __popc(be & before) < need) rows[above + __popc(ba & before) + equal + __popc(be & before)] = i;
-    above += __popc(ba);
-    equal += __popc(be);
+    bool kept = live && high > cut;
+    const bool alike = live && high == cut;
+    if (left > 0 && __any_sync(0xffffffffu, alike)) {
+      const uint32_t be = __ballot_sync(0xffffffffu, alike);
+      kept = kept || (alike && __popc(be & before) < left);
+      left -= min(left, __popc(be));
+    }
+    const uint32_t bk = __ballot_sync(0xffffffffu, kept);
+    if (kept) rows[at + __popc(bk & before)] = i;
+    at += __popc(bk);
   });
   cl.sync();                              // no CTA leaves while another reads its totals
 }
@@ -384,10 +386,13 @@ cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t lists = (int64_t)p.B * p.KVH;
   int C = 1;
-  while (C < MAXC && (int64_t)C * CHOOSE_WARPS * STEP < p.width && lists * C < 2 * sms) C *= 2;
+  while (C < MAXC && C * 4096LL < p.width && lists * C < 2 * sms) C *= 2;
+  // (a run of a warp is whole steps of 32 rows)
+  const int64_t held = ((int64_t)p.width + C * CHOOSE_THREADS - 1) / (C * CHOOSE_THREADS) * CHOOSE_THREADS;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(lists * C));
   cfg.blockDim = dim3(CHOOSE_THREADS);
+  cfg.dynamicSmemBytes = held <= MOST_HELD ? held * 4 : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -397,8 +402,12 @@ cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return (int64_t)C * CHOOSE_WARPS * STEP >= p.width ? cudaLaunchKernelEx(&cfg, choose_rows_kernel<true>, p)
-                                                     : cudaLaunchKernelEx(&cfg, choose_rows_kernel<false>, p);
+  return held <= MOST_HELD ? cudaLaunchKernelEx(&cfg, choose_rows_kernel<true>, p)
+                           : cudaLaunchKernelEx(&cfg, choose_rows_kernel<false>, p);
+}
+
+cudaError_t prepare_choose_rows() {
+  return cudaFuncSetAttribute(choose_rows_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_HELD * 4);
 }
 
 cudaError_t launch_keep_rows(const KeepParams &p, cudaStream_t s) {

@@ -136,6 +136,7 @@ struct ChooseParams {
   unsigned int *err;
 };
 cudaError_t launch_choose_rows(const ChooseParams &p, cudaStream_t s);
+cudaError_t prepare_choose_rows();
 
 struct KeepParams {
   const int *first;          // [B] or NULL (prefix_len)
