@@ -26,7 +26,7 @@ namespace cg = cooperative_groups;
 constexpr int CHOOSE_THREADS = 512, CHOOSE_WARPS = CHOOSE_THREADS / 32, BINS = 2048;
 constexpr int MAXC = 8;
 constexpr int MOST_HELD = 16384;          // weights that a CTA holds in shared memory
-constexpr int LIST = 4096;                // rows near the cut that are told apart in a list
+constexpr int LIST = 2048;                // rows near the cut that are told apart in a list
 constexpr int PER = LIST / CHOOSE_THREADS;
 
 // larger image: larger weight; NaN as -infinity, -0 as 0
@@ -268,8 +268,11 @@ __device__ __forceinline__ void move_rows(uint4 *pages, const int *table, const 
   // pages: head g of cache row 0; row_step: 16-byte chunks from one cache row to the next
   constexpr int RP = KEEP_THREADS / LANES, ROWS = RP * UNITS;
   const int r = threadIdx.x / LANES, c = threadIdx.x % LANES + lane16;
-  int src[UNITS], from[UNITS], to[UNITS], old_to[UNITS];       // rows; slots (-1: stays where it is)
-  uint4 v[UNITS], old[UNITS];
+  struct Step {
+    int from[UNITS], to[UNITS];            // slots; -1: stays where it is
+    uint4 v[UNITS];
+  };
+  int src[UNITS];
   auto look_up = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
@@ -277,39 +280,43 @@ __device__ __forceinline__ void move_rows(uint4 *pages, const int *table, const 
       src[u] = i < count ? __ldg(list + i) : i;
     }
   };
-  auto find = [&](int i0) {
+  auto find = [&](int i0, Step &s) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int i = i0 + u * RP + r, f = own + src[u], t = own + i;
-      from[u] = to[u] = -1;
+      s.from[u] = s.to[u] = -1;
       if (src[u] != i) {
-        from[u] = __ldg(table + f / kPageRows) * kPageRows + f % kPageRows;
-        to[u] = __ldg(table + t / kPageRows) * kPageRows + t % kPageRows;
+        s.from[u] = __ldg(table + f / kPageRows) * kPageRows + f % kPageRows;
+        s.to[u] = __ldg(table + t / kPageRows) * kPageRows + t % kPageRows;
       }
     }
   };
-  auto load = [&] {
+  auto load = [&](Step &s) {
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
-      if (from[u] >= 0) v[u] = pages[from[u] * row_step + c];
+      if (s.from[u] >= 0) s.v[u] = pages[s.from[u] * row_step + c];
   };
-  look_up(0);
-  find(0);
-  look_up(ROWS);
-  load();
-  for (int i0 = 0; i0 < count; i0 += ROWS) {
+  auto store = [&](const Step &s) {
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      old[u] = v[u];
-      old_to[u] = to[u];
-    }
-    find(i0 + ROWS);
+    for (int u = 0; u < UNITS; ++u)
+      if (s.to[u] >= 0) pages[s.to[u] * row_step + c] = s.v[u];
+  };
+  Step a, b;
+  auto advance = [&](int i0, Step &now, Step &next) {
+    find(i0 + ROWS, next);
     look_up(i0 + 2 * ROWS);
     __syncthreads();                       // the rows of this step are loaded
-    load();
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-      if (old_to[u] >= 0) pages[old_to[u] * row_step + c] = old[u];
+    load(next);
+    store(now);
+  };
+  look_up(0);
+  find(0, a);
+  look_up(ROWS);
+  load(a);
+  for (int i0 = 0; i0 < count; i0 += 2 * ROWS) {
+    advance(i0, a, b);
+    if (i0 + ROWS >= count) break;
+    advance(i0 + ROWS, b, a);
   }
 }
 
