@@ -39,6 +39,13 @@
 // two products, the rest waiting for its turn at the tensor pipe and for
 // barriers; the tensor pipe is 40% busy.
 //
+// TREE: rows that see, of their request's new rows, those of a bit mask, and the log of
+// the softmax sum as a second result.  A tile that holds new rows takes the row's 128
+// bits from its mask (shifted by the tile's place); all others are as without.
+// Measured: 32 trees of 16 to 64 rows (1275 rows) over a shared prefix of 8192 and 256
+// to 4096 rows of their own 322 us, 690 TFLOP/s of visible products; one tree of 64
+// rows over 2000 27 us.
+//
 // Warps 0-3, 4-7: the streams; 8: TMA producer (a ring of K and V tiles, one
 // copy per page and 64 dims); 9, 10: issue the MMAs of a stream each; 11
 // completes the register split of the last warpgroup.
