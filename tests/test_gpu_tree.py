@@ -313,7 +313,13 @@ def test_without_a_mask_it_is_the_paged_attention(sess, dtype, dim):
     ws = sess.attention_workspace(lay, 2, pb.rows)
     ref = torch.full(out.shape, FILL, dtype=dtype, device="cuda")
     sess.paged_attention(lay, q.contiguous(), pb.row_start, pb.kv_len, ref, ws)
-    assert torch.equal(ref, out)
+    # fp32: the same arithmetic; bf16: a row's sum is of two threads here, of one there, so the results are
+    # two roundings of values 2^-22 apart, both held to the 64-bit ones
+    if dtype == F32:
+        assert torch.equal(ref, out)
+    else:
+        close(pb, q, 8, ref, None, dim ** -0.5, [causal(30), causal(200)])
+        assert bool(((ref.double() - out.double()).abs() <= 2.0 ** -7 * ref.double().abs() + 2.0 ** -18).all())
 
 
 def test_a_tree_that_is_a_chain_is_causal(sess):
