@@ -1072,7 +1072,12 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
     const uint32_t t_o = tmem + lanes + 256 + x * 128;
     const float sl = p.negative ? -p.scale_log2 : p.scale_log2;
     const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
-    auto wait = [&](uint64_t *b, uint32_t parity) {
+    // barriers by their 32-bit addresses: registers are short here
+    const uint32_t at_full = su32(full), at_empty = at_full + 8 * NS, at_s_full = at_empty + 8 * NS;
+    const uint32_t at_p_full = at_s_full + 32, at_o_full = at_p_full + 16, at_o_read = at_o_full + 16;
+    const uint32_t at_item_full = at_o_read + 16, at_item_empty = at_item_full + 8 * NQ;
+    const uint32_t at_q_free = at_item_empty + 8 * NQ + 8, at_ml_full = at_q_free + 8, at_ml_free = at_q_free + 16;
+    auto wait = [&](uint32_t b, uint32_t parity) {
       if (ok && !mbar_wait(b, parity)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
@@ -1089,31 +1094,41 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
     uint32_t c = 0, u = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
     const int row_tok = row / G, row_head = row % G;
     while (true) {
-      Item it;
-      const bool more = next_item(it);
-      if (any(!ok)) ok = false;
-      if (!ok || !more) break;
-      const int n = it.ntiles;
-      const bool pair = it.ntok > tpt;
+      // the item's words stay where they are until its rows are written: what the tiles do not need is read
+      // again then
+      const uint32_t entry = n_item % NQ;
+      wait(at_item_full + 8 * entry, (n_item / NQ) & 1);
+      if (any(!ok)) {
+        ok = false;
+        break;
+      }
+      ++n_item;
+      int n, keys_left, lim;
+      bool pair, own, live;
+      {
+        const Item it = read_item(s_items + entry * 12);
+        n = it.ntiles;
+        keys_left = it.keys_left;
+        pair = it.ntok > tpt;
+        const int mine = (pair ? x * tpt : 0) + row_tok;       // this thread's token of the item
+        own = row < rt_rows && mine < it.ntok;
+        live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
+        // (rows that nobody owns see every key: the mask costs a warp its fast path)
+        lim = own ? it.lim_base + it.lim_slope * (it.tok0 + mine) : 1 << 30;
+      }
+      if (n == 0) break;
       const int ahead = pair ? 1 : 2;
-      const int mine = (pair ? x * tpt : 0) + row_tok;         // this thread's token of the item
-      const bool own = row < rt_rows && mine < it.ntok;
-      const bool live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
-      const int tok = it.tok0 + mine, h = it.g * G + row_head;
-      // (rows that nobody owns see every key: the mask costs a warp its fast path)
-      const int lim = own ? it.lim_base + it.lim_slope * tok : 1 << 30;
-      const uint32_t *mask = mask_of(p.a, tok);
       float m = -INFINITY, l = 0.f;
       const uint32_t uses = pair ? 1 : 2;   // of a tile by this stream, of the two that free it
-      auto release = [&](int order) { mbar_arrive(&empty[(u + order) % NS], uses); };
+      auto release = [&](int order) { mbar_arrive(at_empty + 8 * ((u + order) % NS), uses); };
       // V rows past the segment's last key may hold anything: 0 times it has to be 0
       auto clear_v = [&](int t) {
-        if (t != n - 1 || it.keys_left >= n * KT) return;
+        if (t != n - 1 || keys_left >= n * KT) return;
         const int ov = u + order_v(t, n, ahead);
-        wait(&full[ov % NS], (ov / NS) & 1);
+        wait(at_full + 8 * (ov % NS), (ov / NS) & 1);
         if (!ok) return;
         uint8_t *vt = ring + (ov % NS) * C::TILE;
-        for (int i = (it.keys_left - t * KT) * 8 + side * 128 + row; i < KT * 8; i += 256)
+        for (int i = (keys_left - t * KT) * 8 + side * 128 + row; i < KT * 8; i += 256)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
             *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
@@ -1121,13 +1136,13 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
       };
       const int step = pair ? 1 : 2;
       for (int t = pair ? 0 : x; t < n; t += step) {
-        wait(&s_full[x], c & 1);
+        wait(at_s_full + 8 * x, c & 1);
         ++c;
         tc_fence_after();
         if (row == 96 && side == 0) {      // S has read K(t), and the product before it its V
           release(order_k(t, n, ahead));
           if (t >= ahead) release(order_v(t - ahead, n, ahead));
-          if (t + ahead >= n) mbar_arrive(q_free, !pair && n == 1 ? 2 : 1);   // its last S
+          if (t + ahead >= n) mbar_arrive(at_q_free, !pair && n == 1 ? 2 : 1);   // its last S
         }
         const int vis = lim - t * KT - side * 64;              // of this side's keys, those seen without a look at the mask
         const bool whole = __all_sync(0xffffffffu, vis >= 64);
@@ -1159,10 +1174,11 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
         float mx = -INFINITY, alpha = 1.f;
         if (live) {
           if (!whole) {
+            const uint32_t *mask = mask_of(p.a, s_items[entry * 12 + 1] + (pair ? x * tpt : 0) + row_tok);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) &
-                        first_bits(it.keys_left - t * KT - side * 64 - 32 * i);
+                        first_bits(keys_left - t * KT - side * 64 - 32 * i);
           }
           load(0);
           mx = maximum(0);
@@ -1250,23 +1266,27 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
         }
         clear_v(t);
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(at_p_full + 8 * x);
       }
       // ---- the item's rows: o / l and log2 of their weight, or the result
+      const Item it = read_item(s_items + entry * 12);
+      const int mine = (pair ? x * tpt : 0) + row_tok, tok = it.tok0 + mine, h = it.g * G + row_head;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(at_item_empty + 8 * entry);
       const bool both = !pair && n > 1;    // the other stream holds the odd tiles' share
       if (both && x == 1 && side == 0) {
-        if (n_ml > 0) wait(ml_free, (n_ml - 1) & 1);
+        if (n_ml > 0) wait(at_ml_free, (n_ml - 1) & 1);
         if (ok) {
           s_ml[row] = make_float2(m, l);
-          mbar_arrive(ml_full);
+          mbar_arrive(at_ml_full);
         }
       }
       if (pair || x == 0) {
-        wait(&o_full[x], (o_par >> x) & 1);
+        wait(at_o_full + 8 * x, (o_par >> x) & 1);
         float a0 = 1.f, a1 = 0.f;
         if (both) {
-          wait(&o_full[1], (o_par >> 1) & 1);
-          wait(ml_full, n_ml & 1);
+          wait(at_o_full + 8, (o_par >> 1) & 1);
+          wait(at_ml_full, n_ml & 1);
           if (ok) {
             const float2 ml = s_ml[row];
             const float ms = fmaxf(m, ml.x), base = ms == -INFINITY ? 0.f : ms;
@@ -1274,7 +1294,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
             a1 = ex2(ml.x - base);
             l = l * a0 + ml.y * a1;
             m = ms;
-            mbar_arrive(ml_free);
+            mbar_arrive(at_ml_free);
           }
         }
         if (ok) {
@@ -1287,7 +1307,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
             // a row may see no key, of the split or at all: zeros
             const float inv = l == 0.f ? 0.f : 1.f / l;
             // new rows among the item's keys, that the row may not see
-            const int end = min(n * KT, it.keys_left);
+            const int end = min(n * KT, keys_left);
             const bool hides = own && lim < end && l != 0.f;
             bool odd = false;
             a0 *= inv;
@@ -1346,8 +1366,8 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
               list_spoiled<D, true>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
           }
           tc_fence_before();
-          mbar_arrive(&o_read[x]);
-          if (both) mbar_arrive(&o_read[1]);
+          mbar_arrive(at_o_read + 8 * x);
+          if (both) mbar_arrive(at_o_read + 8);
         }
       }
       // streams that took part in this item
