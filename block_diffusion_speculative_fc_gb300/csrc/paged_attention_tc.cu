@@ -64,14 +64,10 @@ namespace dflash {
 namespace {
 
 constexpr int KT = 128;                   // keys of a tile
-// SIDES: threads of a row, each with that share of a tile's keys.  Registers a thread: 168 at launch (384
-// threads), then 208 for the streams and 80 for the rest (256 * 208 + 128 * 80 <= 384 * 168); with two sides
-// 96 (640 threads), then 104 and 64 (512 * 104 + 128 * 64 <= 640 * 96).
-template <bool TREE> struct Roles {
-  static constexpr int SIDES = TREE ? 2 : 1, STREAM = 128 * SIDES, THREADS = 2 * STREAM + 128;
-  static constexpr int PRODUCER = 8 * SIDES, ISSUER = PRODUCER + 1;   // warps
-  static constexpr int REGS_STREAM = TREE ? 104 : 208, REGS_REST = TREE ? 64 : 80;
-};
+constexpr int THREADS = 384;
+// registers a thread: 168 at launch (384 threads), then 208 for the streams and 80 for the rest
+// (256 * 208 + 128 * 80 <= 384 * 168)
+constexpr int REGS_STREAM = 208, REGS_REST = 80;
 constexpr int PLAN_THREADS = 1024;
 constexpr int NQ = 4;                     // items known ahead in a CTA
 constexpr int EXTRA = 1024;               // items beyond one per (segment, head, row tile pair)
@@ -546,10 +542,8 @@ template <int D, bool TREE> __device__ __noinline__ void redo_rows(const Params 
 }
 
 template <int D, bool TREE>
-__global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
-  using W = Roles<TREE>;
-  constexpr int SIDES = W::SIDES;
   constexpr int NS = C::NSLOT, NB = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -575,27 +569,27 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&turn[i], 1);
-      mbar_init(&p_full[i], W::STREAM);
+      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_read[i], W::STREAM);
+      mbar_init(&o_read[i], 128);
     }
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 2 + 8 * SIDES);   // a lane of each MMA and stream warp
+      mbar_init(&item_empty[i], 10);      // a lane of each MMA and stream warp
     }
     mbar_init(q_full, 1);
     mbar_init(q_free, 2);
     mbar_init(ml_full, 128);
-    mbar_init(ml_free, W::STREAM);
+    mbar_init(ml_free, 128);
     mbar_init(done, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == W::ISSUER) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(s_tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == W::PRODUCER && lane == 0) {
+  if (warp == 8 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmK) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmV) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&p.tmQ) : "memory");
@@ -621,9 +615,9 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
     return it.ntiles > 0;
   };
 
-  if (warp >= W::PRODUCER) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::REGS_REST));
-    if (warp == W::PRODUCER) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    if (warp == 8) {
       // ------------------------------------------------------------ producer (one warp)
       uint32_t u = 0, k = 0;                // tiles issued, items begun
       int slot = 0, phase = 1;              // place in the ring; parity of its empty barrier
@@ -733,7 +727,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
         for (uint32_t v = u > (uint32_t)NS ? u - NS : 0; v < u; ++v) mbar_wait(&full[v % NS], (v / NS) & 1);
         if (k > 0) mbar_wait(q_full, (k - 1) & 1);
       }
-    } else if (warp <= W::ISSUER + 1) {
+    } else if (warp <= 10) {
       // ------------------------------------------------------------ MMA issuers: a lane a stream
       // Groups of MMAs alternate between the streams (a token goes back and forth), which keeps
       // them out of phase: one's softmax runs while the other's products do.  Without the token
@@ -742,7 +736,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
       // addresses.  Commits cost the tensor pipe 40 to 80 clocks each, so a step has one: S of the
       // stream's next tile, after which the tiles that the step has read are released by the
       // stream that waits for that S.
-      const uint32_t x = warp - W::ISSUER;
+      const uint32_t x = warp - 9;
       if (lane == 0) {
         constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
         const uint64_t k_desc = desc_k(su32(ring)), v_desc = desc_mn(su32(ring), KT * 128);
@@ -809,8 +803,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-              // (with two sides each has its weights in the upper half of its own S columns)
-              umma_ts(t_o, TREE ? t_s + (kk >> 2) * 64 + 32 + (kk & 3) * 8 : t_s + P_COL + kk * 8, vd + kk * (2048 >> 4), ID_O, (t == t0 && kk == 0) ? 0u : 1u);
+              umma_ts(t_o, t_s + P_COL + kk * 8, vd + kk * (2048 >> 4), ID_O, (t == t0 && kk == 0) ? 0u : 1u);
             if (more) issue_s(order + 1);
             else umma_commit(&o_full[x]);
             // the other stream's step, or after the item's last the next item's first group, stream 0's
@@ -826,13 +819,12 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::REGS_STREAM));
-    if constexpr (!TREE) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_STREAM));
     // ------------------------------------------------------------ softmax, a row a thread
     const int x = warp >> 2, row = threadIdx.x & 127;          // stream, row of its tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + x * KT;
-    const float sl = p.scale_log2;
+    const float sl = p.negative ? -p.scale_log2 : p.scale_log2;
     const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
     // every wait is one for the warp, so that its lanes stay together
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -885,16 +877,21 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
             tmem_ld32(t_s + half * 64, sv);
             tmem_ld32(t_s + half * 64 + 32, sv + 32);
             tmem_ld_wait();
-            if (p.negative) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) sv[i] ^= 0x80000000u;
-            }
           };
           const int vis = lim - t * KT;                        // visible keys of this tile
           const bool whole = __all_sync(0xffffffffu, vis >= KT);
-          auto maximum = [&](int half, float a0) {
-            if (whole) {
-              float a1 = __uint_as_float(sv[0]), a2 = __uint_as_float(sv[1]), a3 = __uint_as_float(sv[2]);
+          uint32_t bits[KT / 32];                              // of them, where the new rows are among them
+          if (TREE && !whole) {
+            const uint32_t *mask = mask_of(p.a, tok);
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i)
+              bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) & first_bits(it.keys_left - t * KT - 32 * i);
+          }
+          auto sees = [&](int e) { return TREE ? (bits[e >> 5] >> (e & 31) & 1u) != 0 : e < vis; };
+          // the largest of a half's seen scores times the scale
+          auto maximum = [&](int half) {
+            if (whole && !p.negative) {
+              float a0 = -INFINITY, a1 = __uint_as_float(sv[0]), a2 = __uint_as_float(sv[1]), a3 = __uint_as_float(sv[2]);
               a0 = fmaxf(a0, __uint_as_float(sv[3]));
 #pragma unroll
               for (int i = 4; i < 60; i += 8) {
@@ -905,17 +902,22 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
               }
               a0 = max3(a0, __uint_as_float(sv[60]), __uint_as_float(sv[61]));
               a1 = max3(a1, __uint_as_float(sv[62]), __uint_as_float(sv[63]));
-              return max3(fmaxf(a0, a1), a2, a3);
+              return max3(fmaxf(a0, a1), a2, a3) * sl;
             }
+            float a0 = -INFINITY;
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) a0 = half * 64 + i < vis ? fmaxf(a0, __uint_as_float(sv[i])) : a0;
+              for (int i = 0; i < 64; ++i) a0 = fmaxf(a0, __uint_as_float(sv[i]) * sl);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) a0 = sees(half * 64 + i) ? fmaxf(a0, __uint_as_float(sv[i]) * sl) : a0;
+            }
             return a0;
           };
           load(0);
-          float mx = maximum(0, -INFINITY);
+          float mx = maximum(0);
           load(1);
-          mx = maximum(1, mx);
-          mx = vis > 0 ? mx * sl : -INFINITY;
+          mx = fmaxf(mx, maximum(1));
           float alpha = 1.f;
           if (mx > m + TAU || m == -INFINITY) {
             if (m != -INFINITY) alpha = ex2(m - mx);
@@ -924,22 +926,26 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
           const float mm = m == -INFINITY ? 0.f : m;
           const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
           float2 sum = make_float2(0.f, 0.f);
-          auto weights = [&](int half) {
+          auto weights_of = [&](int half, auto all) {          // `all`: every key is seen
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int e = half * 64 + 2 * i;
               const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
               float2 q = make_float2(ex2(a.x), ex2(a.y));
-              if (!whole) {
-                q.x = e < vis ? q.x : 0.f;
-                q.y = e + 1 < vis ? q.y : 0.f;
+              if (!decltype(all)::value) {
+                q.x = sees(e) ? q.x : 0.f;
+                q.y = sees(e + 1) ? q.y : 0.f;
               }
               sum = add2(sum, q);
               __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
               w[i] = *reinterpret_cast<uint32_t *>(&h2);
             }
             tmem_st32(t_s + P_COL + half * 32, w);
+          };
+          auto weights = [&](int half) {
+            if (whole) weights_of(half, std::true_type());
+            else weights_of(half, std::false_type());
           };
           weights(1);
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -994,8 +1000,9 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
           if (both) release(order_v(n - 2, n, ahead));
         }
         if (live) {
-          // a split may hold no key that the row sees; a whole row of -infinities has no result (NaN)
-          const float inv = l == 0.f && it.part >= 0 ? 0.f : 1.f / l;
+          // a split may hold no key that the row sees; a whole row of -infinities has no result (NaN),
+          // with masks zeros, as one that sees nothing
+          const float inv = l == 0.f && (TREE || it.part >= 0) ? 0.f : 1.f / l;
           // keys of these tiles that the row does not see
           const int end = min(n * KT, it.keys_left);
           const bool hides = own && lim < end && l != 0.f;
@@ -1006,6 +1013,8 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
           const int at = it.part + mine * G + row_head;        // partial row
           float *po = p.part_o + (int64_t)at * D;
           if (own && it.part >= 0) p.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+          if (TREE && own && it.part < 0 && p.a.lse)
+            p.a.lse[(int64_t)tok * p.a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 #pragma unroll
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
@@ -1049,7 +1058,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
             }
           }
           if (__builtin_expect(__any_sync(0xffffffffu, odd), 0))
-            list_spoiled<D, false>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
+            list_spoiled<D, TREE>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
         }
         tc_fence_before();
         mbar_arrive(&o_read[x]);
@@ -1059,322 +1068,6 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
       o_par ^= pair || n > 1 ? 3u : 1u;
       if (both) ++n_ml;
       u += 2 * n;
-    }
-    } else {
-    // ------------------------------------------------------------ softmax, two threads a row: keys 0..63 and
-    // 64..127 of a tile.  They share the running reference: one barrier of the stream's 256 threads a tile
-    // says whether any row has to move its own, and where one has, the sides exchange their maxima through
-    // TMEM.  After a wait that gave up, `ok` is false in its warp; the barriers carry that to the others, so that
-    // all of a stream leave together.
-    const int x = warp >> 3, side = (warp >> 2) & 1, row = threadIdx.x & 127;   // stream, keys, row of its tile
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + x * KT + side * 64, t_other = tmem + lanes + x * KT + (side ^ 1) * 64;
-    const uint32_t t_o = tmem + lanes + 256 + x * 128;
-    const float sl = p.negative ? -p.scale_log2 : p.scale_log2;
-    const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
-    // barriers by their 32-bit addresses: registers are short here
-    const uint32_t at_full = su32(full), at_empty = at_full + 8 * NS, at_s_full = at_empty + 8 * NS;
-    const uint32_t at_p_full = at_s_full + 32, at_o_full = at_p_full + 16, at_o_read = at_o_full + 16;
-    const uint32_t at_item_full = at_o_read + 16, at_item_empty = at_item_full + 8 * NQ;
-    const uint32_t at_q_free = at_item_empty + 8 * NQ + 8, at_ml_full = at_q_free + 8, at_ml_free = at_q_free + 16;
-    auto wait = [&](uint32_t b, uint32_t parity) {
-      if (ok && !mbar_wait(b, parity)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    auto any = [&](bool v) {               // of the stream's threads
-      uint32_t r;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-          "barrier.cta.red.or.pred q, %2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(r)
-          : "r"((uint32_t)v), "r"(2 + x)
-          : "memory");
-      return r != 0;
-    };
-    uint32_t c = 0, u = 0, o_par = 0, n_ml = 0;   // o_par bit x: parity of o_full[x]
-    const int row_tok = row / G, row_head = row % G;
-    while (true) {
-      // the item's words stay where they are until its rows are written: what the tiles do not need is read
-      // again then
-      const uint32_t entry = n_item % NQ;
-      wait(at_item_full + 8 * entry, (n_item / NQ) & 1);
-      if (any(!ok)) {
-        ok = false;
-        break;
-      }
-      ++n_item;
-      int n, keys_left, lim;
-      bool pair, own, live;
-      {
-        const Item it = read_item(s_items + entry * 12);
-        n = it.ntiles;
-        keys_left = it.keys_left;
-        pair = it.ntok > tpt;
-        const int mine = (pair ? x * tpt : 0) + row_tok;       // this thread's token of the item
-        own = row < rt_rows && mine < it.ntok;
-        live = ((pair ? x * tpt : 0) + ((warp & 3) * 32) / G) < it.ntok && (warp & 3) * 32 < rt_rows;
-        // (rows that nobody owns see every key: the mask costs a warp its fast path)
-        lim = own ? it.lim_base + it.lim_slope * (it.tok0 + mine) : 1 << 30;
-      }
-      if (n == 0) break;
-      const int ahead = pair ? 1 : 2;
-      float m = -INFINITY, l = 0.f;
-      const uint32_t uses = pair ? 1 : 2;   // of a tile by this stream, of the two that free it
-      auto release = [&](int order) { mbar_arrive(at_empty + 8 * ((u + order) % NS), uses); };
-      // V rows past the segment's last key may hold anything: 0 times it has to be 0
-      auto clear_v = [&](int t) {
-        if (t != n - 1 || keys_left >= n * KT) return;
-        const int ov = u + order_v(t, n, ahead);
-        wait(at_full + 8 * (ov % NS), (ov / NS) & 1);
-        if (!ok) return;
-        uint8_t *vt = ring + (ov % NS) * C::TILE;
-        for (int i = (keys_left - t * KT) * 8 + side * 128 + row; i < KT * 8; i += 256)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            *reinterpret_cast<uint4 *>(vt + b * (KT * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_async_smem();
-      };
-      const int step = pair ? 1 : 2;
-      for (int t = pair ? 0 : x; t < n; t += step) {
-        wait(at_s_full + 8 * x, c & 1);
-        ++c;
-        tc_fence_after();
-        if (row == 96 && side == 0) {      // S has read K(t), and the product before it its V
-          release(order_k(t, n, ahead));
-          if (t >= ahead) release(order_v(t - ahead, n, ahead));
-          if (t + ahead >= n) mbar_arrive(at_q_free, !pair && n == 1 ? 2 : 1);   // its last S
-        }
-        const int vis = lim - t * KT - side * 64;              // of this side's keys, those seen without a look at the mask
-        const bool whole = __all_sync(0xffffffffu, vis >= 64);
-        uint32_t sv[32], bits[2] = {0xffffffffu, 0xffffffffu};
-        auto load = [&](int half) {
-          tmem_ld32(t_s + half * 32, sv);
-          tmem_ld_wait32(sv);
-        };
-        // the largest of a half's scores times the scale
-        auto maximum = [&](int half) {
-          if (whole && !p.negative) {
-            float a0 = __uint_as_float(sv[0]), a1 = __uint_as_float(sv[1]), a2 = __uint_as_float(sv[2]);
-            a0 = fmaxf(a0, __uint_as_float(sv[3]));
-#pragma unroll
-            for (int i = 4; i < 28; i += 6) {
-              a0 = max3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-              a1 = max3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-              a2 = max3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
-            }
-            a1 = max3(a1, __uint_as_float(sv[28]), __uint_as_float(sv[29]));
-            a2 = max3(a2, __uint_as_float(sv[30]), __uint_as_float(sv[31]));
-            return max3(a0, a1, a2) * sl;
-          }
-          float a0 = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) a0 = bits[half] >> i & 1u ? fmaxf(a0, __uint_as_float(sv[i]) * sl) : a0;
-          return a0;
-        };
-        float mx = -INFINITY, alpha = 1.f;
-        if (live) {
-          if (!whole) {
-            const uint32_t *mask = mask_of(p.a, s_items[entry * 12 + 1] + (pair ? x * tpt : 0) + row_tok);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) &
-                        first_bits(keys_left - t * KT - side * 64 - 32 * i);
-          }
-          load(0);
-          mx = maximum(0);
-          load(1);
-          mx = fmaxf(mx, maximum(1));
-        }
-        if (any(mx > m + TAU || !ok)) {
-          // (keys 32..63 of a side are in registers now: their first column carries its maximum)
-          if (live) {
-            tmem_st1(t_s + 32, __float_as_uint(mx));
-            tmem_st_wait();
-          }
-          tc_fence_before();
-          if (any(!ok)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (live) {
-            uint32_t o;
-            tmem_ld1(t_other + 32, &o);
-            const float both = fmaxf(mx, __uint_as_float(o));
-            if (both > m + TAU) {
-              if (m != -INFINITY) alpha = ex2(m - both);
-              m = both;
-            }
-          }
-          tc_fence_before();
-          any(false);                      // both have read before either writes its weights there
-          tc_fence_after();
-        }
-        if (live) {
-          const float mm = m == -INFINITY ? 0.f : m;
-          const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
-          float2 sum = make_float2(0.f, 0.f);
-          auto weights_of = [&](int half, auto all) {   // `all`: every key is seen
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
-              float2 q = make_float2(ex2(a.x), ex2(a.y));
-              if (!decltype(all)::value) {
-                q.x = bits[half] >> (2 * i) & 1u ? q.x : 0.f;
-                q.y = bits[half] >> (2 * i + 1) & 1u ? q.y : 0.f;
-              }
-              sum = add2(sum, q);
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
-              w[i] = *reinterpret_cast<uint32_t *>(&h2);
-            }
-            tmem_st16(t_s + 32 + half * 16, w);
-          };
-          auto weights = [&](int half) {
-            if (whole) weights_of(half, std::true_type());
-            else weights_of(half, std::false_type());
-          };
-          weights(1);
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-            // S of this tile was issued after the last O product of the stream: O is at rest
-#pragma unroll
-            for (int i = 0; i < D / 2; i += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + side * (D / 2) + i, o);
-              tmem_ld_wait32(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(t_o + side * (D / 2) + i, o);
-            }
-          }
-          load(0);
-          weights(0);
-          l = fmaf(l, alpha, sum.x + sum.y);
-          // the row's sum, of both sides, once its last tile is done
-          if (t + step >= n) tmem_st1(t_s, __float_as_uint(l));
-          tmem_st_wait();
-        }
-        if (t + step >= n) {
-          tc_fence_before();
-          any(false);
-          tc_fence_after();
-          if (live) {
-            uint32_t o;
-            tmem_ld1(t_other, &o);
-            l += __uint_as_float(o);
-          }
-        }
-        clear_v(t);
-        tc_fence_before();
-        mbar_arrive(at_p_full + 8 * x);
-      }
-      // ---- the item's rows: o / l and log2 of their weight, or the result
-      const Item it = read_item(s_items + entry * 12);
-      const int mine = (pair ? x * tpt : 0) + row_tok, tok = it.tok0 + mine, h = it.g * G + row_head;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(at_item_empty + 8 * entry);
-      const bool both = !pair && n > 1;    // the other stream holds the odd tiles' share
-      if (both && x == 1 && side == 0) {
-        if (n_ml > 0) wait(at_ml_free, (n_ml - 1) & 1);
-        if (ok) {
-          s_ml[row] = make_float2(m, l);
-          mbar_arrive(at_ml_full);
-        }
-      }
-      if (pair || x == 0) {
-        wait(at_o_full + 8 * x, (o_par >> x) & 1);
-        float a0 = 1.f, a1 = 0.f;
-        if (both) {
-          wait(at_o_full + 8, (o_par >> 1) & 1);
-          wait(at_ml_full, n_ml & 1);
-          if (ok) {
-            const float2 ml = s_ml[row];
-            const float ms = fmaxf(m, ml.x), base = ms == -INFINITY ? 0.f : ms;
-            a0 = ex2(m - base);
-            a1 = ex2(ml.x - base);
-            l = l * a0 + ml.y * a1;
-            m = ms;
-            mbar_arrive(at_ml_free);
-          }
-        }
-        if (ok) {
-          tc_fence_after();
-          if (row == 0 && side == 0) {     // the last V tiles
-            release(order_v(n - 1, n, ahead));
-            if (both) release(order_v(n - 2, n, ahead));
-          }
-          if (live) {
-            // a row may see no key, of the split or at all: zeros
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            // new rows among the item's keys, that the row may not see
-            const int end = min(n * KT, keys_left);
-            const bool hides = own && lim < end && l != 0.f;
-            bool odd = false;
-            a0 *= inv;
-            a1 *= inv;
-            const int col = side * (D / 2);
-            bf16 *out = (bf16 *)p.a.out + (int64_t)tok * p.a.out_stride + (int64_t)h * D + col;
-            const int at = it.part + mine * G + row_head;      // partial row
-            float *po = p.part_o + (int64_t)at * D + col;
-            if (own && side == 0) {
-              if (it.part >= 0) p.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
-              else if (p.a.lse) p.a.lse[(int64_t)tok * p.a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 2; i += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + col + i, o);
-              tmem_ld_wait32(o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(a0 != 0.f ? __uint_as_float(o[j]) * a0 : 0.f);
-              if (both) {
-                uint32_t q[32];
-                tmem_ld32(tmem + lanes + 256 + 128 + col + i, q);
-                tmem_ld_wait32(q);
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) + (a1 != 0.f ? __uint_as_float(q[j]) * a1 : 0.f));
-              }
-              if (hides) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) odd = odd || !isfinite(__uint_as_float(o[j]));
-              }
-              // 32 bytes a store: whole sectors, as a lane's rows are far apart
-              if (own && it.part >= 0) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 8) store32(po + i + j, o + j);
-              } else if (own) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 16) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]),
-                                                              __uint_as_float(o[j + 2 * e + 1]));
-                    w[e] = *reinterpret_cast<uint32_t *>(&h2);
-                  }
-                  if (wide) {
-                    store32(out + i + j, w);
-                  } else {
-                    *reinterpret_cast<uint4 *>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(out + i + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                  }
-                }
-              }
-            }
-            if (__builtin_expect(__any_sync(0xffffffffu, odd), 0))
-              list_spoiled<D, true>(p, s_redo, it.req, it.g, it.page0, tok * p.a.H + h, it.part >= 0 ? at : -1, lim, end, odd);
-          }
-          tc_fence_before();
-          mbar_arrive(at_o_read + 8 * x);
-          if (both) mbar_arrive(at_o_read + 8);
-        }
-      }
-      // streams that took part in this item
-      o_par ^= pair || n > 1 ? 3u : 1u;
-      if (both) ++n_ml;
-      u += 2 * n;
-    }
     }
     if (!ok && lane == 0) raise_error(p.a.err, DFLASH_DERR_TIMEOUT);
   }
@@ -1386,7 +1079,7 @@ __global__ void __launch_bounds__(Roles<TREE>::THREADS, 1) paged_attention_kerne
     __syncthreads();
   }
   pdl_trigger();   // every global write of this CTA is done
-  if (warp == W::ISSUER) {
+  if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
@@ -1514,9 +1207,9 @@ Layout layout(int B, int total_rows, int H, int KVH, int D, int prefix) {
   L.items = take(sizeof(Item) * max_items);
   L.req = take(sizeof(Request) * B);
   L.row_req = take(4 * (size_t)total_rows);
-  // a row may be done again in every split that holds new rows (without masks in one), up to 1024 of them in
-  // 9 tiles and no more items than there are, and be listed by both of its threads
-  L.redo = take(sizeof(Redo) * 2 * (size_t)std::min(9 * rows, rows + extra));
+  // a row may be done again in every split that holds new rows (without masks in one): up to 1024 of
+  // them in 9 tiles, and no more items than there are
+  L.redo = take(sizeof(Redo) * (size_t)std::min(9 * rows, rows + extra));
   L.part_lse = take(4 * cap);
   L.part_o = take(4 * cap * D);
   L.total = o;
@@ -1549,7 +1242,7 @@ template <int D, bool TREE> cudaError_t launch(const PagedAttnParams &a, void *w
   // a thread a request; barriers of 256 threads are cheaper than those of 1024
   cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(a.rows.B <= 256 ? 256 : PLAN_THREADS), 0, s, p);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_attention_kernel<D, TREE>, dim3(p.sms), dim3(Roles<TREE>::THREADS), Cfg<D>::SMEM, s, p);
+  e = launch_pdl(paged_attention_kernel<D, TREE>, dim3(p.sms), dim3(THREADS), Cfg<D>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.rows.total_rows * a.H;
   const int grid = (int)std::min<int64_t>((warps + 7) / 8, 16LL * p.sms);
