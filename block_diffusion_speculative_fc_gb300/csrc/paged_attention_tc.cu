@@ -871,83 +871,86 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           if (t + ahead >= n) mbar_arrive(q_free, !pair && n == 1 ? 2 : 1);   // its last S
         }
         if (live) {
-          // keys 0..63 for their maximum, then keys 64..127 and their weights, then keys 0..63 again: reading TMEM twice is cheaper than 128 live registers
-          uint32_t sv[KT / 2];
-          auto load = [&](int half) {
-            tmem_ld32(t_s + half * 64, sv);
-            tmem_ld32(t_s + half * 64 + 32, sv + 32);
-            tmem_ld_wait();
-          };
           const int vis = lim - t * KT;                        // visible keys of this tile
-          const bool whole = __all_sync(0xffffffffu, vis >= KT);
           uint32_t bits[KT / 32];                              // of them, where the new rows are among them
-          if (TREE && !whole) {
-            const uint32_t *mask = mask_of(p.a, tok);
+          // Keys 0..63 for their maximum, then keys 64..127 and their weights, then keys 0..63 again: reading TMEM
+          // twice is cheaper than 128 live registers.  ALL: every key is seen and the scale is not negative,
+          // by far most tiles, in code of its own and in loops over the halves, so that it fits the instruction
+          // cache (one code for all tiles, with a selection a weight, took 216 us for the prompts instead of 188).
+          auto tile = [&](auto every) {
+            constexpr bool ALL = decltype(every)::value;
+            uint32_t sv[KT / 2];
+            auto load = [&](int half) {
+              tmem_ld32(t_s + half * 64, sv);
+              tmem_ld32(t_s + half * 64 + 32, sv + 32);
+              tmem_ld_wait();
+            };
+            // key i of a half
+            auto seen = [&](int half, int i) {
+              return TREE ? ((half ? bits[2 + (i >> 5)] : bits[i >> 5]) >> (i & 31) & 1u) != 0 : half * 64 + i < vis;
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              load(half);
+              if (ALL) {
+                float a0 = __uint_as_float(sv[0]), a1 = __uint_as_float(sv[1]), a2 = __uint_as_float(sv[2]), a3 = __uint_as_float(sv[3]);
 #pragma unroll
-            for (int i = 0; i < KT / 32; ++i)
-              bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) & first_bits(it.keys_left - t * KT - 32 * i);
-          }
-          auto sees = [&](int e) { return TREE ? (bits[e >> 5] >> (e & 31) & 1u) != 0 : e < vis; };
-          // the largest of a half's seen scores times the scale
-          auto maximum = [&](int half) {
-            if (whole && !p.negative) {
-              float a0 = -INFINITY, a1 = __uint_as_float(sv[0]), a2 = __uint_as_float(sv[1]), a3 = __uint_as_float(sv[2]);
-              a0 = fmaxf(a0, __uint_as_float(sv[3]));
+                for (int i = 4; i < 60; i += 8) {
+                  a0 = max3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+                  a1 = max3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+                  a2 = max3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
+                  a3 = max3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+                }
+                a0 = max3(a0, __uint_as_float(sv[60]), __uint_as_float(sv[61]));
+                a1 = max3(a1, __uint_as_float(sv[62]), __uint_as_float(sv[63]));
+                mx = fmaxf(mx, max3(fmaxf(a0, a1), a2, a3) * sl);
+              } else {
 #pragma unroll
-              for (int i = 4; i < 60; i += 8) {
-                a0 = max3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-                a1 = max3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-                a2 = max3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
-                a3 = max3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+                for (int i = 0; i < 64; ++i) mx = seen(half, i) ? fmaxf(mx, __uint_as_float(sv[i]) * sl) : mx;
               }
-              a0 = max3(a0, __uint_as_float(sv[60]), __uint_as_float(sv[61]));
-              a1 = max3(a1, __uint_as_float(sv[62]), __uint_as_float(sv[63]));
-              return max3(fmaxf(a0, a1), a2, a3) * sl;
             }
-            float a0 = -INFINITY;
-            if (whole) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) a0 = fmaxf(a0, __uint_as_float(sv[i]) * sl);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) a0 = sees(half * 64 + i) ? fmaxf(a0, __uint_as_float(sv[i]) * sl) : a0;
+            float alpha = 1.f;
+            if (mx > m + TAU || m == -INFINITY) {
+              if (m != -INFINITY) alpha = ex2(m - mx);
+              m = mx;
             }
-            return a0;
-          };
-          load(0);
-          float mx = maximum(0);
-          load(1);
-          mx = fmaxf(mx, maximum(1));
-          float alpha = 1.f;
-          if (mx > m + TAU || m == -INFINITY) {
-            if (m != -INFINITY) alpha = ex2(m - mx);
-            m = mx;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
-          float2 sum = make_float2(0.f, 0.f);
-          auto weights_of = [&](int half, auto all) {          // `all`: every key is seen
-            uint32_t w[32];
+            const float mm = m == -INFINITY ? 0.f : m;
+            const float2 sl2 = make_float2(sl, sl), mm2 = make_float2(-mm, -mm);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int half = 1; half >= 0; --half) {
+              if (half == 0) load(0);
+              uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int e = half * 64 + 2 * i;
-              const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
-              float2 q = make_float2(ex2(a.x), ex2(a.y));
-              if (!decltype(all)::value) {
-                q.x = sees(e) ? q.x : 0.f;
-                q.y = sees(e + 1) ? q.y : 0.f;
+              for (int i = 0; i < 32; ++i) {
+                const float2 a = fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sl2, mm2);
+                float2 q = make_float2(ex2(a.x), ex2(a.y));
+                if (!ALL) {
+                  q.x = seen(half, 2 * i) ? q.x : 0.f;
+                  q.y = seen(half, 2 * i + 1) ? q.y : 0.f;
+                }
+                sum = add2(sum, q);
+                __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
+                w[i] = *reinterpret_cast<uint32_t *>(&h2);
               }
-              sum = add2(sum, q);
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(q.x, q.y);
-              w[i] = *reinterpret_cast<uint32_t *>(&h2);
+              tmem_st32(t_s + P_COL + half * 32, w);
             }
-            tmem_st32(t_s + P_COL + half * 32, w);
+            l = fmaf(l, alpha, sum.x + sum.y);
+            return alpha;
           };
-          auto weights = [&](int half) {
-            if (whole) weights_of(half, std::true_type());
-            else weights_of(half, std::false_type());
-          };
-          weights(1);
+          float alpha;
+          if (__all_sync(0xffffffffu, vis >= KT) && !p.negative) {
+            alpha = tile(std::true_type());
+          } else {
+            if (TREE) {
+              const uint32_t *mask = mask_of(p.a, tok);
+#pragma unroll
+              for (int i = 0; i < KT / 32; ++i)
+                bits[i] = mask_bits(mask, p.a.mask_words, 32 * i - vis) & first_bits(it.keys_left - t * KT - 32 * i);
+            }
+            alpha = tile(std::false_type());
+          }
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this tile was issued after the last O product of the stream: O is at rest
 #pragma unroll
@@ -960,9 +963,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
               tmem_st32(tmem + lanes + 256 + x * 128 + i, o);
             }
           }
-          load(0);
-          weights(0);
-          l = fmaf(l, alpha, sum.x + sum.y);
           tmem_st_wait();
         }
         clear_v(t);
