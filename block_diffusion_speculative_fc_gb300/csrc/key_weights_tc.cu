@@ -111,7 +111,8 @@ __device__ __forceinline__ bool read_request(const KeyWeightParams &a, int b, bo
 // A run of tiles j0 .. j1-1 of one (request, KV head).
 struct Run {
   Request q;
-  int b, g, tiles, j0, j1, rows, blocks;  // tiles of the request; query rows, blocks of QB of them
+  int b, g, tiles, j0, j1, rows;          // tiles of the request; query rows
+  int block0, blocks;                     // blocks of QB of them: the first that sees a key of the run, and behind the last
 };
 __device__ __forceinline__ int tile_of(const Run &u, int j) { return j & 1 ? u.tiles - 1 - (j >> 1) : j >> 1; }
 // The last key that the rows of a block, and of the block before, may see; up to which key all rows
@@ -234,6 +235,11 @@ key_weights_kernel(const __grid_constant__ Params p) {
       u.g = g++;
       u.j0 = from > u.g * span ? (int)((from - u.g * span + per - 1) / per) : 0;
       u.j1 = (int)min((long long)u.tiles, (upto - u.g * span + per - 1) / per);
+      // Blocks before block0 see nothing of the run and are not loaded: every block that is has a product,
+      // which the sums wait for, so that a block is loaded when the one before has been taken.  (The first
+      // tile of a run is its first early one, if it has one.)
+      const int t0 = u.j0 + (u.j0 & 1) < u.j1 ? (u.j0 + 1) >> 1 : tile_of(u, u.j0);
+      u.block0 = masked || t0 * KT <= u.q.ctx ? 0 : (t0 * KT - u.q.ctx) * G / QB;
       if (u.j0 < u.j1) return true;
     }
     return false;
@@ -268,7 +274,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
       more = next_run(at_b, at_g, next);
       if (more) first = pages_of(next, next.j0);
       const int npages = (u.q.ctx + u.q.n + kPageRows - 1) / kPageRows;
-      for (int rb = 0; rb < u.blocks && ok; ++rb) {
+      for (int rb = u.block0; rb < u.blocks && ok; ++rb) {
         const Limits lim(u, masked, G, rb * QB, QB);
         int ahead = head, batch = 0;
         for (int j = u.j0; j < u.j1 && ok; ++j) {
@@ -322,7 +328,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
       uint32_t n_tile = 0, n_q = 0, parity = 0;   // tiles and query blocks before; bit x: of group x's products
       Run u;
       while (ok && next_run(at_b, at_g, u)) {
-        for (int rb = 0; rb < u.blocks && ok; ++rb) {
+        for (int rb = u.block0; rb < u.blocks && ok; ++rb) {
           const Limits lim(u, masked, G, rb * QB, QB);
           const int rows = min(QB, u.rows - rb * QB), products = (rows + PC - 1) / PC;
           ok = mbar_wait(q_full, n_q++ & 1);
@@ -374,7 +380,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
     // (after a wait that gave up the loops go on, without work, to the barriers that all groups share)
     while (next_run(at_b, at_g, u)) {
       float *out = a.weights + ((int64_t)u.b * KVH + u.g) * a.width;
-      for (int rb = 0; rb < u.blocks; ++rb) {
+      for (int rb = u.block0; rb < u.blocks; ++rb) {
         // The block's queries, and every row's z / c = (log2(row_weight) - lse log2 e) / c as the sum of three
         // bf16 values; every product with the block before has been read.  (A row that counts for nothing
         // gets a term that no score outweighs.)

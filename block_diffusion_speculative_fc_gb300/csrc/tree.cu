@@ -26,11 +26,11 @@ __device__ __forceinline__ bool tree_range(const int *row_start, int b, int tota
   return n > 0;
 }
 
-// ancestors(i) = {i} + ancestors(parent(i)), by pointer doubling: after k rounds a
+// ancestors(i) = {i} + ancestors(parent(i)), by pointer doubling: after k steps a
 // row's mask holds its first 2^k ancestors and its pointer names the one 2^k
-// above, so that a chain of 1024 rows takes 10 rounds and a tree of depth 14
+// above, so that a chain of 1024 rows takes 10 steps and a tree of depth 14
 // four.  A mask is read while its own row may be adding to it: whatever is seen
-// of it are ancestors, and those of the round before are all there.  The depth is
+// of it are ancestors, and those of the step before are all there.  The depth is
 // the number of bits less one.
 __global__ void __launch_bounds__(1024) tree_plan_kernel(const __grid_constant__ TreePlanParams p) {
   extern __shared__ uint32_t s_mask[];          // [n][W]

@@ -116,6 +116,13 @@ def test_large(sess, lens, ctx, heads, kvh, kind):
     weigh(sess, lens, ctx, heads, kvh, 128, BF, seed=len(lens), kind=kind, decay=0.9, rows="some")
 
 
+# whole prompts: most shares of the keys are seen by the later blocks of query rows alone
+@pytest.mark.parametrize("lens,ctx,heads,kvh", [([3000], [0], 16, 2), ([1500, 1, 900], [0, 40, 129], 64, 1)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_blocks_that_see_nothing_of_a_share(sess, lens, ctx, heads, kvh, dim):
+    weigh(sess, lens, ctx, heads, kvh, dim, BF, seed=dim, decay=0.5, rows="any")
+
+
 @pytest.mark.parametrize("dtype,dim", KINDS)
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
 def test_scales(sess, dtype, dim, scale):
