@@ -15,8 +15,8 @@
 //
 // Few rows (decoding): HBM bounds it, K is read once and V not at all.  Many rows:
 // an exponential per key and row (1024 clocks of the MUFU for 128 keys by 256 rows)
-// and the product (1150 clocks) bound it.  Rows beyond 512 of a request and KV head
-// are further passes over the CTA's keys.
+// and the product (1150 clocks) bound it.  Rows of a request and KV head
+// beyond a block (128, 256 or 512) are further passes over the CTA's keys.
 //
 // Every CTA lays out the same plan from the requests' lengths: the tiles of all
 // (request, KV head)s in a row, a tile's cost its blocks of 128 query rows, and takes
@@ -27,7 +27,11 @@
 // each, over 500 to 16000 rows (558 MB) 91 us, 6.1 TB/s; the last 64 rows of two
 // prompts, 64 heads, over 8000 and 30000 rows 52 us (156 million exponentials and 40
 // GFLOP: 17 and 20 us at the units' rates; per 128 keys and 512 rows about 4600
-// clocks, of which the sums take 3100 and a product that nothing hides 1000).
+// clocks, of which the sums take 3100 and a product that nothing hides 1000).  Tried
+// for it and no faster: products of 128 columns with two places a group, so that one
+// runs while another is summed (8% more: more waits a column), an issuer a group,
+// both products of a tile one after the other (5% more), key tiles fetched to the L2
+// ahead, an arrival a warp instead of a thread, waits that poll.
 //
 // Warps: the groups that sum (of even and odd tiles; 128 or 256 threads each), the TMA
 // producer (a ring of key tiles), the MMA issuer.
@@ -54,7 +58,7 @@ template <int D, int QB> struct Cfg {
   static constexpr int TILE = KT * D * 2;
   static constexpr int PC = QB < 256 ? QB : 256, HALVES = PC / 128;
   static constexpr int PER_SM = QB == 128 ? 2 : 1;            // CTAs
-  static constexpr int NSLOT = 2 * (D == 128 ? 1 : 2);
+  static constexpr int NSLOT = (QB == 256 ? 4 : 2) * (D == 128 ? 1 : 2);
   static constexpr int GROUP = 128 * HALVES, SUM_THREADS = NG * GROUP, THREADS = SUM_THREADS + 64;
   static constexpr int OFF_RING = QB * D * 2;
   static constexpr int OFF_ONES = OFF_RING + NSLOT * TILE;    // [KT][16] bf16
@@ -587,9 +591,12 @@ template <int D, int QB> cudaError_t prepare() {
 template <int D> cudaError_t launch(const KeyWeightParams &a, cudaStream_t s) {
   // Blocks of 128 query rows and two CTAs an SM, or of 512 and one: 32 requests over 3000 to 6000 rows with
   // 4 query rows each (a token) 57 us against 72, with 128 65 against 85; with 192 112 against 97, with 256 121
-  // against 111; 2 requests with 512 over 8000 and 30000 168 against 58.
-  const bool few = (int64_t)a.rows.total_rows * (a.H / a.KVH) <= 128LL * a.rows.B;
-  return few ? launch<D, 128>(a, s) : launch<D, 512>(a, s);
+  // against 111; 2 requests with 512 over 8000 and 30000 168 against 58.  Blocks of 256, with twice the key
+  // tiles on their way, against those of 512: with 192 77 against 90, with 256 93 against 97, with 384 148 both
+  // ways, with 400 37 against 35 (4 requests).
+  const int64_t rows = (int64_t)a.rows.total_rows * (a.H / a.KVH);
+  if (rows <= 128LL * a.rows.B) return launch<D, 128>(a, s);
+  return rows <= 256LL * a.rows.B ? launch<D, 256>(a, s) : launch<D, 512>(a, s);
 }
 
 }  // namespace
@@ -600,8 +607,10 @@ cudaError_t launch_key_weights_tc(const KeyWeightParams &p, cudaStream_t s) {
 
 cudaError_t prepare_key_weights_tc() {
   cudaError_t e = prepare<64, 128>();
+  if (e == cudaSuccess) e = prepare<64, 256>();
   if (e == cudaSuccess) e = prepare<64, 512>();
   if (e == cudaSuccess) e = prepare<128, 128>();
+  if (e == cudaSuccess) e = prepare<128, 256>();
   return e == cudaSuccess ? prepare<128, 512>() : e;
 }
 

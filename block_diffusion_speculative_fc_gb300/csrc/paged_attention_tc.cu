@@ -29,8 +29,8 @@
 //
 // Measured (32 query heads on 8 KV heads of 128, graph replays): two prompts of
 // 2500 and 4096 tokens 189 us, 1000 TFLOP/s of visible products; 32 requests x 16
-// rows over a shared prefix of 8192 and 256..4096 rows of their own 142 us
-// (plan and join 19); 64 single tokens of 64 heads over a prefix of 16384 115 us;
+// rows over a shared prefix of 8192 and 256..4096 rows of their own 139 us
+// (plan and join 17); 64 single tokens of 64 heads over a prefix of 16384 115 us;
 // 128 requests x 16 rows over 64..14755 rows of their own and no prefix 604 us (3.9
 // GB of keys and values at 6.5 TB/s: HBM bounds it), with one row each 588 us; one
 // token over 1001 keys 19 us.  Where HBM does not bound it a 128-key step takes a
@@ -43,7 +43,7 @@
 // the softmax sum as a second result.  A tile that holds new rows takes the row's 128
 // bits from its mask (shifted by the tile's place); all others are as without.
 // Measured: 32 trees of 16 to 64 rows (1275 rows) over a shared prefix of 8192 and 256
-// to 4096 rows of their own 283 us, 785 TFLOP/s of visible products; one tree of 64
+// to 4096 rows of their own 284 us, 785 TFLOP/s of visible products; one tree of 64
 // rows over 2000 27 us.  What was tried for it: two threads a row (half the keys each,
 // a barrier of the stream a tile to agree on the reference) 312 us; 128 live scores
 // instead of two reads 292; the upper keys' product ahead of the lower keys' weights

@@ -116,6 +116,16 @@ def test_large(sess, lens, ctx, heads, kvh, kind):
     weigh(sess, lens, ctx, heads, kvh, 128, BF, seed=len(lens), kind=kind, decay=0.9, rows="some")
 
 
+# 129 to 256 query rows a request and KV head on average, more and fewer in some
+@pytest.mark.parametrize("lens,ctx,heads,kvh", [([64] * 5, [700, 0, 64, 1999, 5000], 32, 8),
+                                                ([33, 90, 1, 17], [100, 3000, 777, 0], 8, 2),
+                                                ([20, 2, 9], [1500, 40, 0], 128, 8)])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+def test_middling_rows(sess, lens, ctx, heads, kvh, dim, kind):
+    weigh(sess, lens, ctx, heads, kvh, dim, BF, seed=dim, decay=0.5, rows="some", kind=kind)
+
+
 # whole prompts: most shares of the keys are seen by the later blocks of query rows alone
 @pytest.mark.parametrize("lens,ctx,heads,kvh", [([3000], [0], 16, 2), ([1500, 1, 900], [0, 40, 129], 64, 1)])
 @pytest.mark.parametrize("dim", [64, 128])
