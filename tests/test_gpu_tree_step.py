@@ -263,3 +263,37 @@ def test_the_session_refuses_wrong_tensors(sess):
             with pytest.raises(ValueError):
                 call(**{**good, **b})
     sess.error()
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_pages_far_into_a_large_pool(sess, dtype):
+    """Pages behind 2^32 elements of the pool give what the same pages at its start give: append, attention,
+    weights, chosen and moved rows."""
+    rows, heads, far = [20, 1, 33], 4, 2 ** 32 // (64 * KVH * D) + 5
+    got = []
+    for shift in (0, far):
+        pb = Paged(rows, [300, 64, 5], prefix=64, kvh=KVH, dim=D, dtype=dtype, seed=3)
+        n_pages, T = pb.n_pages, pb.rows
+        if shift:
+            small = (pb.k, pb.v)
+            pb.k, pb.v = (torch.empty((far + n_pages, 64, KVH, D), dtype=dtype, device="cuda") for _ in "kv")
+            pb.k[far:], pb.v[far:] = small
+            pb.table += far
+            pb.prefix_pages += far
+        lay, q, k, v = pb.layer(heads), pb.normal(T, heads, D), pb.normal(T, KVH, D), pb.normal(T, KVH, D)
+        parent = i32([p for n in rows for p in random_parents(n, rng_of(n))])
+        mask, pos = z(T, WORDS), z(T)
+        sess.tree_plan(pb.row_start, parent, mask, pos, root=pb.kv_len)
+        sess.append_kv(lay, q, k, v, pb.row_start, pb.kv_len, pkg.rope_plan(D, 1e6), q_out=q, positions=pos)
+        out, lse = torch.zeros_like(q), z(T, heads, dt=torch.float32)
+        sess.tree_attention(lay, q, pb.row_start, pb.kv_len, out, sess.attention_workspace(lay, 3, T), mask=mask, lse=lse)
+        weights = z(3, KVH, 64 * pb.width, dt=torch.float32)
+        sess.key_weights(lay, q, pb.row_start, pb.kv_len, lse, weights, mask=mask)
+        keep, count = z(3, KVH, 40), z(3, KVH)
+        sess.choose_rows(lay, weights, pb.kv_len, i32([40, 30, 5]), keep, count, first=2, last=3)
+        sess.keep_rows(lay, keep, count, weights=weights)
+        assert sess.error() == 0
+        got.append([out, lse, weights, keep, count, pb.k[shift:].clone(), pb.v[shift:].clone()])
+        del lay, pb
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
