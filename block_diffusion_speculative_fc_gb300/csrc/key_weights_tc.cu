@@ -23,9 +23,9 @@
 // an equal share.  Within a (request, KV head) early and late tiles alternate: new
 // keys are seen by few rows, so that shares of equal cost take equal time.
 //
-// Measured (graph replays; 8 KV heads of 128, inputs beyond L2): 32 requests, a token
-// each, over 500 to 16000 rows (558 MB) 91 us, 6.1 TB/s; the last 64 rows of two
-// prompts, 64 heads, over 8000 and 30000 rows 52 us (156 million exponentials and 40
+// Measured (calls in a row; 8 KV heads of 128, inputs beyond L2): 32 requests, a token
+// each, over 500 to 16000 rows (558 MB) 90 us, 6.2 TB/s; the last 64 rows of two
+// prompts, 64 heads, over 8000 and 30000 rows 53 us (156 million exponentials and 40
 // GFLOP: 17 and 20 us at the units' rates; per 128 keys and 512 rows about 4600
 // clocks, of which the sums take 3100 and a product that nothing hides 1000).  Tried
 // for it and no faster: products of 128 columns with two places a group, so that one
