@@ -285,7 +285,9 @@ class DraftSession:
                     bonus, out_tokens, path, output_ids=None, row_weight=None):
         """Walk down the trees along the target's tokens, and commit: tokens and
         posterior int32 [rows]; out_tokens, path int32 [batch, max_path];
-        row_weight float32 [rows]: 1 for the path's rows."""
+        row_weight float32 [rows]: 1 for the path's rows.  Nothing is written
+        for a request without rows or a refused one: commit_len and row_weight
+        that are used again from step to step are set to 0 before the call."""
         dev, i32 = self.device, torch.int32
         batch, rows = row_start.shape[0] - 1, parent.shape[0]
         check(row_start, "row_start", i32, dev, (batch + 1,))

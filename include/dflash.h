@@ -743,7 +743,10 @@ int dflash_tree_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t b
  * At most 1024 rows a request; more, or a parent out of its range (a first row with
  * one), set DFLASH_DERR_TREE.  A committed token outside the vocabulary sets
  * DFLASH_DERR_TOKEN_RANGE, a commit past out_stride DFLASH_DERR_OUTPUT_ROW.  Nothing is
- * written for such a request, nor for one without rows.
+ * written for such a request, nor for one without rows: commit_len, path and row_weight
+ * keep what they held.  Where buffers are used again from step to step, commit_len and
+ * row_weight are set to 0 before the call, so that dflash_keep_rows, the caller's kv_len
+ * and dflash_key_weights take nothing for such a request from an earlier step.
  */
 int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_rows,
                               const int32_t *row_start, const int32_t *parent,
@@ -800,8 +803,8 @@ int dflash_key_weights(dflash_handle *h, const dflash_layer_kv *kv, int32_t batc
  *             lies behind the count is left as it is
  *   count     device int32 [batch, n_kv_heads]
  * kv_len below prefix_len or n above `width` sets DFLASH_DERR_KV_CAPACITY, a keep out of
- * range DFLASH_DERR_ROW_LIST; the request is skipped.  Of the layer the shape and prefix_len
- * are read.  batch <= 1024.
+ * range DFLASH_DERR_ROW_LIST; the request is skipped (its rows and count keep what they
+ * held).  Of the layer the shape and prefix_len are read.  batch <= 1024.
  */
 int dflash_choose_rows(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
                        const int32_t *kv_len, const float *weights, int32_t width,
