@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float scale) {
   return r;
 }
 
+// The wait for tcgen05.ld in flight, tied to the N registers that they fill: nothing computed from
+// those is scheduled before it.  (The empty statements are no instructions; statements with volatile
+// stay in order.)
+template <int N> __device__ __forceinline__ void tmem_ld_wait(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // Programmatic dependent launch.  Every kernel is launched so that it may be
 // scheduled before its predecessor in the stream has exited.  A kernel waits
 // for its predecessor (griddepcontrol.wait) right before it first reads what

@@ -528,7 +528,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
             if (cols <= 16 && half == 0) {
               uint32_t v[16];
               tmem_ld16(t_s, v);
-              tmem_ld_wait();
+              tmem_ld_wait<16>(v);
               release();
               sum += piece(v, pr * PC, std::integral_constant<int, 16>());
             } else {
@@ -536,7 +536,7 @@ key_weights_kernel(const __grid_constant__ Params p) {
               for (int c = from; c < upto; c += 32) {
                 uint32_t v[32];
                 tmem_ld32(t_s + c, v);
-                tmem_ld_wait32(v);
+                tmem_ld_wait<32>(v);
                 if (c + 32 >= upto) release();
                 sum += piece(v, pr * PC + c, std::integral_constant<int, 32>());
               }

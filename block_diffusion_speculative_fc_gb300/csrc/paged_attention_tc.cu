@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             auto load = [&](int half) {
               tmem_ld32(t_s + half * 64, sv);
               tmem_ld32(t_s + half * 64 + 32, sv + 32);
-              tmem_ld_wait();
+              tmem_ld_wait<64>(sv);
             };
             // key i of a half
             auto seen = [&](int half, int i) {
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             for (int i = 0; i < D; i += 32) {
               uint32_t o[32];
               tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
-              tmem_ld_wait();
+              tmem_ld_wait<32>(o);
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
               tmem_st32(tmem + lanes + 256 + x * 128 + i, o);
@@ -1022,13 +1022,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
             tmem_ld32(tmem + lanes + 256 + x * 128 + i, o);
-            tmem_ld_wait();
+            tmem_ld_wait<32>(o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(a0 != 0.f ? __uint_as_float(o[j]) * a0 : 0.f);
             if (both) {
               uint32_t q[32];
               tmem_ld32(tmem + lanes + 256 + 128 + i, q);
-              tmem_ld_wait();
+              tmem_ld_wait<32>(q);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 o[j] = __float_as_uint(__uint_as_float(o[j]) + (a1 != 0.f ? __uint_as_float(q[j]) * a1 : 0.f));
