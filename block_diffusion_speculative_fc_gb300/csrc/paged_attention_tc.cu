@@ -128,7 +128,7 @@ struct Params {
   float *part_o, *part_lse;               // [partial rows][D], [partial rows]
   int sms;
   float scale_log2;                       // |scale| log2 e
-  int negative;                           // scale < 0: S changes its sign
+  int negative;                           // scale < 0: the product takes -Q
 };
 
 // Places of V(t) and K(t) in an item's load order: the first `ahead` K tiles,
@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
       // stream that waits for that S.
       const uint32_t x = warp - 9;
       if (lane == 0) {
-        constexpr uint32_t ID_S = idesc(128, KT, false), ID_O = idesc(128, D, true);
+        constexpr uint32_t ID_O = idesc(128, D, true);
+        const uint32_t id_s = idesc(128, KT, false) | (p.negative ? NEGATE_A : 0u);
         const uint64_t k_desc = desc_k(su32(ring)), v_desc = desc_mn(su32(ring), KT * 128);
         const uint32_t full_at = su32(full), p_at = su32(&p_full[x]);
         const uint32_t t_s = tmem + x * KT, t_o = tmem + 256 + x * 128;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
               umma_ss(t_s, q_desc + (i >> 2) * ((128 * 128) >> 4) + 2 * (i & 3),
-                      kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3), ID_S, i ? 1u : 0u);
+                      kd + (i >> 2) * ((KT * 128) >> 4) + 2 * (i & 3), id_s, i ? 1u : 0u);
             umma_commit(&s_full[x]);
           };
           wait(su32(q_full), k & 1);
@@ -827,7 +828,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
     const int x = warp >> 2, row = threadIdx.x & 127;          // stream, row of its tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + x * KT;
-    const float sl = p.negative ? -p.scale_log2 : p.scale_log2;
+    const float sl = p.scale_log2;
     const bool wide = (((uintptr_t)p.a.out | (uint64_t)(p.a.out_stride * 2)) & 31) == 0;   // 32-byte rows
     // every wait is one for the warp, so that its lanes stay together
     auto wait = [&](uint64_t *b, uint32_t parity) {
@@ -877,9 +878,11 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
           const int vis = lim - t * KT;                        // visible keys of this tile
           uint32_t bits[KT / 32];                              // of them, where the new rows are among them
           // Keys 0..63 for their maximum, then keys 64..127 and their weights, then keys 0..63 again: reading TMEM
-          // twice is cheaper than 128 live registers.  ALL: every key is seen and the scale is not negative,
-          // by far most tiles, in code of its own and in loops over the halves, so that it fits the instruction
-          // cache (one code for all tiles, with a selection a weight, took 216 us for the prompts instead of 188).
+          // twice is cheaper than 128 live registers.  ALL: every key is seen, by far most tiles, in code of its
+          // own and in loops over the halves, so that it fits the instruction cache (one code for all tiles,
+          // with a selection a weight, took 216 us for the prompts instead of 188).  A negative scale is in the
+          // product's operand, which costs nothing (with the sign in the exponents its tiles had to take the
+          // code with selections: prompts 251 us).
           auto tile = [&](auto every) {
             constexpr bool ALL = decltype(every)::value;
             uint32_t sv[KT / 2];
@@ -943,7 +946,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attention_kernel(const __gri
             return alpha;
           };
           float alpha;
-          if (__all_sync(0xffffffffu, vis >= KT) && !p.negative) {
+          if (__all_sync(0xffffffffu, vis >= KT)) {
             alpha = tile(std::true_type());
           } else {
             if (TREE) {

@@ -165,7 +165,8 @@ __device__ __forceinline__ uint64_t desc_plain(uint32_t saddr, uint32_t lbo, uin
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
          ((uint64_t)1 << 46);
 }
-// kind::f16: bf16 A and B, fp32 D; b_mn: B is MN-major
+// kind::f16: bf16 A and B, fp32 D; b_mn: B is MN-major.  With NEGATE_A the product is (-A) B.
+constexpr uint32_t NEGATE_A = 1u << 13;
 constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
