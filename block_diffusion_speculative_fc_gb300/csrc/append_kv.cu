@@ -74,8 +74,9 @@ template <> struct Chunk<float> {
 // any other halves
 enum Rotation { kInterleaved, kWholeHalves, kLowHalves, kPartHalves };
 
-// L lanes per head; D = 2 L E.
-template <typename T, int L, int ROT>
+// L lanes per head; D = 2 L E.  AT: rotary positions are given.  (A branch instead of the parameter costs the call
+// without them a twentieth: 2048 rows 16.5 -> 17.4 us.)
+template <typename T, int L, int ROT, bool AT>
 __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ AppendParams p) {
   constexpr int E = Chunk<T>::E, D = 2 * L * E;
   __shared__ float2 s_cs[64];
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
   }
   const int pos = (int)pos64, own = pos - r.prefix_len;
   const int page = r.page_table[(int64_t)b * r.pages_per_req + own / kPageRows];
-  const int half = p.rot >> 1, at = p.positions ? p.positions[t] : pos;
+  const int half = p.rot >> 1, at = AT ? p.positions[t] : pos;
   for (int i = tid; i < half; i += nt) {
     const unsigned long long turn = (unsigned long long)at * p.turns[i];
     float sn, cs;   // of pi * x, x in [-1, 1): half turns
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int L>
+template <typename T, int L, bool AT>
 cudaError_t launch(const AppendParams &p, cudaStream_t s) {
   constexpr int E = Chunk<T>::E, D = 2 * L * E;
   const int units = (p.H + 2 * p.KVH) * L;
@@ -247,11 +248,14 @@ cudaError_t launch(const AppendParams &p, cudaStream_t s) {
   int nt = (units + passes * kU - 1) / (passes * kU);
   nt = (nt + 31) / 32 * 32;
   const dim3 grid(p.rows.total_rows), block(nt);
-  if (p.inter || p.rot == 0) return launch_pdl(append_kv_kernel<T, L, kInterleaved>, grid, block, 0, s, p);
-  if (p.rot == D) return launch_pdl(append_kv_kernel<T, L, kWholeHalves>, grid, block, 0, s, p);
+  if (p.inter || p.rot == 0) return launch_pdl(append_kv_kernel<T, L, kInterleaved, AT>, grid, block, 0, s, p);
+  if (p.rot == D) return launch_pdl(append_kv_kernel<T, L, kWholeHalves, AT>, grid, block, 0, s, p);
   if (p.rot <= D / 2 && p.rot / 2 % E == 0)
-    return launch_pdl(append_kv_kernel<T, L, kLowHalves>, grid, block, 0, s, p);
-  return launch_pdl(append_kv_kernel<T, L, kPartHalves>, grid, block, sizeof(float) * 2 * E * nt, s, p);
+    return launch_pdl(append_kv_kernel<T, L, kLowHalves, AT>, grid, block, 0, s, p);
+  return launch_pdl(append_kv_kernel<T, L, kPartHalves, AT>, grid, block, sizeof(float) * 2 * E * nt, s, p);
+}
+template <typename T, int L> cudaError_t launch(const AppendParams &p, cudaStream_t s) {
+  return p.positions ? launch<T, L, true>(p, s) : launch<T, L, false>(p, s);
 }
 
 }  // namespace
