@@ -717,7 +717,8 @@ int dflash_append_kv_at(dflash_handle *h, const dflash_layer_kv *kv, int32_t bat
  * A request of more than 32 mask_words rows sets DFLASH_DERR_TREE and is skipped.
  * Everything else, the workspace (of dflash_paged_attention_workspace_size) among
  * it, as for dflash_paged_attention; lse has the error of its scores, about (D + 8)
- * 2^-24 of the largest scale sum_d |q_d k_d|, and that of its own rounding.
+ * 2^-24 of the largest scale sum_d |q_d k_d|; about 2^-18 at most for the exponentials,
+ * their float32 sum and its log; and 2^-22 |lse| for its own roundings.
  */
 int dflash_tree_attention(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
                           int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
@@ -782,8 +783,10 @@ int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_row
  *              are left as they are.  A request with more than `width` own rows sets
  *              DFLASH_DERR_KV_CAPACITY and is skipped
  * A row whose lse is not finite, or whose row_weight is 0, counts for nothing.  Sums
- * are in float32 and in the same order in every run; a term has the relative error of
- * its exponent: (D + 8) 2^-24 of the largest scale sum_d |q_d k_d|, and 2^-23 |lse|.
+ * are in float32 and in the same order in every run, n terms to n 2^-24 of the sum at
+ * most.  A term has the relative error of its exponent, (D + 8) 2^-24 of the largest
+ * scale sum_d |q_d k_d| and 2^-21 of |lse| and of |ln row_weight|, and 2^-21 for the
+ * exponential (below 2^-126 it may be 0).
  */
 int dflash_key_weights(dflash_handle *h, const dflash_layer_kv *kv, int32_t batch,
                        int32_t total_rows, const int32_t *row_start, const int32_t *kv_len,
