@@ -323,7 +323,8 @@ class DraftSession:
                     decay=1.0, scale=None):
         """weights float32 [batch, KVH, width] <- decay * weights + the attention
         weight of q's rows (lse of tree_attention, mask as there) on every own
-        cache row; row_weight float32 [rows]: a factor a row."""
+        cache row; row_weight float32 [rows]: a factor a row, finite and not
+        below 0 (any other counts as 0, as does a row whose lse is not finite)."""
         batch = self._ragged(layer, row_start, kv_len)
         dt, dev, D, rows = layer.dtype, layer.device, layer.head_dim, q.shape[0]
         qs = rows_of(q, "q", layer.n_heads, D, dt, dev)

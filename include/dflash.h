@@ -776,13 +776,14 @@ int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_row
  * kv_len[b] - prefix_len on) begin at 0, and with decay 0 nothing is read of the old.
  *   row_start, kv_len, mask, mask_words, q, scale: as for dflash_tree_attention,
  *              which gives lse; scale 0 or of magnitude 2^-100 to 2^100
- *   row_weight optional device float32 [total_rows] (NULL: 1), such as the accepted
- *              rows' of dflash_accept_commit_tree
+ *   row_weight optional device float32 [total_rows] (NULL: 1), finite and not below 0,
+ *              such as the accepted rows' of dflash_accept_commit_tree
  *   decay      0 to 1
  *   weights    device float32 [batch, n_kv_heads, width]; rows past a request's last
  *              are left as they are.  A request with more than `width` own rows sets
  *              DFLASH_DERR_KV_CAPACITY and is skipped
- * A row whose lse is not finite, or whose row_weight is 0, counts for nothing.  Sums
+ * A row whose lse is not finite, or whose row_weight is 0, below 0, infinite or NaN,
+ * counts for nothing, and nothing is flagged.  Sums
  * are in float32 and in the same order in every run, n terms to n 2^-24 of the sum at
  * most.  A term has the relative error of its exponent, (D + 8) 2^-24 of the largest
  * scale sum_d |q_d k_d| and 2^-21 of |lse| and of |ln row_weight|, and 2^-21 for the

@@ -49,3 +49,21 @@ def test_error_of_a_single_term(sess, dtype, dim, scale, weighted):
     bound = 2.0 ** -21 * (1 + lse.double().abs() + ln.abs())
     for key in range(3):
         assert float(((got[:, :, key].double() / want - 1).abs() / bound).max()) <= 1
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("heads,kvh,rows", [(4, 1, 6), (16, 2, 40), (64, 1, 9)])
+def test_factors_that_count_for_nothing(sess, dtype, dim, heads, kvh, rows):
+    """Factors below zero, infinite ones and NaN are as zero: the same weights, bit for bit."""
+    pb = Paged([rows, 3], [200, 64], kvh=kvh, dim=dim, dtype=dtype, seed=rows)
+    q, lse = pb.normal(pb.rows, heads, dim), f32(pb.rows, heads, g=pb.g, lo=3, hi=6)
+    rw = f32(pb.rows, g=pb.g, lo=0.1, hi=2)
+    inf, none = float("inf"), [0, 2, 3, 5, rows + 1]
+    got = []
+    for what in ([0.0] * 5, [-0.0, -1e-30, -3.0, inf, float("nan")], [-inf, -inf, inf, -0.5, -float("nan")]):
+        rw[none] = torch.tensor(what, device="cuda")
+        w = torch.ones((2, kvh, 64 * pb.width), device="cuda")
+        sess.key_weights(pb.layer(heads), q, pb.row_start, pb.kv_len, lse, w, row_weight=rw, decay=0.5)
+        got.append(w)
+    assert sess.error() == 0
+    assert bool(got[0].isfinite().all()) and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
