@@ -780,7 +780,8 @@ int dflash_accept_commit_tree(dflash_handle *h, int32_t batch, int32_t total_row
  *              such as the accepted rows' of dflash_accept_commit_tree
  *   decay      0 to 1
  *   weights    device float32 [batch, n_kv_heads, width]; rows past a request's last
- *              are left as they are.  A request with more than `width` own rows sets
+ *              are left as they are, and those of a request without new rows are not
+ *              decayed.  A request with more than `width` own rows sets
  *              DFLASH_DERR_KV_CAPACITY and is skipped
  * A row whose lse is not finite, or whose row_weight is 0, below 0, infinite or NaN,
  * counts for nothing, and nothing is flagged.  Sums

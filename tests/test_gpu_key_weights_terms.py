@@ -67,3 +67,14 @@ def test_factors_that_count_for_nothing(sess, dtype, dim, heads, kvh, rows):
         got.append(w)
     assert sess.error() == 0
     assert bool(got[0].isfinite().all()) and torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_request_without_rows_keeps_its_weights(sess, dtype):
+    pb = Paged([2, 0, 1], [30, 64, 7], kvh=1, dim=64, dtype=dtype, seed=3)
+    q, lse = pb.normal(3, 2, 64), torch.zeros((3, 2), device="cuda")
+    w = torch.rand((3, 1, 80), generator=pb.g, device="cuda")
+    old = w.clone()
+    sess.key_weights(pb.layer(2), q, pb.row_start, pb.kv_len, lse, w, decay=0.5)
+    assert sess.error() == 0
+    assert torch.equal(w[1], old[1]) and not bool((w[0, 0, :30] == old[0, 0, :30]).any())
