@@ -467,8 +467,10 @@ int dflash_select_tokens_noalloc(dflash_handle *h, int32_t rows, const void *hid
  * dflash_append_kv flags such rows and skips them; the outputs that
  * dflash_paged_attention writes for them are unspecified, and where the
  * ranges hold more than total_rows rows in all it flags that
- * (DFLASH_DERR_ROW_RANGE) and writes nothing.  Arrays of 32-bit values are
- * 4-byte aligned.
+ * (DFLASH_DERR_ROW_RANGE) and writes nothing.  What the tree calls and
+ * dflash_key_weights write for such rows is unspecified too (ranges that share
+ * rows have a decreasing pair between them, which is flagged).  Arrays of
+ * 32-bit values are 4-byte aligned.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -670,6 +672,9 @@ int dflash_sample_tokens(dflash_handle *h, int32_t rows, int32_t vocab, const vo
  *   dflash_tree_attention      each layer's attention under the mask
  *   dflash_accept_commit_tree  the walk down the tree along the target's tokens
  *   dflash_keep_rows           each layer's accepted rows, moved together
+ * dflash_inject_context takes consecutive feature rows, and a path's lie apart: the
+ * caller gathers rows row_start[b] + path[b][i], i < commit_len[b], of the target's
+ * features before it extends the draft's cache by them.
  * Where the target's tokens are drawn for every row (dflash_sample_tokens on the
  * rows' logits), the walk commits exactly the target's distribution: each
  * committed token is the draw of the row before it, whatever was proposed.
